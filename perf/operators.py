@@ -1,0 +1,486 @@
+"""The 4-bit microscaled (MXFP4) Linear and the routing around its experts, as cases to measure.
+
+Operators: the cast to MXFP4 (tiles of 32 along a row, along a column, or both) and its read-back; the product of
+two MXFP4 operands (a token, a batch, a training step); the experts' products over rows grouped by a router's choices,
+with the dispatch plan they need; the router's balance loss with its gradient.
+
+Layouts (those of the package): codes are two to a byte, the element with the even index in the low four bits, in rows
+padded with zero codes to a multiple of 256 elements; scales are E8M0 bytes [chunk of 256 elements][row][8].
+"""
+
+import math
+
+import torch
+
+own = False
+
+_GRID = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+
+def listed():
+    return [
+        # the activation of one generated token on its way into a 4-bit Linear
+        {"name": "cast-token", "op": "cast", "rows": 1, "cols": 7168, "both": False, "type": "bf16"},
+        # a training step's activations, cast along tokens and channels in one go (forward and weight gradient)
+        {"name": "cast-both", "op": "cast", "rows": 4096, "cols": 7168, "both": True, "type": "bf16"},
+        # one token against a resident 4-bit weight
+        {"name": "linear-token", "op": "linear", "m": 1, "n": 2048, "k": 7168, "type": "bf16"},
+        # a small serving batch against a wide weight: the weight's bytes are the cost
+        {"name": "linear-batch", "op": "linear", "m": 48, "n": 18432, "k": 7168, "type": "bf16"},
+        # odd sizes all round, half-precision activations
+        {"name": "linear-ragged", "op": "linear", "m": 1003, "n": 1001, "k": 1057, "type": "fp16"},
+        # a prompt through a large Linear
+        {"name": "linear-large", "op": "linear", "m": 16384, "n": 18432, "k": 7168, "type": "bf16"},
+        # one Linear's training step: output, gradient of the input and of the weight
+        {"name": "step-dense", "op": "step", "m": 4096, "n": 2048, "k": 7168, "type": "bf16"},
+        # 8 of 256 experts on this GPU, 256 generated tokens
+        {"name": "experts-decode", "op": "experts", "tokens": 256, "topk": 8, "experts": 256, "local": 8, "n": 2048,
+         "k": 7168, "zipf": 1.1},
+        # the same experts over a long batch of tokens
+        {"name": "experts-prompt", "op": "experts", "tokens": 16384, "topk": 8, "experts": 256, "local": 8, "n": 2048,
+         "k": 7168, "zipf": 1.1},
+        # a layer of experts in training: outputs, gradients of rows and weights
+        {"name": "experts-step", "op": "experts_step", "tokens": 4096, "topk": 4, "experts": 32, "local": 32, "n": 1024,
+         "k": 2048, "zipf": 0.5},
+        # a short packed batch with padding behind its sequences
+        {"name": "balance-short", "op": "balance", "tokens": 333, "experts": 64, "topk": 6, "sequences": 3,
+         "score": "sigmoid", "type": "bf16"},
+        # a training batch of sequences
+        {"name": "balance-batch", "op": "balance", "tokens": 16384, "experts": 256, "topk": 8, "sequences": 4,
+         "score": "softmax", "type": "fp32"},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["cast", "linear", "linear", "step", "experts", "experts_step", "balance"])
+    kind = rng.choice(["bf16", "bf16", "fp16", "fp32"])
+    if op == "cast":
+        return {"op": op, "rows": _log(rng, 1, 4096), "cols": _log(rng, 32, 7168), "both": rng.random() < 0.5, "type": kind}
+    if op == "linear":
+        return {"op": op, "m": _log(rng, 1, 8192), "n": _log(rng, 64, 18432), "k": _log(rng, 32, 7168), "type": kind}
+    if op == "step":
+        return {"op": op, "m": _log(rng, 64, 4096), "n": _log(rng, 64, 4096), "k": _log(rng, 64, 7168), "type": kind}
+    if op == "experts":
+        local = rng.choice([4, 8, 16, 32])
+        return {"op": op, "tokens": _log(rng, 1, 8192), "topk": rng.randint(1, 8), "experts": local * rng.choice([1, 2, 8]),
+                "local": local, "n": _log(rng, 64, 2048), "k": _log(rng, 64, 4096), "zipf": rng.choice([0.0, 0.5, 1.1])}
+    if op == "experts_step":
+        local = rng.choice([4, 8, 16, 32])
+        return {"op": op, "tokens": _log(rng, 16, 4096), "topk": rng.randint(1, 4), "experts": local * rng.choice([1, 2]),
+                "local": local, "n": _log(rng, 64, 1024), "k": _log(rng, 64, 2048), "zipf": rng.choice([0.0, 0.5, 1.1])}
+    experts = rng.choice([8, 16, 60, 64, 128, 160, 256])
+    return {"op": op, "tokens": _log(rng, 8, 16384), "experts": experts, "topk": rng.randint(1, 8),
+            "sequences": rng.randint(1, 8), "score": rng.choice(["softmax", "sigmoid"]), "type": rng.choice(["bf16", "fp32"])}
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+
+_TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def _normal(gen, shape, std, dtype, outliers=0.0):
+    x = torch.randn(shape, generator=gen, device="cuda")
+    if outliers:
+        x = torch.where(torch.rand(shape, generator=gen, device="cuda") < outliers, x * 50, x)
+    return (x * std).to(dtype)
+
+
+def _choices(gen, tokens, topk, experts, zipf):
+    """Distinct experts of each token, drawn with probabilities (i + 1)^-zipf."""
+    logp = -zipf * torch.log(torch.arange(1, experts + 1, device="cuda", dtype=torch.float32))
+    u = torch.rand((tokens, experts), generator=gen, device="cuda").clamp_(1e-20, 1.0 - 1e-7)
+    return torch.topk(logp - torch.log(-torch.log(u)), min(topk, experts), dim=1).indices.to(torch.int32)
+
+
+def _pack(v, e):
+    """Values on the E2M1 grid (already divided by their tiles' scales) [..., rows, k] and exponents [..., rows, k / 32]
+    in the package's layout: codes [..., rows, k padded to 256, / 2] and scales [..., k padded / 256, rows, 8]."""
+    k = v.shape[-1]
+    pad = -k % 256
+    a = v.abs()
+    code = torch.where(a < 2, a * 2, torch.where(a < 4, a + 2, a / 2 + 4)).to(torch.uint8)
+    code = torch.where((v < 0) | ((v == 0) & torch.signbit(v)), code | 8, code)
+    code = torch.nn.functional.pad(code, (0, pad))
+    q = code[..., 0::2] | (code[..., 1::2] << 4)
+    b = torch.nn.functional.pad((e + 127).to(torch.uint8), (0, (k + pad) // 32 - e.shape[-1]))
+    b = b.reshape(*b.shape[:-1], -1, 8).transpose(-2, -3).contiguous()
+    return q.contiguous(), b
+
+
+def _weight(gen, shape):
+    """A bf16 weight [..., n, k] cast to MXFP4 both ways: (codes, scales) along k and, transposed, along n."""
+    w = _normal(gen, shape, 0.02, torch.bfloat16)
+    out = []
+    for t in (w, w.transpose(-1, -2)):
+        v, e = _cast(t)
+        out += list(_pack(v, e))
+    return out
+
+
+def _seq_off(tokens, sequences, real):
+    cut = [round(real * (i / sequences) ** 1.3) for i in range(sequences + 1)]
+    return torch.tensor(cut, dtype=torch.int32, device="cuda")
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    st = {"case": case}
+    op = case["op"]
+    if op == "cast":
+        st["x"] = _normal(gen, (case["rows"], case["cols"]), 1.0, _TYPES[case["type"]], 1e-3)
+    elif op in ("linear", "step"):
+        m, n, k = case["m"], case["n"], case["k"]
+        st["x"] = _normal(gen, (m, k), 1.0, _TYPES[case["type"]], 1e-3)
+        if op == "linear":
+            st["w"], st["ws"] = _weight(gen, (n, k))[:2]
+        else:
+            st["w"], st["ws"], st["wt"], st["wts"] = _weight(gen, (n, k))
+            st["dy"] = _normal(gen, (m, n), 1e-3, torch.bfloat16)
+    elif op in ("experts", "experts_step"):
+        g, n, k, pad = case["local"], case["n"], case["k"], 256 if op == "experts_step" else 1
+        st["idx"] = _choices(gen, case["tokens"], case["topk"], case["experts"], case["zipf"])
+        # choices of experts that live elsewhere stay in the table; this GPU's are 0 .. local - 1
+        st["x"] = _normal(gen, (case["tokens"], k), 1.0, torch.bfloat16, 1e-3)
+        cap = st["idx"].numel() + g * (pad - 1)
+        cap += -cap % pad
+        st["w"], st["ws"], st["wt"], st["wts"] = _weight(gen, (g, n, k))
+        st["y"] = torch.zeros((cap, n), dtype=torch.bfloat16, device="cuda")
+        if op == "experts_step":
+            st["dy"] = _normal(gen, (case["tokens"], n), 1e-3, torch.bfloat16)
+            st["dx"] = torch.zeros((cap, k), dtype=torch.bfloat16, device="cuda")
+        else:
+            del st["wt"], st["wts"]
+    else:
+        tokens, experts, s = case["tokens"], case["experts"], case["sequences"]
+        real = tokens - (tokens // 8 if s > 1 else 0)     # padding behind the last sequence
+        st["logits"] = _normal(gen, (tokens, experts), 1.0, _TYPES[case["type"]])
+        st["idx"] = torch.topk(st["logits"].float() + 0.3 * torch.randn((tokens, experts), generator=gen, device="cuda"),
+                               min(case["topk"], experts), dim=1).indices.to(torch.int32)
+        st["idx"][torch.rand(tokens, generator=gen, device="cuda") < 0.02] = -1     # tokens masked inside a sequence
+        st["seq_off"] = _seq_off(tokens, s, real)
+        st["dloss"] = torch.rand((), generator=gen, device="cuda") + 0.5
+    return st
+
+
+# ---------------------------------------------------------------------------
+# plain forms
+# ---------------------------------------------------------------------------
+
+def _tiles(x):
+    """x [..., k] as float32 tiles [..., ceil(k / 32), 32], the last filled up with zeros."""
+    x = x.to(torch.float32)
+    x = torch.nn.functional.pad(x, (0, -x.shape[-1] % 32))
+    return x.reshape(*x.shape[:-1], -1, 32)
+
+
+def _cast(x):
+    """MXFP4 of x along its last axis: values divided by their tile's scale, on the E2M1 grid, and exponents."""
+    t = _tiles(x)
+    amax = t.abs().amax(-1)
+    e = torch.frexp(amax)[1] - 3                      # floor(log2(amax)) - 2
+    e = torch.where(amax == 0, -127, e).clamp(-127, 127)
+    y = torch.ldexp(t, -e.unsqueeze(-1))
+    a = y.abs()
+    step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
+    v = torch.copysign((torch.round(a / step) * step).clamp(max=6.0), y)
+    return v.flatten(-2)[..., : x.shape[-1]], e
+
+
+def _values(x):
+    """What the MXFP4 codes of x along its last axis stand for, float32."""
+    v, e = _cast(x)
+    return torch.ldexp(v, e.repeat_interleave(32, -1)[..., : v.shape[-1]])
+
+
+def _decode(q, s, k):
+    """Float32 values of packed codes and scales, [..., rows, k]."""
+    grid = torch.tensor(_GRID + tuple(-v for v in _GRID), device=q.device)
+    v = torch.stack((grid[(q & 15).int()], grid[(q >> 4).int()]), -1).flatten(-2)
+    e = s.transpose(-2, -3).flatten(-2).to(torch.int32) - 127
+    return torch.ldexp(v, e.repeat_interleave(32, -1))[..., :k]
+
+
+def _plan(idx, groups, pad):
+    """Counts, offsets (each group padded to `pad` rows), source token of each dispatched row (-1: none) and the row of
+    each choice (-1: another GPU's expert), rows of a group in the order of tokens."""
+    flat = idx.flatten().long()
+    mine = (flat >= 0) & (flat < groups)
+    key = torch.where(mine, flat, groups)
+    counts = torch.bincount(key, minlength=groups + 1)[:groups]
+    off = torch.nn.functional.pad(((counts + pad - 1) // pad * pad).cumsum(0), (1, 0))
+    order = torch.argsort(key, stable=True)
+    first = torch.nn.functional.pad(counts.cumsum(0), (1, 0))
+    rank = torch.arange(flat.numel(), device=idx.device)
+    sorted_key = key[order]
+    row = off[sorted_key] + rank - first[sorted_key]
+    row = torch.where(sorted_key < groups, row, -1)
+    pos = torch.empty_like(flat)
+    pos[order] = row
+    cap = flat.numel() + groups * (pad - 1)
+    src = torch.full((cap + -cap % pad + 1,), -1, dtype=torch.int64, device=idx.device)
+    src[row] = order // idx.shape[1]                  # row -1: the spare last entry
+    return (counts.to(torch.int32), off.to(torch.int32), src[:-1].to(torch.int32), pos.reshape(idx.shape).to(torch.int32))
+
+
+def _gather(x, src):
+    return torch.where((src >= 0).unsqueeze(1), x[src.clamp(min=0).long()], torch.zeros((), dtype=x.dtype, device=x.device))
+
+
+def _grouped(off, a, w, out_rows):
+    """Rows off[e] .. off[e + 1] of a against w[e], the rows behind the last group zero."""
+    cut = off.tolist()
+    y = torch.zeros((out_rows, w.shape[1]), dtype=torch.float32, device=a.device)
+    for e in range(w.shape[0]):
+        torch.matmul(a[cut[e]:cut[e + 1]], w[e].t(), out=y[cut[e]:cut[e + 1]])
+    return y
+
+
+def _grouped_k(off, a, b):
+    """a[:, off[e] .. off[e + 1]] against the same columns of b, for each group e."""
+    cut = off.tolist()
+    return torch.stack([a[:, i:j] @ b[:, i:j].t() for i, j in zip(cut, cut[1:])])
+
+
+def _run_plain(st):
+    case, op = st["case"], st["case"]["op"]
+    if op == "cast":
+        out = [_values(st["x"]).to(torch.bfloat16)]
+        if case["both"]:
+            out.append(_values(st["x"].t()).to(torch.bfloat16))
+        return out
+    if op == "linear":
+        return (_values(st["x"]) @ _decode(st["w"], st["ws"], case["k"]).t()).to(torch.bfloat16)
+    if op == "step":
+        y = _values(st["x"]) @ _decode(st["w"], st["ws"], case["k"]).t()
+        dx = _values(st["dy"]) @ _decode(st["wt"], st["wts"], case["n"]).t()
+        dw = _values(st["dy"].t()) @ _values(st["x"].t()).t()
+        return y.to(torch.bfloat16), dx.to(torch.bfloat16), dw
+    if op in ("experts", "experts_step"):
+        counts, off, src, pos = _plan(st["idx"], case["local"], 256 if op == "experts_step" else 1)
+        x = _gather(st["x"], src)
+        y = _grouped(off, _values(x), _decode(st["w"], st["ws"], case["k"]), len(src)).to(torch.bfloat16)
+        if op == "experts":
+            return counts, off, pos, y
+        dy = _gather(st["dy"], src)
+        dx = _grouped(off, _values(dy), _decode(st["wt"], st["wts"], case["n"]), len(src)).to(torch.bfloat16)
+        return counts, off, pos, y, dx, _grouped_k(off, _values(dy.t()), _values(x.t()))
+    logits, idx, off = st["logits"].float(), st["idx"], st["seq_off"]
+    tokens, experts = logits.shape
+    s, k = off.numel() - 1, idx.shape[1]
+    seq = torch.searchsorted(off[1:].contiguous(), torch.arange(tokens, device=off.device, dtype=torch.int32), right=True)
+    real = (idx >= 0).any(1) & (seq < s)
+    seq = torch.where(real, seq, s)
+    n = torch.bincount(seq, minlength=s + 1)[:s].float()
+    key = torch.where((idx >= 0) & real[:, None], seq[:, None] * experts + idx, s * experts)
+    counts = torch.bincount(key.flatten(), minlength=s * experts + 1)[: s * experts].reshape(s, experts)
+    if case["score"] == "softmax":
+        p = torch.exp(logits - logits.amax(1, keepdim=True))
+    else:
+        p = 1 / (1 + torch.exp(-logits))
+        open_ = 1 - p
+    p = p / p.sum(1, keepdim=True)
+    mean = torch.zeros((s + 1, experts), device=off.device).index_add_(0, seq, p)[:s] / n.clamp(min=1)[:, None]
+    f = counts * (experts / (k * n.clamp(min=1)))[:, None]
+    coef = 1e-2 / s
+    loss = coef * (f * mean).sum()
+    dp = torch.cat((f * (st["dloss"] * coef / n.clamp(min=1))[:, None], torch.zeros((1, experts), device=off.device)))[seq]
+    d = p * (dp - (p * dp).sum(1, keepdim=True))
+    if case["score"] != "softmax":
+        d = d * open_
+    return loss, counts.to(torch.int32), d.to(st["logits"].dtype)
+
+
+# ---------------------------------------------------------------------------
+# the package's calls
+# ---------------------------------------------------------------------------
+
+def _run_own(st):
+    import fp8_fine_grained_fp8bq_amd as fb
+    case, op = st["case"], st["case"]["op"]
+    if op == "cast":
+        q, s, qt, sct = fb.quant_mxfp4_1x32(st["x"], colwise=case["both"])
+        out = [fb.dequant_mxfp4_1x32(q, s, case["cols"])]
+        if case["both"]:
+            out.append(fb.dequant_mxfp4_1x32(qt, sct, case["rows"]))
+        return out
+    if op == "linear":
+        q, s, _, _ = fb.quant_mxfp4_1x32(st["x"])
+        return fb.gemm_mxfp4(q, s, st["w"], st["ws"])
+    if op == "step":
+        xq, xs, xqt, xst = fb.quant_mxfp4_1x32(st["x"], colwise=True)
+        gq, gs, gqt, gst = fb.quant_mxfp4_1x32(st["dy"], colwise=True)
+        return (fb.gemm_mxfp4(xq, xs, st["w"], st["ws"]), fb.gemm_mxfp4(gq, gs, st["wt"], st["wts"]),
+                fb.gemm_mxfp4(gqt, gst, xqt, xst, dtype=torch.float32))
+    if op == "experts":
+        counts, off, src, pos = fb.moe_plan(st["idx"], case["local"])
+        q, s, _, _ = fb.dispatch_mxfp4_1x32(st["x"], src)
+        return counts, off, pos, fb.grouped_gemm_mxfp4(off, q, s, st["w"], st["ws"], out=st["y"])
+    if op == "experts_step":
+        counts, off, src, pos = fb.moe_plan(st["idx"], case["local"], pad=256)
+        xq, xs, xqt, xst = fb.dispatch_mxfp4_1x32(st["x"], src, colwise=True)
+        gq, gs, gqt, gst = fb.dispatch_mxfp4_1x32(st["dy"], src, colwise=True)
+        return (counts, off, pos, fb.grouped_gemm_mxfp4(off, xq, xs, st["w"], st["ws"], out=st["y"]),
+                fb.grouped_gemm_mxfp4(off, gq, gs, st["wt"], st["wts"], out=st["dx"]),
+                fb.grouped_wgrad_mxfp4(off, gqt, gst, xqt, xst))
+    loss, counts = fb.moe_balance(st["logits"], st["idx"], 1e-2, score=case["score"], seq_off=st["seq_off"])
+    return loss, counts, fb.moe_balance_grad(st["dloss"], st["logits"], st["idx"], counts, 1e-2, score=case["score"],
+                                             seq_off=st["seq_off"])
+
+
+def run(state):
+    return _run_own(state) if own else _run_plain(state)
+
+
+# ---------------------------------------------------------------------------
+# the definition in 64 bits
+# ---------------------------------------------------------------------------
+
+def _exact_values(x):
+    """MXFP4 values along the last axis by search among the grid's midpoints, float64."""
+    x = x.double()
+    k = x.shape[-1]
+    fill = -k % 32
+    t = torch.cat((x, x.new_zeros(*x.shape[:-1], fill)), -1).unflatten(-1, (-1, 32))
+    amax = t.abs().amax(-1, keepdim=True)
+    scale = torch.exp2(torch.clamp(torch.floor(torch.log2(amax.clamp(min=2.0 ** -300))) - 2, -127, 127))
+    grid = torch.tensor(_GRID, dtype=torch.float64, device=x.device)
+    mid = (grid[1:] + grid[:-1]) / 2
+    a = t.abs() / scale
+    # a midpoint goes to the neighbour with the even code: up from an odd code, down from an even one
+    below, upto = torch.searchsorted(mid, a.contiguous()), torch.searchsorted(mid, a.contiguous(), right=True)
+    code = torch.where(below == upto, below, torch.where(below % 2 == 0, below, upto))
+    return (torch.sign(t) * grid[code] * scale).flatten(-2)[..., :k]
+
+
+def _exact_packed(q, s, k):
+    low, high = (q % 16).long(), (q // 16).long()
+    code = torch.empty((*q.shape[:-1], 2 * q.shape[-1]), dtype=torch.int64, device=q.device)
+    code[..., 0::2], code[..., 1::2] = low, high
+    grid = torch.tensor(_GRID, dtype=torch.float64, device=q.device)
+    v = grid[code % 8] * (1 - 2 * (code // 8))
+    b = s.movedim(-3, -2).reshape(*v.shape[:-1], -1, 1).double()
+    return (v.unflatten(-1, (-1, 32)) * torch.exp2(b - 127)).flatten(-2)[..., :k]
+
+
+def _exact_experts(st, case, step):
+    idx = st["idx"].cpu()
+    groups, pad = case["local"], 256 if step else 1
+    topk = idx.shape[1]
+    rows, pos = [], torch.full_like(idx, -1)
+    counts, off = [], [0]
+    for e in range(groups):
+        at = (idx.flatten() == e).nonzero().flatten()
+        pos.view(-1)[at] = torch.arange(len(at), dtype=torch.int32) + off[-1]
+        rows.append((off[-1], at // topk))
+        counts.append(len(at))
+        off.append(off[-1] + -(-len(at) // pad) * pad)
+    out = [torch.tensor(counts, dtype=torch.int32), torch.tensor(off, dtype=torch.int32), pos]
+    w = _exact_packed(st["w"], st["ws"], case["k"])
+    x = _exact_values(st["x"])
+    y = torch.zeros(st["y"].shape, dtype=torch.float64, device="cuda")
+    for e, (at, token) in enumerate(rows):
+        y[at:at + len(token)] = x[token.cuda()] @ w[e].t()
+    out.append(y)
+    if step:
+        wt = _exact_packed(st["wt"], st["wts"], case["n"])
+        dy = _exact_values(st["dy"])
+        dx = torch.zeros(st["dx"].shape, dtype=torch.float64, device="cuda")
+        dw = torch.zeros((groups, case["n"], case["k"]), dtype=torch.float64, device="cuda")
+        for e, (at, token) in enumerate(rows):
+            token = token.cuda()
+            dx[at:at + len(token)] = dy[token] @ wt[e].t()
+            dw[e] = _exact_values(st["dy"][token].t()) @ _exact_values(st["x"][token].t()).t()
+        out += [dx, dw]
+    return out
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    op = case["op"]
+    if op == "cast":
+        out = [_exact_values(st["x"])]
+        if case["both"]:
+            out.append(_exact_values(st["x"].t()))
+        return out
+    if op == "linear":
+        return _exact_values(st["x"]) @ _exact_packed(st["w"], st["ws"], case["k"]).t()
+    if op == "step":
+        return (_exact_values(st["x"]) @ _exact_packed(st["w"], st["ws"], case["k"]).t(),
+                _exact_values(st["dy"]) @ _exact_packed(st["wt"], st["wts"], case["n"]).t(),
+                _exact_values(st["dy"].t()) @ _exact_values(st["x"].t()).t())
+    if op in ("experts", "experts_step"):
+        return _exact_experts(st, case, op == "experts_step")
+    logits, idx, off = st["logits"].double(), st["idx"].long(), st["seq_off"].tolist()
+    s, experts = len(off) - 1, logits.shape[1]
+    sig = torch.sigmoid(logits)
+    score = torch.softmax(logits, 1) if case["score"] == "softmax" else sig / sig.sum(1, keepdim=True)
+    loss = torch.zeros((), dtype=torch.float64, device="cuda")
+    counts = torch.zeros((s, experts), dtype=torch.int32, device="cuda")
+    grad = torch.zeros_like(logits)
+    for i in range(s):
+        token = torch.arange(off[i], off[i + 1], device="cuda")
+        token = token[(idx[token] >= 0).any(1)]
+        if not len(token):
+            continue
+        chosen = idx[token]
+        counts[i] = torch.bincount(chosen[chosen >= 0], minlength=experts)
+        f = counts[i].double() * experts / (idx.shape[1] * len(token))
+        p = score[token]
+        loss += 1e-2 / s * torch.dot(f, p.mean(0))
+        back = st["dloss"].double() * 1e-2 / s * f / len(token)
+        g = p * (back - (p @ back)[:, None])
+        grad[token] = g if case["score"] == "softmax" else g * (1 - sig[token])
+    return loss, counts, grad
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+
+_MX = 17 / 32     # bytes an element: half a byte of code, a scale byte for 32
+
+
+def _local(case):
+    """Rows this GPU's experts are expected to get."""
+    p = [(i + 1) ** -case["zipf"] for i in range(case["experts"])]
+    k = min(case["topk"], case["experts"])
+    # probability that expert i is among k distinct draws, close enough: 1 - (1 - p)^c with sum k
+    total = sum(p)
+    lo, hi = 0.0, 1e4
+    for _ in range(60):
+        c = (lo + hi) / 2
+        lo, hi = (c, hi) if sum(1 - (1 - v / total) ** c for v in p) < k else (lo, c)
+    return case["tokens"] * sum(1 - (1 - v / total) ** lo for v in p[: case["local"]])
+
+
+def work(case):
+    size = {"bf16": 2, "fp16": 2, "fp32": 4}.get(case.get("type", "bf16"))
+    op = case["op"]
+    if op == "cast":
+        n = case["rows"] * case["cols"]
+        return {"bytes": n * (size + (4 if case["both"] else 2)), "flops": 2 * n}
+    if op in ("linear", "step"):
+        m, n, k = case["m"], case["n"], case["k"]
+        if op == "linear":
+            return {"bytes": m * k * size + n * k * _MX + m * n * 2, "flops": 2 * m * n * k}
+        return {"bytes": m * k * (size + 2) + m * n * 4 + n * k * (2 * _MX + 4), "flops": 6 * m * n * k}
+    if op in ("experts", "experts_step"):
+        rows, t, n, k, g = _local(case), case["tokens"], case["n"], case["k"], case["local"]
+        ints = 8 * t * case["topk"]
+        if op == "experts":
+            return {"bytes": ints + min(t, rows) * k * 2 + g * n * k * _MX + rows * n * 2, "flops": 2 * rows * n * k}
+        return {"bytes": ints + min(t, rows) * (n + k) * 2 + g * n * k * (2 * _MX + 4) + rows * (n + k) * 2,
+                "flops": 6 * rows * n * k}
+    n = case["tokens"] * case["experts"]
+    return {"bytes": 2 * n * size + 4 * case["tokens"] * case["topk"], "flops": 12 * n}
