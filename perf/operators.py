@@ -333,9 +333,9 @@ def _run_own(st):
         return (counts, off, pos, fb.grouped_gemm_mxfp4(off, xq, xs, st["w"], st["ws"], out=st["y"]),
                 fb.grouped_gemm_mxfp4(off, gq, gs, st["wt"], st["wts"], out=st["dx"]),
                 fb.grouped_wgrad_mxfp4(off, gqt, gst, xqt, xst))
-    loss, counts = fb.moe_balance(st["logits"], st["idx"], 1e-2, score=case["score"], seq_off=st["seq_off"])
-    return loss, counts, fb.moe_balance_grad(st["dloss"], st["logits"], st["idx"], counts, 1e-2, score=case["score"],
-                                             seq_off=st["seq_off"])
+    loss, counts, real = fb.moe_balance(st["logits"], st["idx"], 1e-2, score=case["score"], seq_off=st["seq_off"])
+    return loss, counts, fb.moe_balance_grad(st["dloss"], st["logits"], st["idx"], counts, real, 1e-2,
+                                             score=case["score"], seq_off=st["seq_off"])
 
 
 def run(state):
