@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp8bq.so")
 PROBE_LIB = os.path.join(PKG, "libfp8bq_probe.so")
 
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "gemm_quant.hip", "gemm_grouped.hip", "gemm_decode.hip"]
+SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "gemm_quant.hip", "gemm_grouped.hip", "gemm_decode.hip",
+           "api_mxfp4.cpp", "mxfp4_quant.hip", "mxfp4_gemm.hip", "moe.hip"]
 # measurement probes of the matrix instruction (a library of their own, not the GEMM path)
 PROBE_SOURCES = ["probe.hip"]
 

@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "entry.h"
 #include "internal.h"
 
 static_assert(FP8BQ_DECODE_NOALLOC_SCRATCH_BYTES == fp8bq::kNoAllocScratchBytes, "scratch size in the header");
@@ -69,6 +70,20 @@ int launched(hipError_t e, const char* what) {
 constexpr int64_t kMaxTiles = (int64_t)1 << 31;
 
 }  // namespace
+
+// For the entry points in the other files (entry.h).
+namespace fp8bq {
+
+int entry_fail(int status, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return status;
+}
+int entry_device() { return check_device(); }
+
+}  // namespace fp8bq
 
 extern "C" {
 

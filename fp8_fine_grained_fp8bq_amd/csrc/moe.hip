@@ -1,0 +1,496 @@
+// Routing of tokens to experts: the dispatch plan (counts, offsets, stable row
+// order) and the router's balance loss with its gradient. Definitions:
+// include/fp8bq.h. No floating-point atomics: every sum has a fixed order.
+#include "../../include/fp8bq.h"
+#include "mxfp4.h"
+
+namespace fp8bq {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Dispatch plan: a stable counting sort of the choices by expert. Each block
+// owns a contiguous piece of the flattened choices. Up to one piece it is one
+// launch; with more, a first launch writes each piece's histogram to the
+// workspace and every block of the second adds up what comes before it (at
+// most 256 x 256 counts from the cache, one expert per thread). Within a
+// block, wave w owns a contiguous quarter, walks it 64 choices at a time and
+// ranks equal experts by eight ballots over the expert's bits, so that the
+// order is that of the tokens whatever runs when.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 256;
+constexpr int kPlanPiece = 2048;
+
+struct PlanArgs {
+  const int32_t* idx;
+  int tokens, topk;
+  int64_t ldidx;
+  int groups, pad, cap;
+  int piece;                         // choices per block
+  int32_t *counts, *row_off, *src, *pos, *ws;
+};
+
+__device__ __forceinline__ int choice(const PlanArgs& p, int i) {
+  const int t = i / p.topk;
+  const int e = p.idx[(int64_t)t * p.ldidx + (i - t * p.topk)];
+  return e >= 0 && e < p.groups ? e : -1;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void moe_histogram_kernel(PlanArgs p) {
+  __shared__ int hist[256];
+  hist[threadIdx.x] = 0;
+  __syncthreads();
+  const int total = p.tokens * p.topk;
+  const int lo = blockIdx.x * p.piece, hi = min(lo + p.piece, total);
+  for (int i = lo + (int)threadIdx.x; i < hi; i += kPlanThreads) {
+    const int e = choice(p, i);
+    if (e >= 0) atomicAdd(&hist[e], 1);
+  }
+  __syncthreads();
+  p.ws[blockIdx.x * 256 + threadIdx.x] = hist[threadIdx.x];
+}
+
+__global__ __launch_bounds__(kPlanThreads) void moe_place_kernel(PlanArgs p) {
+  constexpr int kWaves = kPlanThreads / 64;
+  __shared__ int next[kWaves][256];       // next free row of (wave, expert)
+  __shared__ int scan[256];               // end of each expert's padded rows
+  __shared__ int filled[256];             // end of its real rows
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int total = p.tokens * p.topk;
+  const int nb = gridDim.x, blk = blockIdx.x;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) next[w][t] = 0;
+  __syncthreads();
+
+  // this block's choices per wave and expert
+  const int lo = blk * p.piece, hi = min(lo + p.piece, total);
+  const int part = p.piece / kWaves;
+  const int wlo = lo + wave * part, whi = min(wlo + part, hi);
+  for (int i = wlo + lane; i < whi; i += 64) {
+    const int e = choice(p, i);
+    if (e >= 0) atomicAdd(&next[wave][e], 1);
+  }
+  __syncthreads();
+
+  // expert t: choices before this block, and in all
+  int before = 0, all = 0;
+  if (nb == 1) {
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) all += next[w][t];
+  } else {
+#pragma unroll 8
+    for (int b = 0; b < nb; ++b) {
+      const int c = p.ws[b * 256 + t];
+      before += b < blk ? c : 0;
+      all += c;
+    }
+  }
+  // padded offsets: exclusive scan over the experts
+  const int padded = (all + p.pad - 1) / p.pad * p.pad;
+  scan[t] = padded;
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int v = t >= d ? scan[t - d] : 0;
+    __syncthreads();
+    scan[t] += v;
+    __syncthreads();
+  }
+  const int first = scan[t] - padded;
+  int at = first + before;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const int c = next[w][t];
+    next[w][t] = at;
+    at += c;
+  }
+  if (blk == 0) {
+    if (t < p.groups) {
+      p.counts[t] = all;
+      p.row_off[t] = first;
+    }
+    if (t == 255) p.row_off[p.groups] = scan[255];
+  }
+  // rows without a token: the padding of the experts dealt to this wave, and
+  // this block's share of what lies behind the last expert
+  filled[t] = first + all;
+  __syncthreads();
+  for (int e = blk + nb * wave; e < p.groups; e += nb * kWaves)
+    for (int r = filled[e] + lane; r < scan[e]; r += 64) p.src[r] = -1;
+  for (int64_t r = (int64_t)scan[255] + blk * kPlanThreads + t; r < p.cap; r += (int64_t)nb * kPlanThreads) p.src[r] = -1;
+
+  // places, in order
+  for (int i0 = wlo; i0 < whi; i0 += 64) {
+    const int i = i0 + lane;
+    const int e = i < whi ? choice(p, i) : -1;
+    uint64_t same = __ballot(e >= 0);
+#pragma unroll
+    for (int bit = 0; bit < 8; ++bit) {
+      const uint64_t m = __ballot((e >> bit) & 1);
+      same &= ((e >> bit) & 1) ? m : ~m;
+    }
+    const uint64_t below = same & ((1ull << lane) - 1);
+    const int rank = __popcll(below);
+    int row = -1;
+    if (e >= 0) row = next[wave][e] + rank;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before the first of its kind adds
+    if (e >= 0 && below == 0) next[wave][e] += __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (i < whi) {
+      p.pos[i] = row;
+      if (row >= 0) p.src[row] = i / p.topk;
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_moe_plan(const int32_t* idx, int tokens, int topk, int64_t ldidx, int groups, int pad,
+                           int32_t* counts, int32_t* row_off, int32_t* src, int cap, int32_t* pos, int32_t* ws,
+                           hipStream_t stream) {
+  PlanArgs p{idx, tokens, topk, ldidx, groups, pad, cap, kPlanPiece, counts, row_off, src, pos, ws};
+  const int total = tokens * topk;
+  if ((total + kPlanPiece - 1) / kPlanPiece > kMoePlanMaxBlocks)
+    p.piece = ((total + kMoePlanMaxBlocks - 1) / kMoePlanMaxBlocks + 255) / 256 * 256;
+  const int nb = (total + p.piece - 1) / p.piece;
+  if (nb > 1) {
+    moe_histogram_kernel<<<nb, kPlanThreads, 0, stream>>>(p);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  moe_place_kernel<<<nb, kPlanThreads, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Balance loss.
+// ---------------------------------------------------------------------------
+namespace {
+
+template <int T>
+__device__ __forceinline__ float logit(const void* base, int64_t i) {
+  if constexpr (T == FP8BQ_FP32) return static_cast<const float*>(base)[i];
+  else if constexpr (T == FP8BQ_BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[i] << 16);
+  else return (float)static_cast<const _Float16*>(base)[i];
+}
+template <int T>
+__device__ __forceinline__ void put(void* base, int64_t i, float v) {
+  if constexpr (T == FP8BQ_FP32) static_cast<float*>(base)[i] = v;
+  else if constexpr (T == FP8BQ_BF16) static_cast<__bf16*>(base)[i] = (__bf16)v;
+  else static_cast<_Float16*>(base)[i] = (_Float16)v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+
+// Tokens of sequence s, clamped into the batch; s == sequences: nothing here.
+__device__ __forceinline__ void seq_range(const MoeBalanceArgs& a, int s, int64_t& lo, int64_t& hi) {
+  lo = 0;
+  hi = a.tokens;
+  if (a.seq_off) {
+    lo = min(max((int64_t)a.seq_off[s], (int64_t)0), a.tokens);
+    hi = min(max((int64_t)a.seq_off[s + 1], lo), a.tokens);
+  }
+}
+
+// Whether a token has a choice inside [0, experts) (all lanes of the wave).
+__device__ __forceinline__ bool is_real(const MoeBalanceArgs& a, int64_t t) {
+  bool any = false;
+  for (int j = threadIdx.x & 63; j < a.topk; j += 64) {
+    const int e = a.idx[t * a.ldidx + j];
+    any |= e >= 0 && e < a.experts;
+  }
+  return __any(any);
+}
+
+// p of a token: lane l holds experts l, l + 64, .... v: logits in, p out;
+// open: 1 - sigmoid (SIGMOID).
+template <bool SIG, int VPL>
+__device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL], int experts) {
+  const int lane = threadIdx.x & 63;
+  float sum = 0.f;
+  if constexpr (SIG) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      // sigmoid and its complement from the same exponential, neither by subtraction
+      const float z = expf(-fabsf(v[i])), inv = 1.f / (1.f + z);
+      const float big = inv, small = z * inv;
+      const bool in = lane + 64 * i < experts;
+      open[i] = v[i] >= 0.f ? small : big;
+      v[i] = in ? (v[i] >= 0.f ? big : small) : 0.f;
+      sum += v[i];
+    }
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, lane + 64 * i < experts ? v[i] : -INFINITY);
+    m = wave_max(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = lane + 64 * i < experts && m > -INFINITY ? expf(v[i] - m) : 0.f;
+      sum += v[i];
+    }
+  }
+  sum = wave_sum(sum);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] *= inv;
+}
+
+constexpr int kBalWaves = 4;
+
+// Pieces a sequence is cut into: about 1024 blocks in all, none shorter than
+// it need be for the tokens at hand.
+int balance_pieces(int64_t tokens, int64_t sequences) {
+  int64_t c = 1024 / sequences;
+  const int64_t per = (tokens / sequences + 4 * kBalWaves - 1) / (4 * kBalWaves);
+  c = c < per ? c : per;
+  return (int)(c < 1 ? 1 : c > 256 ? 256 : c);
+}
+
+// Workspace: per (sequence, piece): experts floats (sums of p), experts ints
+// (counts), one int (real tokens); then one float per sequence (its loss) and
+// the ticket.
+struct BalanceWs {
+  float* psum;
+  int32_t* cnt;
+  int32_t* real;
+  float* seq_loss;
+  int32_t* ticket;
+};
+__host__ __device__ inline BalanceWs balance_ws(void* ws, int64_t experts, int64_t sequences, int64_t pieces) {
+  BalanceWs w;
+  const int64_t rows = sequences * pieces;
+  w.psum = static_cast<float*>(ws);
+  w.cnt = reinterpret_cast<int32_t*>(w.psum + rows * experts);
+  w.real = w.cnt + rows * experts;
+  w.seq_loss = reinterpret_cast<float*>(w.real + rows);
+  w.ticket = reinterpret_cast<int32_t*>(w.seq_loss + sequences);
+  return w;
+}
+
+// Block (piece, sequence): a wave per token; lane l sums p of experts l, l + 64,
+// ... in registers, the waves meet in LDS.
+template <int T, bool SIG, int VPL>
+__global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBalanceArgs a, int pieces, void* ws) {
+  __shared__ float sums[kBalWaves][VPL * 64];
+  __shared__ int hist[VPL * 64];
+  __shared__ int reals[kBalWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const BalanceWs w = balance_ws(ws, a.experts, a.sequences, pieces);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *w.ticket = 0;
+  for (int i = tid; i < VPL * 64; i += 64 * kBalWaves) hist[i] = 0;
+  __syncthreads();
+  int64_t lo, hi;
+  seq_range(a, blockIdx.y, lo, hi);
+  const int64_t per = (hi - lo + pieces - 1) / pieces;
+  const int64_t t0 = lo + (int64_t)blockIdx.x * per, t1 = min(t0 + per, hi);
+  float acc[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  int real = 0;
+  for (int64_t t = t0 + wave; t < t1; t += kBalWaves) {
+    if (!is_real(a, t)) continue;
+    ++real;
+    for (int j = lane; j < a.topk; j += 64) {
+      const int e = a.idx[t * a.ldidx + j];
+      if (e >= 0 && e < a.experts) atomicAdd(&hist[e], 1);
+    }
+    float v[VPL], open[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      v[i] = lane + 64 * i < a.experts ? logit<T>(a.logits, t * a.ldl + lane + 64 * i) : 0.f;
+    probabilities<SIG, VPL>(v, open, a.experts);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) sums[wave][lane + 64 * i] = acc[i];
+  if (lane == 0) reals[wave] = real;
+  __syncthreads();
+  const int64_t row = (int64_t)blockIdx.y * pieces + blockIdx.x;
+  for (int e = tid; e < a.experts; e += 64 * kBalWaves) {
+    float s = sums[0][e];
+#pragma unroll
+    for (int v = 1; v < kBalWaves; ++v) s += sums[v][e];
+    w.psum[row * a.experts + e] = s;
+    w.cnt[row * a.experts + e] = hist[e];
+  }
+  if (tid == 0) {
+    int s = 0;
+    for (int v = 0; v < kBalWaves; ++v) s += reals[v];
+    w.real[row] = s;
+  }
+}
+
+// One block per sequence adds up its pieces (256 threads over experts), writes
+// counts and real, and its loss; the last block to finish adds the sequences'
+// losses in order.
+__global__ __launch_bounds__(256) void balance_final_kernel(MoeBalanceArgs a, int pieces, void* ws, float* loss,
+                                                            int32_t* counts, int32_t* real_out) {
+  __shared__ double red[256];
+  __shared__ int last;
+  const int tid = threadIdx.x, s = blockIdx.x;
+  const BalanceWs w = balance_ws(ws, a.experts, a.sequences, pieces);
+  const int64_t row0 = (int64_t)s * pieces;
+  int real = 0;
+  for (int c = 0; c < pieces; ++c) real += w.real[row0 + c];
+  double dot = 0.0;
+  for (int e = tid; e < a.experts; e += 256) {
+    double p = 0.0;
+    int n = 0;
+#pragma unroll 8
+    for (int c = 0; c < pieces; ++c) {
+      p += (double)w.psum[(row0 + c) * a.experts + e];
+      n += w.cnt[(row0 + c) * a.experts + e];
+    }
+    counts[(int64_t)s * a.experts + e] = n;
+    dot += p * n;
+  }
+  red[tid] = dot;
+  __syncthreads();
+  for (int d = 128; d >= 1; d >>= 1) {
+    if (tid < d) red[tid] += red[tid + d];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    real_out[s] = real;
+    const double r = (double)real;
+    const double l = real ? red[0] * a.experts / ((double)a.topk * r * r) : 0.0;
+    __hip_atomic_store(&w.seq_loss[s], (float)l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == a.sequences - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  double sum = 0.0;
+  for (int i = tid; i < a.sequences; i += 256)
+    sum += (double)__hip_atomic_load(&w.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  red[tid] = sum;
+  __syncthreads();
+  for (int d = 128; d >= 1; d >>= 1) {
+    if (tid < d) red[tid] += red[tid + d];
+    __syncthreads();
+  }
+  if (tid == 0) *loss = (float)(red[0] * (double)a.coef / a.sequences);
+}
+
+// Gradient. Block (piece, sequence), a wave per token; the lane's coefficients
+// dloss * coef / S * experts * c / (topk * n^2) stay in registers. Block row
+// `sequences` clears the tokens outside every sequence.
+template <int T, bool SIG, int VPL>
+__global__ __launch_bounds__(64 * kBalWaves) void balance_grad_kernel(MoeBalanceArgs a, int pieces, const float* dloss,
+                                                                      const int32_t* counts, const int32_t* real,
+                                                                      void* dlogits, int64_t lddl) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int s = blockIdx.y;
+  if (s == a.sequences) {
+    int64_t lo, hi, end;
+    seq_range(a, 0, lo, end);
+    seq_range(a, a.sequences - 1, end, hi);
+    for (int64_t t = (int64_t)blockIdx.x * kBalWaves + wave; t < a.tokens; t += (int64_t)pieces * kBalWaves) {
+      if (t >= lo && t < hi) continue;
+      for (int e = lane; e < a.experts; e += 64) put<T>(dlogits, t * lddl + e, 0.f);
+    }
+    return;
+  }
+  int64_t lo, hi;
+  seq_range(a, s, lo, hi);
+  const int64_t per = (hi - lo + pieces - 1) / pieces;
+  const int64_t t0 = lo + (int64_t)blockIdx.x * per, t1 = min(t0 + per, hi);
+  if (t0 >= t1) return;
+  const float n = (float)max(real[s], 1);
+  const float scale = dloss[0] * (a.coef / a.sequences) * ((float)a.experts / ((float)a.topk * n)) / n;
+  float f[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    f[i] = lane + 64 * i < a.experts ? scale * counts[(int64_t)s * a.experts + lane + 64 * i] : 0.f;
+  for (int64_t t = t0 + wave; t < t1; t += kBalWaves) {
+    const bool ok = is_real(a, t);
+    float v[VPL], open[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      v[i] = lane + 64 * i < a.experts ? logit<T>(a.logits, t * a.ldl + lane + 64 * i) : 0.f;
+    probabilities<SIG, VPL>(v, open, a.experts);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) dot += v[i] * f[i];
+    dot = wave_sum(dot);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      float d = v[i] * (f[i] - dot);
+      if constexpr (SIG) d *= open[i];
+      if (lane + 64 * i < a.experts) put<T>(dlogits, t * lddl + lane + 64 * i, ok ? d : 0.f);
+    }
+  }
+}
+
+template <int T, bool SIG, int VPL>
+hipError_t run_balance(const MoeBalanceArgs& a, float* loss, int32_t* counts, int32_t* real, void* ws, hipStream_t st) {
+  const int pieces = balance_pieces(a.tokens, a.sequences);
+  balance_partial_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences), 64 * kBalWaves, 0, st>>>(a, pieces, ws);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  balance_final_kernel<<<a.sequences, 256, 0, st>>>(a, pieces, ws, loss, counts, real);
+  return hipGetLastError();
+}
+template <int T, bool SIG, int VPL>
+hipError_t run_grad(const MoeBalanceArgs& a, const float* dloss, const int32_t* counts, const int32_t* real,
+                    void* dlogits, int64_t lddl, hipStream_t st) {
+  const int pieces = balance_pieces(a.tokens, a.sequences);
+  balance_grad_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences + 1), 64 * kBalWaves, 0, st>>>(a, pieces, dloss, counts,
+                                                                                             real, dlogits, lddl);
+  return hipGetLastError();
+}
+
+// f<T, SIG, VPL>() for the call's type, score and experts per lane.
+template <int T, bool SIG, class F>
+hipError_t by_width(int experts, F&& f) {
+  if (experts <= 64) return f.template operator()<T, SIG, 1>();
+  if (experts <= 128) return f.template operator()<T, SIG, 2>();
+  if (experts <= 256) return f.template operator()<T, SIG, 4>();
+  if (experts <= 512) return f.template operator()<T, SIG, 8>();
+  return f.template operator()<T, SIG, 16>();
+}
+template <class F>
+hipError_t by_kind(int ltype, bool sigmoid, int experts, F&& f) {
+  switch (ltype) {
+    case FP8BQ_BF16: return sigmoid ? by_width<FP8BQ_BF16, true>(experts, f) : by_width<FP8BQ_BF16, false>(experts, f);
+    case FP8BQ_FP16: return sigmoid ? by_width<FP8BQ_FP16, true>(experts, f) : by_width<FP8BQ_FP16, false>(experts, f);
+    default: return sigmoid ? by_width<FP8BQ_FP32, true>(experts, f) : by_width<FP8BQ_FP32, false>(experts, f);
+  }
+}
+struct Forward {
+  const MoeBalanceArgs& a; float* loss; int32_t* counts; int32_t* real; void* ws; hipStream_t st;
+  template <int T, bool SIG, int VPL> hipError_t operator()() { return run_balance<T, SIG, VPL>(a, loss, counts, real, ws, st); }
+};
+struct Backward {
+  const MoeBalanceArgs& a; const float* dloss; const int32_t* counts; const int32_t* real; void* dlogits; int64_t lddl;
+  hipStream_t st;
+  template <int T, bool SIG, int VPL> hipError_t operator()() {
+    return run_grad<T, SIG, VPL>(a, dloss, counts, real, dlogits, lddl, st);
+  }
+};
+
+}  // namespace
+
+int64_t moe_balance_workspace(int64_t tokens, int64_t experts, int64_t sequences) {
+  const int64_t rows = sequences * balance_pieces(tokens, sequences);
+  return 4 * (rows * (2 * experts + 1) + sequences + 1);
+}
+
+hipError_t launch_moe_balance(const MoeBalanceArgs& a, int ltype, bool sigmoid, float* loss, int32_t* counts,
+                              int32_t* real, void* ws, hipStream_t stream) {
+  return by_kind(ltype, sigmoid, a.experts, Forward{a, loss, counts, real, ws, stream});
+}
+
+hipError_t launch_moe_balance_grad(const MoeBalanceArgs& a, int ltype, bool sigmoid, const float* dloss,
+                                   const int32_t* counts, const int32_t* real, void* dlogits, int64_t lddl,
+                                   hipStream_t stream) {
+  return by_kind(ltype, sigmoid, a.experts, Backward{a, dloss, counts, real, dlogits, lddl, stream});
+}
+
+}  // namespace fp8bq

@@ -1,0 +1,343 @@
+// MXFP4 quantisation (along rows, along columns, or both in one read), the
+// dispatch form that picks rows by an index, and the read-back. Formats and
+// layouts: include/fp8bq.h; the codec: mxfp4_codec.h. All of it is bound by
+// memory: 2 (4) bytes read and 17/32 bytes written per element and form.
+#include "../../include/fp8bq.h"
+#include "mxfp4.h"
+#include "mxfp4_codec.h"
+
+namespace fp8bq {
+namespace {
+
+typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
+
+template <int T> struct Elem;
+template <> struct Elem<FP8BQ_BF16> {
+  using type = uint16_t;
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+  static __device__ __forceinline__ uint16_t round(float v) {
+    const __bf16 b = (__bf16)v;
+    uint16_t r;
+    __builtin_memcpy(&r, &b, 2);
+    return r;
+  }
+};
+template <> struct Elem<FP8BQ_FP16> {
+  using type = uint16_t;
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ float value(uint16_t b) {
+    _Float16 h;
+    __builtin_memcpy(&h, &b, 2);
+    return (float)h;
+  }
+  static __device__ __forceinline__ uint16_t round(float v) {
+    const _Float16 h = (_Float16)v;
+    uint16_t r;
+    __builtin_memcpy(&r, &h, 2);
+    return r;
+  }
+};
+template <> struct Elem<FP8BQ_FP32> {
+  using type = float;
+  static constexpr int kBytes = 4;
+  static __device__ __forceinline__ float value(float b) { return b; }
+  static __device__ __forceinline__ float round(float v) { return v; }
+};
+
+// The values of the dwords w (two 16-bit elements each, or one fp32).
+template <int T, int N>
+__device__ __forceinline__ void unpack(const uint32_t* w, float (&v)[N]) {
+  if constexpr (T == FP8BQ_FP32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      v[2 * i] = Elem<T>::value((uint16_t)(w[i] & 0xFFFFu));
+      v[2 * i + 1] = Elem<T>::value((uint16_t)(w[i] >> 16));
+    }
+  }
+}
+
+// N elements of a row from column col on as dwords, zeros past `cols`. VEC: the
+// row is 16-byte aligned; a group that crosses the end, and every group
+// without VEC, is read element by element.
+template <int T, int N, bool VEC>
+__device__ __forceinline__ void load_row(const typename Elem<T>::type* row, int64_t col, int64_t cols, bool ok,
+                                         uint32_t (&w)[N * Elem<T>::kBytes / 4]) {
+  constexpr int kDw = N * Elem<T>::kBytes / 4;
+#pragma unroll
+  for (int i = 0; i < kDw; ++i) w[i] = 0;
+  if (!ok || col >= cols) return;
+  if (VEC && col + N <= cols) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + col);
+#pragma unroll
+    for (int i = 0; i < kDw / 4; ++i) {
+      const uint4 u = p[i];
+      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (col + i < cols) {
+      if constexpr (T == FP8BQ_FP32) w[i] = __float_as_uint(row[col + i]);
+      else w[i / 2] |= (uint32_t)row[col + i] << (16 * (i & 1));
+    }
+  }
+}
+
+// DPP moves within 16-lane rows.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;            // quad_perm [1,0,3,2], [2,3,0,1]
+constexpr int kRor4 = 0x124, kRor8 = 0x128;          // row_ror: rotate a row of 16 lanes
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The source row of row r of the quantised matrix; ok = false for a zero row.
+template <bool IDX>
+__device__ __forceinline__ int64_t source(const MxQuantArgs& p, int64_t r, bool& ok) {
+  ok = r < p.rows;
+  if constexpr (IDX) {
+    const int32_t t = ok ? p.src[r] : -1;
+    ok = t >= 0 && t < p.xrows;
+    return ok ? t : 0;
+  }
+  return ok ? r : 0;
+}
+
+// Row form. 16 lanes take one 256-element chunk of a row, 16 elements each (32
+// contiguous bytes of bf16), so a tile is a pair of lanes and a lane's codes
+// are one 8-byte store; a block takes 16 rows of one chunk, the chunks of a row
+// run fastest over the grid. A lane pair's scale byte is shifted to its place
+// in the chunk's eight; OR over the lanes of each half row gives dwords.
+template <int T, bool NOSAT, bool IDX, bool VEC>
+__global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks) {
+  const int t = threadIdx.x, l16 = t & 15;
+  const int chunk = (int)(blockIdx.x % (unsigned)chunks);
+  const int64_t r = (int64_t)(blockIdx.x / (unsigned)chunks) * 16 + (t >> 4);
+  bool ok;
+  const int64_t xr = source<IDX>(p, r, ok);
+  constexpr int kDw = 16 * Elem<T>::kBytes / 4;
+  uint32_t w[kDw];
+  const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
+  load_row<T, 16, VEC>(row, (int64_t)chunk * 256 + l16 * 16, p.cols, ok, w);
+  float v[16];
+  unpack<T>(w, v);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max2(amax, mx_mag(v[i]));
+  amax = max2(amax, dpp<kXor1>(amax));
+  const uint32_t byte = mx_scale_byte<NOSAT>(amax);
+  uint32_t sc = (l16 & 1) ? 0u : byte << (8 * ((l16 >> 1) & 3));
+  sc |= dpp<kXor2>(sc);
+  sc |= dpp<kRor4>(sc) & ((l16 & 7) < 4 ? 0u : 0xFFFFFFFFu);   // lane 4 (12) gathers lanes 0 .. 3 (8 .. 11)
+  if (r >= p.rows) return;
+  const uint2 codes = make_uint2(mx_codes8(v, byte), mx_codes8(v + 8, byte));
+  *reinterpret_cast<uint2*>(p.q + r * p.ldq + chunk * 128 + l16 * 8) = codes;
+  if ((l16 & 7) == 4) *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + r) * 8 + (l16 >> 3) * 4) = sc;
+}
+
+// Column form, and (ROWS) the row form beside it from the same read. A block
+// stages 128 rows of 256 bytes (128 columns, 64 of fp32) in LDS; then thread
+// (column dword, row tile) walks 32 rows of its dword: consecutive lanes on
+// consecutive dwords, no bank conflict, 16 bytes of codes per column. The four
+// row tiles' scale bytes of a column meet in LDS for one 4-byte store. Blocks
+// run over the rows first, so that the 64-byte pieces of a column's codes
+// that neighbouring blocks write meet in the cache. The grid covers whole
+// 256-element chunks in both directions: what lies past the matrix is zeros.
+template <int T, bool NOSAT, bool IDX, bool VEC, bool ROWS>
+__global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p) {
+  constexpr int kPer = 4 / Elem<T>::kBytes;             // elements per dword
+  constexpr int kCols = 64 * kPer;
+  constexpr int kLane = 4 * kPer;                       // elements of a lane's 16 bytes
+  __shared__ uint32_t tile[128][64];
+  __shared__ uint8_t scales[kCols][4];
+  const int t = threadIdx.x, l16 = t & 15;
+  const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * kCols;
+
+  uint32_t w[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bool ok;
+    const int64_t xr = source<IDX>(p, r0 + i * 16 + (t >> 4), ok);
+    const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
+    load_row<T, kLane, VEC>(row, c0 + l16 * kLane, p.cols, ok, w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(&tile[i * 16 + (t >> 4)][l16 * 4]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+
+  if constexpr (ROWS) {
+    // a tile is 4 lanes (8 of fp32)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + i * 16 + (t >> 4);
+      float v[8];
+      if constexpr (kPer == 1) v[4] = v[5] = v[6] = v[7] = 0.f;
+      float u[kLane];
+      unpack<T>(w[i], u);
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) v[j] = u[j];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < kLane; ++j) amax = max2(amax, mx_mag(v[j]));
+      amax = max2(amax, dpp<kXor1>(amax));
+      amax = max2(amax, dpp<kXor2>(amax));
+      if constexpr (kPer == 1) {                        // lanes 0 .. 3 and 4 .. 7 of each half row
+        const uint32_t a = dpp<kRor4>(amax), b = dpp<0x12C>(amax);   // ror 4, ror 12
+        amax = max2(amax, (l16 & 4) ? a : b);
+      }
+      const uint32_t byte = mx_scale_byte<NOSAT>(amax);
+      const uint32_t code = mx_codes8(v, byte);
+      if constexpr (kPer == 2) {
+        uint32_t sc = byte << (8 * (l16 >> 2));
+        sc |= dpp<kRor4>(sc);
+        sc |= dpp<kRor8>(sc);
+        if (r < p.rows) {
+          *reinterpret_cast<uint32_t*>(p.q + r * p.ldq + c0 / 2 + l16 * 4) = code;
+          if (l16 == 0) *reinterpret_cast<uint32_t*>(p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32) = sc;
+        }
+      } else {
+        uint32_t sc = byte << (8 * (l16 >> 3));
+        sc |= dpp<kRor8>(sc);
+        if (r < p.rows) {
+          *reinterpret_cast<uint16_t*>(p.q + r * p.ldq + c0 / 2 + l16 * 2) = (uint16_t)code;
+          if (l16 == 0) *reinterpret_cast<uint16_t*>(p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32) = (uint16_t)sc;
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  const int cd = t & 63, rt = t >> 6;
+  uint32_t d[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) d[i] = tile[rt * 32 + i][cd];
+#pragma unroll
+  for (int h = 0; h < kPer; ++h) {
+    float v[32];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if constexpr (kPer == 1) v[i] = __uint_as_float(d[i]);
+      else v[i] = Elem<T>::value((uint16_t)(d[i] >> (16 * h)));
+      amax = max2(amax, mx_mag(v[i]));
+    }
+    const uint32_t byte = mx_scale_byte<NOSAT>(amax);
+    scales[cd * kPer + h][rt] = (uint8_t)byte;
+    const int64_t c = c0 + cd * kPer + h;
+    if (c < p.cols)
+      *reinterpret_cast<uint4*>(p.qt + c * p.ldqt + r0 / 2 + rt * 16) =
+          make_uint4(mx_codes8(v, byte), mx_codes8(v + 8, byte), mx_codes8(v + 16, byte), mx_codes8(v + 24, byte));
+  }
+  __syncthreads();
+  if (t < kCols && c0 + t < p.cols)
+    *reinterpret_cast<uint32_t*>(p.st + ((r0 / 256) * p.ldst + c0 + t) * 8 + (r0 % 256) / 32) =
+        *reinterpret_cast<const uint32_t*>(scales[t]);
+}
+
+// Read-back: 16 lanes take a chunk of a row, 16 codes each.
+template <int T, bool VEC>
+__global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ q, int64_t rows, int64_t cols,
+                                                         int64_t ldq, const uint8_t* __restrict__ s, int64_t lds,
+                                                         typename Elem<T>::type* __restrict__ y, int64_t ldy,
+                                                         int chunks) {
+  const int t = threadIdx.x, l16 = t & 15;
+  const int chunk = (int)(blockIdx.x % (unsigned)chunks);
+  const int64_t r = (int64_t)(blockIdx.x / (unsigned)chunks) * 16 + (t >> 4);
+  const int64_t c = (int64_t)chunk * 256 + l16 * 16;
+  if (r >= rows || c >= cols) return;
+  const uint2 codes = *reinterpret_cast<const uint2*>(q + r * ldq + chunk * 128 + l16 * 8);
+  const float sc = mx_scale(s[((int64_t)chunk * lds + r) * 8 + (l16 >> 1)]);
+  typename Elem<T>::type o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t code = ((i < 8 ? codes.x : codes.y) >> (4 * (i & 7))) & 15u;
+    // E2M1 to fp32: exponent field 0 holds 0 and 0.5, else (1 + m / 2) * 2^(e - 1)
+    const uint32_t em = code & 7u;
+    const uint32_t mag = em >= 2 ? (em << 22) + (126u << 23) : (em ? 126u << 23 : 0u);
+    o[i] = Elem<T>::round(__uint_as_float(mag | ((code & 8u) << 28)) * sc);
+  }
+  auto* dst = y + r * ldy + c;
+  if (VEC && c + 16 <= cols) {
+    constexpr int kVecs = 16 * Elem<T>::kBytes / 16;
+    uint4 u[kVecs];
+    __builtin_memcpy(u, o, sizeof(u));
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4*>(dst)[i] = u[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c + i < cols) dst[i] = o[i];
+  }
+}
+
+template <int T, bool NOSAT, bool IDX, bool VEC>
+hipError_t run_quant(const MxQuantArgs& a, hipStream_t st) {
+  const int cchunks = (int)((a.cols + 255) / 256);
+  if (a.qt) {
+    constexpr int kCols = 64 * 4 / Elem<T>::kBytes;
+    const dim3 grid((unsigned)((a.rows + 255) / 256 * 2), (unsigned)(cchunks * (256 / kCols)));
+    if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, 256, 0, st>>>(a);
+    else mx_quant_cols_kernel<T, NOSAT, IDX, VEC, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    const unsigned blocks = (unsigned)((a.rows + 15) / 16) * (unsigned)cchunks;
+    mx_quant_rows_kernel<T, NOSAT, IDX, VEC><<<blocks, 256, 0, st>>>(a, cchunks);
+  }
+  return hipGetLastError();
+}
+
+template <int T>
+hipError_t pick_quant(const MxQuantArgs& a, bool nosat, hipStream_t st) {
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * Elem<T>::kBytes % 16 == 0;
+  const int sel = (nosat ? 4 : 0) + (a.src ? 2 : 0) + (vec ? 1 : 0);
+  switch (sel) {
+    case 0: return run_quant<T, false, false, false>(a, st);
+    case 1: return run_quant<T, false, false, true>(a, st);
+    case 2: return run_quant<T, false, true, false>(a, st);
+    case 3: return run_quant<T, false, true, true>(a, st);
+    case 4: return run_quant<T, true, false, false>(a, st);
+    case 5: return run_quant<T, true, false, true>(a, st);
+    case 6: return run_quant<T, true, true, false>(a, st);
+    default: return run_quant<T, true, true, true>(a, st);
+  }
+}
+
+template <int T>
+hipError_t run_dequant(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq, const uint8_t* s, int64_t lds,
+                       void* y, int64_t ldy, hipStream_t st) {
+  using E = typename Elem<T>::type;
+  const int chunks = (int)((cols + 255) / 256);
+  const unsigned blocks = (unsigned)((rows + 15) / 16) * (unsigned)chunks;
+  E* out = static_cast<E*>(y);
+  if (reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * Elem<T>::kBytes % 16 == 0)
+    mx_dequant_kernel<T, true><<<blocks, 256, 0, st>>>(q, rows, cols, ldq, s, lds, out, ldy, chunks);
+  else
+    mx_dequant_kernel<T, false><<<blocks, 256, 0, st>>>(q, rows, cols, ldq, s, lds, out, ldy, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, hipStream_t stream) {
+  switch (xtype) {
+    case FP8BQ_BF16: return pick_quant<FP8BQ_BF16>(a, nosat, stream);
+    case FP8BQ_FP16: return pick_quant<FP8BQ_FP16>(a, nosat, stream);
+    default: return pick_quant<FP8BQ_FP32>(a, nosat, stream);
+  }
+}
+
+hipError_t launch_dequant_mxfp4(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq, const uint8_t* s,
+                                int64_t lds, void* y, int ytype, int64_t ldy, hipStream_t stream) {
+  switch (ytype) {
+    case FP8BQ_BF16: return run_dequant<FP8BQ_BF16>(q, rows, cols, ldq, s, lds, y, ldy, stream);
+    case FP8BQ_FP16: return run_dequant<FP8BQ_FP16>(q, rows, cols, ldq, s, lds, y, ldy, stream);
+    default: return run_dequant<FP8BQ_FP32>(q, rows, cols, ldq, s, lds, y, ldy, stream);
+  }
+}
+
+}  // namespace fp8bq

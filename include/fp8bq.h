@@ -38,7 +38,7 @@
  * Conventions:
  *   - All matrices are row-major with an explicit leading dimension (ld, in
  *     elements). bf16 data is passed as raw 16-bit patterns.
- *   - Every pointer except `row_off` of fp8bq_grouped_gemm is a DEVICE pointer
+ *   - Every pointer except `row_off` of the FP8 grouped GEMMs is a DEVICE pointer
  *     owned by the caller. The library never allocates or frees memory and
  *     keeps no device state; outputs must not alias inputs.
  *   - `stream` is a hipStream_t (NULL = the null stream). Calls only enqueue
@@ -389,6 +389,206 @@ int fp8bq_grouped_gemm_decode_noalloc(int32_t groups, const int64_t* row_off, in
                                       const void* a, int64_t lda, const float* sa, int64_t ldsa,
                                       const void* b, int64_t ldb, const float* sb, int64_t ldsb,
                                       void* out, int64_t ldo, int flags, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * MXFP4: 4-bit microscaled operands (OCP Microscaling Formats v1.0: E2M1
+ * elements, one E8M0 scale for 32 of them), the matrix unit's own block
+ * scaling at twice the FP8 rate. Report section 3.5.2 asks hardware for this
+ * form of product ("MMA with group scaling"); the Linear's three GEMMs
+ * (section 3.3.1, Figure 6) are all served by one product, out = A B^T, whose
+ * operands are quantised along its inner dimension.
+ *
+ * Format. E2M1 codes stand for +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} (sign in bit 3).
+ * A tile is 32 consecutive elements along the inner dimension K; its scale is
+ * 2^e, stored as the byte e + 127. With amax the tile's largest magnitude,
+ *   e = floor(log2(amax)) - 2, at least -127 (the OCP rule: the largest
+ *       elements of a tile may saturate to 6 * 2^e), or, with
+ *   FP8BQ_MX_NOSAT, the smallest e >= -127 with amax <= 6 * 2^e (nothing
+ *       saturates); an all-zero tile gets byte 0.
+ * Codes are the exact quotient x * 2^-e rounded to nearest, ties to even,
+ * saturated to +-6, sign kept. A tile that holds a NaN or an infinity gets
+ * byte 0xFF (NaN) and zero codes: it reads back as NaN, and a product's rows
+ * or columns that meet it are NaN.
+ *
+ * Layout. Codes: two to a byte, the element with the even index in the low
+ * four bits; rows are padded with zero codes to a multiple of 256 elements
+ * ("chunks" of 128 bytes), so ld (bytes) >= 128 * ceil(k / 256), a multiple
+ * of 16. Scales: chunk-major like the FP8 activations', eight bytes (the
+ * chunk's tiles in order) per row: tile (r, 8 c + t) at s[(c * lds + r) * 8 + t],
+ * lds >= rows; bytes of tiles past k are 0.
+ * ------------------------------------------------------------------------- */
+enum { FP8BQ_MX_NOSAT = 0x20 };
+typedef enum { FP8BQ_BF16 = 0, FP8BQ_FP16 = 1, FP8BQ_FP32 = 2 } fp8bq_dtype;
+
+/*
+ * MXFP4 quantisation of x [rows, cols] (xtype: fp8bq_dtype, leading dimension
+ * ldx >= cols elements, any alignment of the element's own size; 16-byte
+ * aligned rows are read faster) along its rows, its columns, or both in one
+ * read.
+ * q, s     tiles along each row: codes [rows, ldq], scales as above over
+ *          ceil(cols / 256) chunks, lds >= rows. Both NULL: not wanted.
+ * qt, st   tiles along each column, written transposed: codes [cols, ldqt],
+ *          row j encoding column j; scales over ceil(rows / 256) chunks,
+ *          ldst >= cols. Both NULL: not wanted.
+ * flags    0 or FP8BQ_MX_NOSAT.
+ * Any rows, cols >= 1 (an incomplete last tile is filled up with zeros).
+ * Errors: E_INVAL (null, no output asked for, sizes <= 0, ld too small, bad
+ *         type or flags), E_SHAPE (too large), E_ALIGN (q, qt 16-byte aligned,
+ *         ldq, ldqt multiples of 16, s, st 8-byte aligned), E_DEVICE, E_HIP.
+ */
+int fp8bq_quant_mxfp4_1x32(const void* x, int xtype, int64_t rows, int64_t cols, int64_t ldx,
+                           void* q, int64_t ldq, void* s, int64_t lds,
+                           void* qt, int64_t ldqt, void* st, int64_t ldst, int flags, void* stream);
+
+/*
+ * The same of rows picked by an index: row r of the quantised matrix
+ * [rows, cols] is x[src[r]], x [xrows, cols]; a src[r] outside [0, xrows)
+ * stands for a row of zeros. This is the dispatch of tokens to experts: src is
+ * what fp8bq_moe_plan writes. src: device int32 [rows].
+ */
+int fp8bq_dispatch_mxfp4_1x32(const void* x, int xtype, int64_t xrows, int64_t cols, int64_t ldx,
+                              const int32_t* src, int64_t rows, void* q, int64_t ldq, void* s, int64_t lds,
+                              void* qt, int64_t ldqt, void* st, int64_t ldst, int flags, void* stream);
+
+/*
+ * Reads MXFP4 codes back: y [rows, cols] (ytype, ldy >= cols) = code * 2^e,
+ * rounded once where ytype cannot hold it (bf16 and fp32 hold every value
+ * that the quantiser writes for normal numbers). q, s as above. Errors as
+ * fp8bq_quant_mxfp4_1x32.
+ */
+int fp8bq_dequant_mxfp4_1x32(const void* q, int64_t rows, int64_t cols, int64_t ldq, const void* s, int64_t lds,
+                             void* y, int ytype, int64_t ldy, void* stream);
+
+/*
+ * MXFP4 product: out[i][j] = sum_k a_hat[i][k] * b_hat[j][k], accumulated in
+ * FP32 by the matrix unit, rounded once to otype (FP8BQ_BF16 or FP8BQ_FP32).
+ * a [m, k] and b [n, k] as the quantiser writes them (codes and scales past k,
+ * up to the next multiple of 256, zero); m, n, k >= 1 are free. The three
+ * GEMMs of a Linear y = x w^T:
+ *   forward  a = x along its rows,            b = w along its rows;
+ *   dgrad    a = dy along its rows,           b = w along its columns (qt, st);
+ *   wgrad    a = dy along its columns (qt, st), b = x along its columns.
+ * out [m, n], ldo >= n, aligned to its element's size (16-byte aligned rows
+ * are written faster). The result does not depend on what else runs and is the
+ * same at every call.
+ * Errors: E_INVAL, E_SHAPE (too large), E_ALIGN (a, b 16-byte aligned, lda, ldb
+ *         multiples of 16, sa, sb 8-byte aligned), E_DEVICE, E_HIP.
+ */
+int fp8bq_gemm_mxfp4(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const void* sa, int64_t ldsa,
+                     const void* b, int64_t ldb, const void* sb, int64_t ldsb,
+                     void* out, int otype, int64_t ldo, void* stream);
+
+/*
+ * Experts' MXFP4 products over rows grouped by expert (forward, and dgrad with
+ * weights quantised along their columns): expert e's rows
+ * [row_off[e], row_off[e + 1]) of a meet its weight b_e [n, k].
+ * groups   1 .. 256.
+ * row_off  DEVICE int32 [groups + 1], non-decreasing, 0 <= row_off[0],
+ *          row_off[groups] <= m; read by the kernel, so the call never waits
+ *          for the device. Any counts, empty experts included. Entries that
+ *          break these rules are clamped into range.
+ * a, sa    [m, k] with ldsa >= m: m is the number of rows the buffers hold.
+ * b, sb    expert e's codes at b + e * n * ldb, scales at
+ *          sb + e * ceil(k / 256) * ldsb * 8, ldsb >= n.
+ * out      [m, n]; rows that belong to no expert are left as they were.
+ * Errors: as fp8bq_gemm_mxfp4; E_INVAL for a null row_off, E_SHAPE for a bad
+ *         group count.
+ */
+int fp8bq_grouped_gemm_mxfp4(int32_t groups, const int32_t* row_off, int64_t m, int64_t n, int64_t k,
+                             const void* a, int64_t lda, const void* sa, int64_t ldsa,
+                             const void* b, int64_t ldb, const void* sb, int64_t ldsb,
+                             void* out, int otype, int64_t ldo, void* stream);
+
+/*
+ * Experts' weight gradients: out_e [m, n] = sum over the rows r of expert e of
+ * a_hat[.][r] * b_hat[.][r], where a [m, rows] and b [n, rows] are dy and x
+ * of the dispatched rows quantised along their columns (qt, st of
+ * fp8bq_dispatch_mxfp4_1x32).
+ * row_off  DEVICE int32 [groups + 1] as above with row_off[groups] <= rows, every
+ *          entry a multiple of 256 (fp8bq_moe_plan with pad = 256; entries are
+ *          rounded down to one). An expert without rows gets zeros.
+ * out      expert e's gradient at out + e * m * ldo elements, ldo >= n.
+ */
+int fp8bq_grouped_wgrad_mxfp4(int32_t groups, const int32_t* row_off, int64_t m, int64_t n, int64_t rows,
+                              const void* a, int64_t lda, const void* sa, int64_t ldsa,
+                              const void* b, int64_t ldb, const void* sb, int64_t ldsb,
+                              void* out, int otype, int64_t ldo, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Routing of tokens to experts (report section 3.2.2 dispatch; section 3.3.3
+ * "low-precision communication": the dispatched rows are what the experts'
+ * products consume).
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Dispatch plan from the router's choices: which rows each expert gets, in the
+ * order of tokens (stable, the same at every call).
+ * idx      int32 [tokens, topk], ldidx >= topk: chosen experts. Entries outside
+ *          [0, groups) are dropped (another GPU's expert, or -1 for none).
+ * pad      rows of each expert are padded to a multiple of it, 1 .. 1024.
+ * counts   int32 [groups]: choices of each expert.
+ * row_off  int32 [groups + 1]: offsets of the experts' padded rows.
+ * src      int32 [cap]: token of each dispatched row, -1 for padding and for
+ *          the rows behind the last expert. cap >= tokens * topk +
+ *          groups * (pad - 1) always suffices, and is required.
+ * pos      int32 [tokens, topk] (contiguous): dispatched row of each choice,
+ *          -1 for a dropped one.
+ * workspace  FP8BQ_MOE_PLAN_WORKSPACE_BYTES of device memory, 4-byte aligned,
+ *          contents irrelevant; calls that run at the same time need one each.
+ * Errors: E_INVAL, E_SHAPE (groups outside 1 .. 256, tokens * topk or cap at or
+ *         above 2^30), E_ALIGN (4-byte pointers), E_DEVICE, E_HIP.
+ */
+enum { FP8BQ_MOE_PLAN_WORKSPACE_BYTES = 256 * 256 * 4 };
+int fp8bq_moe_plan(const int32_t* idx, int64_t tokens, int64_t topk, int64_t ldidx, int32_t groups, int64_t pad,
+                   int32_t* counts, int32_t* row_off, int32_t* src, int64_t cap, int32_t* pos,
+                   void* workspace, void* stream);
+
+/*
+ * Balance loss of a router and its per-expert counts, over S sequences of a
+ * packed batch (the sequence-wise auxiliary loss; one sequence of all tokens
+ * gives the batch-wise one):
+ *   p_te = softmax of the token's logits, or their sigmoids divided by the
+ *          token's sum of sigmoids;
+ *   c_se = how often expert e is chosen in sequence s, n_s = the number of
+ *          tokens of s with at least one choice inside [0, experts) ("real"
+ *          tokens; the others are left out);
+ *   loss = coef / S * sum_s sum_e (experts * c_se / (topk * n_s)) *
+ *          (sum over the real tokens t of s of p_te) / n_s,
+ * a sequence without real tokens adding zero.
+ * logits   [tokens, experts] of ltype, ldl >= experts; experts 1 .. 1024.
+ *          -inf masks an expert out of a token (p = 0; a token with every
+ *          expert masked has p = 0 everywhere). NaN and +inf in a real token
+ *          make the results NaN. Tokens that take no part are not looked at.
+ * idx      int32 [tokens, topk], ldidx >= topk.
+ * seq_off  DEVICE int32 [sequences + 1], non-decreasing, or NULL for one
+ *          sequence of all tokens; clamped into [0, tokens]. Tokens outside
+ *          [seq_off[0], seq_off[sequences]) take no part.
+ * loss     float [1]; counts int32 [sequences, experts] (contiguous); real
+ *          int32 [sequences]: n_s.
+ * workspace  fp8bq_moe_balance_workspace_size bytes, 4-byte aligned, contents
+ *          irrelevant; calls that run at the same time need one each.
+ * Sums are float32 in a fixed order: the same result at every call.
+ * Errors: E_INVAL (null, sizes, score, type), E_SHAPE (experts above 1024,
+ *         more than 65535 sequences, tokens at or above 2^31), E_ALIGN,
+ *         E_DEVICE, E_HIP.
+ */
+enum { FP8BQ_SOFTMAX = 0, FP8BQ_SIGMOID = 1 };
+int fp8bq_moe_balance_workspace_size(int64_t tokens, int64_t experts, int64_t sequences, int64_t* bytes);
+int fp8bq_moe_balance(const void* logits, int ltype, int64_t tokens, int64_t experts, int64_t ldl,
+                      const int32_t* idx, int64_t topk, int64_t ldidx, const int32_t* seq_off, int64_t sequences,
+                      int score, float coef, float* loss, int32_t* counts, int32_t* real,
+                      void* workspace, void* stream);
+
+/*
+ * Its gradient: dlogits [tokens, experts] of ltype, lddl >= experts, from
+ * dloss (device float [1]), the logits and the forward call's idx, counts and
+ * real. Counts are constants of the gradient. Tokens that take no part get
+ * zeros. Other arguments as above.
+ */
+int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, int64_t tokens, int64_t experts,
+                           int64_t ldl, const int32_t* idx, int64_t topk, int64_t ldidx, const int32_t* seq_off,
+                           int64_t sequences, int score, float coef, const int32_t* counts, const int32_t* real,
+                           void* dlogits, int64_t lddl, void* stream);
 
 /* Thread-local description of the last non-OK status on this thread. */
 const char* fp8bq_last_error(void);
