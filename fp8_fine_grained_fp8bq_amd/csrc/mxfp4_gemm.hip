@@ -10,12 +10,14 @@
 // the row and its four scale bytes one dword. The weight side (B) is the
 // first operand: lane l's sixteen results are row l % 32 of A and, register r,
 // column 8 (r / 4) + 4 (l / 32) + r % 4 of B.
+#include <utility>
+
+#include "gemm_kernels.h"
 #include "mxfp4.h"
 
 namespace fp8bq {
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) {
@@ -154,8 +156,449 @@ __global__ __launch_bounds__(64 * WAVES) void mx_stream_kernel(MxGemmArgs p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tiled kernel. Workgroup tile 64 TM x 64 TN, four waves (one per SIMD) of
+// 32 TM x 32 TN; a step is one 256-element chunk: 128 bytes of each operand row
+// and 8 scale bytes. Persistent workgroups walk the output tiles; operands go
+// global -> LDS by LDS DMA two steps ahead into two stages (the FP8 kernels'
+// loads, swizzle and tile walk; an E2M1 chunk has the bytes of an FP8 one and
+// twice the products).
+//
+// A step is four slices of TM x TN MFMAs (slice t: K-blocks t and 4 + t of the
+// chunk). Each slice has its own fragment registers: while slice t runs, the
+// fragments that slice t - 1 used are read for the step they are needed in
+// next, so that every LDS read has a slice or more to land:
+//   slice 0: reads slice 3 of this step, then the one barrier of the step
+//            (every wave has read all of this stage, the other one has landed);
+//   slices 1 .. 3: read slices 0 .. 2 of the next step, and slice 1 on issues
+//            the loads of the step after it into this step's stage.
+// The accumulators sit in the AGPRs (256 of them at TM = TN = 4), tied to the
+// MFMA statements as in the power-of-two FP8 kernel.
+// ---------------------------------------------------------------------------
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+template <int TM, int TN>
+struct TileCfg {
+  static constexpr int kBM = 64 * TM, kBN = 64 * TN;
+  static constexpr int kBOff = kBM * 128;
+  static constexpr int kSaOff = (kBM + kBN) * 128;
+  static constexpr int kSbOff = kSaOff + (kBM < 128 ? 128 : kBM) * 8;   // a scale load covers 128 rows
+  static constexpr int kStage = kSbOff + (kBN < 128 ? 128 : kBN) * 8;
+  static constexpr int kRoundsA = kBM / 32, kRoundsB = kBN / 32;        // loads per wave: 8 rows each
+  static constexpr int kParts = kRoundsA + kRoundsB + 1;
+};
+
+// acc += over slice T; the hazard wait states as mfma_scaled of the FP8 kernels.
+template <int T>
+__device__ __forceinline__ void mfma_slice(v16f& acc, const v4i& b, const v4i& a, int sb, int sa) {
+  if constexpr (T == 0)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else if constexpr (T == 1)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else if constexpr (T == 2)
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+}
+
+struct MxTile {
+  int64_t m0, m_end, n0;
+  int e, c0, nc;                 // group, first chunk, chunks
+};
+
+// Group tables in LDS (rows or chunks of each group; row tiles before it).
+struct MxTables {
+  int lo[256], hi[256], before[257];
+};
+
+template <int MODE, int TM, int TN>
+struct MxWalk {
+  using C = TileCfg<TM, TN>;
+  const MxGemmArgs& p;
+  const MxTables& tab;
+  int tiles_m, tiles_n, total, start, nper, mine;
+
+  // Workgroup w runs on XCD w % 8. A grid of 8 C workgroups deals chunks of C
+  // consecutive tiles to the XCDs in turn, so that an XCD's workgroups share
+  // operand panels in its L2 at any time; another grid (fewer tiles than CUs)
+  // gives XCD x a contiguous range.
+  __device__ __forceinline__ MxWalk(const MxGemmArgs& p_, const MxTables& tab_) : p(p_), tab(tab_) {
+    tiles_n = (int)((p.n + C::kBN - 1) / C::kBN);
+    tiles_m = MODE == MX_ROWS ? tab.before[p.groups] : (int)((p.m + C::kBM - 1) / C::kBM);
+    total = tiles_m * tiles_n * (MODE == MX_K ? p.groups : 1);
+    const int G = gridDim.x, w = blockIdx.x, x = w % kXcds, local = w / kXcds;
+    if (G % kXcds == 0) {
+      start = x * (G / kXcds) + local;
+      nper = G;
+      mine = start < total ? (total - 1 - start) / G + 1 : 0;
+    } else {
+      nper = G / kXcds + (x < G % kXcds ? 1 : 0);
+      const int count = total / kXcds + (x < total % kXcds ? 1 : 0);
+      start = x * (total / kXcds) + min(x, total % kXcds) + local;
+      mine = local < count ? (count - local + nper - 1) / nper : 0;
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    mine = __builtin_amdgcn_readfirstlane(mine);
+  }
+
+  // This workgroup's t-th tile: row tiles in groups of 8, columns within.
+  __device__ __forceinline__ MxTile tile(int t) const {
+    int logical = start + nper * t;
+    MxTile r;
+    r.e = 0;
+    r.c0 = 0;
+    r.nc = p.chunks;
+    if constexpr (MODE == MX_K) {
+      r.e = logical / (tiles_m * tiles_n);
+      logical -= r.e * tiles_m * tiles_n;
+      r.c0 = __builtin_amdgcn_readfirstlane(tab.lo[r.e]);
+      r.nc = __builtin_amdgcn_readfirstlane(tab.hi[r.e]) - r.c0;
+    }
+    const int per = kGroupM * tiles_n, group = logical / per, first = group * kGroupM;
+    const int size = min(tiles_m - first, kGroupM), in = logical - group * per;
+    const int tm = first + in % size, tn = in / size;
+    if constexpr (MODE == MX_ROWS) {
+      int lo = 0, hi = p.groups;                 // e: before[e] <= tm < before[e + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__builtin_amdgcn_readfirstlane(tab.before[mid]) <= tm) lo = mid; else hi = mid;
+      }
+      r.e = lo;
+      r.m0 = __builtin_amdgcn_readfirstlane(tab.lo[lo]) + (int64_t)(tm - __builtin_amdgcn_readfirstlane(tab.before[lo])) * C::kBM;
+      r.m_end = min(r.m0 + C::kBM, (int64_t)__builtin_amdgcn_readfirstlane(tab.hi[lo]));
+    } else {
+      r.m0 = (int64_t)tm * C::kBM;
+      r.m_end = min(r.m0 + C::kBM, p.m);
+    }
+    r.n0 = (int64_t)tn * C::kBN;
+    return r;
+  }
+};
+
+// The loads: wave w brings rows 32 i + 8 w .. + 7 of either operand in round i
+// (lane l: row l / 8 of them, 16 bytes at physical slot l % 8, that is logical
+// slot (l % 8) ^ swz(row)), and 128 rows' scales: waves 0 and 1 of A, 2 and 3
+// of B. Raw buffer resources end with the operand: what lies past it reads as
+// zeros, dword by dword. After the last step the cursor stays where it is and
+// the loads repeat into a stage that nobody reads.
+template <int MODE, int TM, int TN>
+struct MxLoader {
+  using C = TileCfg<TM, TN>;
+  const MxGemmArgs& p;
+  const MxWalk<MODE, TM, TN>& wk;
+  const uint32_t smem;
+  const int wave;
+  uint32_t voff_a[C::kRoundsA], voff_b[C::kRoundsB], voff_s, step_s;
+  u32x4 rs_a, rs_b, rs_s;
+  int tk = 0, c = 0, nc = 0;
+
+  __device__ __forceinline__ MxLoader(const MxGemmArgs& p_, const MxWalk<MODE, TM, TN>& wk_, uint32_t smem_, int wave_,
+                                      int lane)
+      : p(p_), wk(wk_), smem(smem_), wave(wave_) {
+    const uint32_t row = 8 * wave + (lane >> 3);
+    const uint32_t g16 = (uint32_t)(((lane & 7) ^ (lane >> 3) ^ (wave & 1)) * 16);
+#pragma unroll
+    for (int i = 0; i < C::kRoundsA; ++i) voff_a[i] = (32 * i + row) * (uint32_t)p.lda + g16;
+#pragma unroll
+    for (int i = 0; i < C::kRoundsB; ++i) voff_b[i] = (32 * i + row) * (uint32_t)p.ldb + g16;
+    voff_s = (uint32_t)((wave & 1) * 128 + 2 * lane) * 8;
+    step_s = (uint32_t)(wave < 2 ? p.ldsa : p.ldsb) * 8;
+    while (tk < wk.mine && wk.tile(tk).nc == 0) ++tk;      // K groups without rows
+    open();
+  }
+  __device__ __forceinline__ void open() {
+    if (tk >= wk.mine) tk = 0;                             // nothing to load at all: nobody reads the stage
+    const MxTile t = wk.tile(tk);
+    nc = t.nc;
+    c = 0;
+    const uint8_t* b = p.b;
+    const uint8_t* sb = p.sb;
+    if constexpr (MODE == MX_ROWS) {
+      b += (int64_t)t.e * p.n * p.ldb;
+      sb += (int64_t)t.e * p.chunks * p.ldsb * 8;
+    }
+    const int64_t k0 = (int64_t)t.c0 * 128;
+    rs_a = make_rsrc(p.a + t.m0 * p.lda + k0, p.a + (p.m - 1) * p.lda + (int64_t)p.chunks * 128);
+    rs_b = make_rsrc(b + t.n0 * p.ldb + k0, b + (p.n - 1) * p.ldb + (int64_t)p.chunks * 128);
+    if (wave < 2)
+      rs_s = make_rsrc(p.sa + ((int64_t)t.c0 * p.ldsa + t.m0) * 8, p.sa + ((int64_t)(p.chunks - 1) * p.ldsa + p.m) * 8);
+    else
+      rs_s = make_rsrc(sb + ((int64_t)t.c0 * p.ldsb + t.n0) * 8, sb + ((int64_t)(p.chunks - 1) * p.ldsb + p.n) * 8);
+  }
+  __device__ __forceinline__ void advance() {
+    if (c + 1 < nc) {
+      ++c;
+      bump_rsrc(rs_a, 128);
+      bump_rsrc(rs_b, 128);
+      bump_rsrc(rs_s, step_s);
+      return;
+    }
+    int next = tk + 1;
+    if constexpr (MODE == MX_K) while (next < wk.mine && wk.tile(next).nc == 0) ++next;
+    if (next < wk.mine) {
+      tk = next;
+      open();
+    }
+  }
+  __device__ __forceinline__ void part(int q, int stage) const {
+    const uint32_t base = smem + (uint32_t)(stage * C::kStage);
+    if (q < C::kRoundsA) dma16_buf(rs_a, voff_a[q], base + (32 * q + 8 * wave) * 128);
+    else if (q < C::kRoundsA + C::kRoundsB)
+      dma16_buf(rs_b, voff_b[q - C::kRoundsA], base + C::kBOff + (32 * (q - C::kRoundsA) + 8 * wave) * 128);
+    else if ((wave & 1) * 128 < (wave < 2 ? C::kBM : C::kBN))
+      dma16_buf(rs_s, voff_s, base + (wave < 2 ? C::kSaOff : C::kSbOff) + (wave & 1) * 1024);
+  }
+};
+
+// Stores one 32 x 32 subtile (lane: row l % 32; register r: column
+// 8 (r / 4) + 4 (l / 32) + r % 4). vec: 16-byte aligned rows, the whole subtile
+// inside. bf16: v_permlane32_swap puts the two lane halves' four columns side
+// by side (16 bytes per lane), v_permlane16_swap then trades the second such
+// piece of rows 0 .. 15 for the first of rows 16 .. 31, so that a store
+// instruction writes 64 contiguous bytes of each of 16 rows; fp32 the same with
+// 16 bytes per register quad.
+template <bool F32>
+__device__ __forceinline__ void store_subtile(const MxGemmArgs& p, int64_t base, int64_t m0, int64_t m_end, int64_t n0,
+                                              const v16f& acc, bool vec, int lane) {
+  if (vec) {
+    const int l16 = lane & 15, g1 = (lane >> 4) & 1, h = lane >> 5;
+    if constexpr (F32) {
+      // quads q = 0 .. 3 at columns 8 q + 4 h. Swapping quads 2 u and 2 u + 1 between the 16-lane rows g1 = 0 and 1
+      // leaves rows 0 .. 15 in the first, 16 .. 31 in the second.
+      float* out = static_cast<float*>(p.out) + base;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 x, y;
+        uint32_t* xp = &x.x;
+        uint32_t* yp = &y.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[8 * u + i]),
+                                                          __float_as_uint(acc[8 * u + 4 + i]), false, false);
+          xp[i] = s[0];
+          yp[i] = s[1];
+        }
+        const int64_t col = n0 + 16 * u + 8 * g1 + 4 * h;
+        *reinterpret_cast<uint4*>(out + (m0 + l16) * p.ldo + col) = x;
+        *reinterpret_cast<uint4*>(out + (m0 + 16 + l16) * p.ldo + col) = y;
+      }
+    } else {
+      uint16_t* out = static_cast<uint16_t*>(p.out) + base;
+      uint32_t d[8];                                  // quad q: d[2 q], d[2 q + 1]
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bf16x2 v = __builtin_convertvector((f32x2){acc[2 * i], acc[2 * i + 1]}, bf16x2);
+        __builtin_memcpy(&d[i], &v, 4);
+      }
+      // lane half h: columns 8 h .. + 7 (from quads 0, 1) and 16 + 8 h .. + 7 (from quads 2, 3)
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const auto s = __builtin_amdgcn_permlane32_swap(d[i], d[2 + i], false, false);
+        a[i] = s[0];
+        a[2 + i] = s[1];
+        const auto t = __builtin_amdgcn_permlane32_swap(d[4 + i], d[6 + i], false, false);
+        b[i] = t[0];
+        b[2 + i] = t[1];
+      }
+      uint4 x, y;
+      uint32_t* xp = &x.x;
+      uint32_t* yp = &y.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const auto s = __builtin_amdgcn_permlane16_swap(a[i], b[i], false, false);
+        xp[i] = s[0];
+        yp[i] = s[1];
+      }
+      const int64_t col = n0 + 16 * g1 + 8 * h;
+      *reinterpret_cast<uint4*>(out + (m0 + l16) * p.ldo + col) = x;
+      *reinterpret_cast<uint4*>(out + (m0 + 16 + l16) * p.ldo + col) = y;
+    }
+    return;
+  }
+  const int64_t row = m0 + (lane & 31);
+  if (row >= m_end) return;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int64_t col = n0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+    if (col < p.n) {
+      if constexpr (F32) static_cast<float*>(p.out)[base + row * p.ldo + col] = acc[r];
+      else static_cast<uint16_t*>(p.out)[base + row * p.ldo + col] = bf16_bits(acc[r]);
+    }
+  }
+}
+
+template <int MODE, bool F32, int TM, int TN>
+__global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) {
+  using C = TileCfg<TM, TN>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * C::kStage];
+  __shared__ MxTables tab;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_m = wave & 1, wave_n = wave >> 1;
+  const int r32 = lane & 31, h = lane >> 5;
+
+  if constexpr (MODE != MX_DENSE) {
+    int64_t lo = 0, hi = 0;
+    if (tid < p.groups) group_range(p.row_off, tid, MODE == MX_ROWS ? p.m : (int64_t)p.chunks * 256, lo, hi);
+    tab.lo[tid] = (int)(MODE == MX_ROWS ? lo : lo / 256);
+    tab.hi[tid] = (int)(MODE == MX_ROWS ? hi : hi / 256);
+    if constexpr (MODE == MX_ROWS) {
+      const int mine = (int)((hi - lo + C::kBM - 1) / C::kBM);
+      int sum = mine;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(sum, d);
+        if (lane >= d) sum += v;
+      }
+      __shared__ int wsum[4];
+      if (lane == 63) wsum[wave] = sum;
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) sum += wsum[w];
+      tab.before[tid + 1] = sum;
+      if (tid == 0) tab.before[0] = 0;
+    }
+    __syncthreads();
+  }
+  const MxWalk<MODE, TM, TN> wk(p, tab);
+  if (wk.mine == 0) return;                                   // uniform
+  MxLoader<MODE, TM, TN> ld(p, wk, lds_addr(smem), wave, lane);
+
+  // LDS offset of this lane's codes of slice t in a 32-row subtile: logical slot 4 h + t
+  uint32_t off[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) off[t] = r32 * 128 + (((4 * h + t) ^ swz(r32)) * 16);
+  auto frag = [&](const uint8_t* base, int t) { return *reinterpret_cast<const v4i*>(base + off[t]); };
+  auto a_frag = [&](const uint8_t* st, int i, int t) { return frag(st + (wave_m * TM + i) * 32 * 128, t); };
+  auto b_frag = [&](const uint8_t* st, int j, int t) { return frag(st + C::kBOff + (wave_n * TN + j) * 32 * 128, t); };
+  auto a_scale = [&](const uint8_t* st, int i) {
+    return *reinterpret_cast<const int*>(st + C::kSaOff + ((wave_m * TM + i) * 32 + r32) * 8 + 4 * h);
+  };
+  auto b_scale = [&](const uint8_t* st, int j) {
+    return *reinterpret_cast<const int*>(st + C::kSbOff + ((wave_n * TN + j) * 32 + r32) * 8 + 4 * h);
+  };
+
+#pragma unroll
+  for (int q = 0; q < C::kParts; ++q) ld.part(q, 0);
+  ld.advance();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < C::kParts; ++q) ld.part(q, 1);
+  ld.advance();
+
+  v4i af[4][TM], bf[4][TN];
+  int ea[TM], eb[TN], ean[TM], ebn[TN];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) af[t][i] = a_frag(smem, i, t);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bf[t][j] = b_frag(smem, j, t);
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) ea[i] = a_scale(smem, i);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) eb[j] = b_scale(smem, j);
+  __builtin_amdgcn_s_waitcnt(0xC07F);                         // lgkmcnt(0)
+
+  v16f acc[TM][TN];
+  constexpr int kNT = TM * TN, kReads = TM + TN;
+  int s = 0;
+  auto step = [&](bool wait_loads) {
+    const uint8_t* st = smem + (s & 1) * C::kStage;
+    const uint8_t* nst = smem + ((s + 1) & 1) * C::kStage;
+    for_each_const([&](auto tc) {
+      constexpr int t = decltype(tc)::value / kNT, u = decltype(tc)::value % kNT;
+      constexpr int i = u / TN, j = u % TN;
+      mfma_slice<t>(acc[i][j], bf[t][j], af[t][i], eb[j], ea[i]);
+      // the fragments due in this slice, spread over its first MFMAs: slice 3 of this step (t = 0), else slice t - 1 of
+      // the next
+      constexpr int rs = (t + 3) & 3;
+      constexpr int kSpread = kNT / 2 < 1 ? 1 : kNT / 2;      // reads within the first half of the slice
+#pragma unroll
+      for (int q = 0; q < kReads; ++q) {
+        if (q * kSpread / kReads == u) {
+          const uint8_t* from = t == 0 ? st : nst;
+          if (q < TM) af[rs][q] = a_frag(from, q, rs);
+          else bf[rs][q - TM] = b_frag(from, q - TM, rs);
+        }
+      }
+      if constexpr (t == 0 && u == kNT - 1) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);                   // slice 3 has been read
+        if (wait_loads) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < TM; ++q) ean[q] = a_scale(nst, q);
+#pragma unroll
+        for (int q = 0; q < TN; ++q) ebn[q] = b_scale(nst, q);
+      }
+      // the cursor's loads over slices 1 and 2
+      if constexpr (t == 1 || t == 2) {
+        constexpr int at = (t - 1) * kNT + u;
+#pragma unroll
+        for (int q = 0; q < C::kParts; ++q)
+          if (q * (2 * kNT) / C::kParts == at) ld.part(q, s & 1);
+      }
+      if constexpr (t == 3 && u == 0) ld.advance();
+      __builtin_amdgcn_sched_barrier(0);
+    }, std::make_integer_sequence<int, 4 * kNT>{});
+#pragma unroll
+    for (int q = 0; q < TM; ++q) ea[q] = ean[q];
+#pragma unroll
+    for (int q = 0; q < TN; ++q) eb[q] = ebn[q];
+    ++s;
+  };
+
+#pragma clang loop unroll(disable)
+  for (int tk = 0; tk < wk.mine; ++tk) {
+    const MxTile cur = wk.tile(tk);
+    const int nc = cur.nc;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+#pragma clang loop unroll(disable)
+    for (int c = 0; c < nc; ++c) step(c != 0 || tk == 0);
+    mfma_results_ready();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the loads the next tile's first step reads
+    const MxTile done = wk.tile(tk);
+    const int el = lane_fresh();
+    const int64_t base = MODE == MX_K ? (int64_t)done.e * p.m * p.ldo : 0;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int64_t m0 = done.m0 + (wave_m * TM + i) * 32, n0 = done.n0 + (wave_n * TN + j) * 32;
+        asm volatile("" : "+a"(acc[i][j]));                   // read its registers here, not all 256 at once
+        store_subtile<F32>(p, base, m0, done.m_end, n0, acc[i][j], vec_ok && m0 + 32 <= done.m_end && n0 + 32 <= p.n, el);
+      }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");            // the repeated loads land before the LDS is released
+}
+
+template <int MODE, bool F32, int TM, int TN>
+hipError_t run_tile(const MxGemmArgs& p, hipStream_t st) {
+  using C = TileCfg<TM, TN>;
+  constexpr int kEsz = F32 ? 4 : 2;
+  const int64_t tm = (p.m + C::kBM - 1) / C::kBM + (MODE == MX_ROWS ? p.groups : 0);
+  const int64_t tiles = tm * ((p.n + C::kBN - 1) / C::kBN) * (MODE == MX_K ? p.groups : 1);
+  const int64_t cus = 256 * (C::kStage * 2 > 80 * 1024 ? 1 : 2);
+  const unsigned grid = (unsigned)(tiles < cus ? tiles : cus);
+  const int vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * kEsz % 16 == 0 && p.m * p.ldo * kEsz % 16 == 0;
+  mx_tile_kernel<MODE, F32, TM, TN><<<grid, 256, 0, st>>>(p, vec);
+  return hipGetLastError();
+}
+
 template <int MODE, bool F32>
 hipError_t run(const MxGemmArgs& p, hipStream_t st) {
+  if (p.m / (MODE == MX_ROWS ? p.groups : 1) > 64 && p.n > 64) return run_tile<MODE, F32, 4, 4>(p, st);
   constexpr int kWaves = 4;
   const unsigned mt = (unsigned)((p.m + 31) / 32) + (MODE == MX_ROWS ? (unsigned)p.groups : 0u);
   const dim3 grid((unsigned)((p.n + 31) / 32), mt, MODE == MX_K ? (unsigned)p.groups : 1u);
