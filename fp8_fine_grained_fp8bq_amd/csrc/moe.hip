@@ -12,131 +12,174 @@ namespace {
 // owns a contiguous piece of the flattened choices. Up to one piece it is one
 // launch; with more, a first launch writes each piece's histogram to the
 // workspace and every block of the second adds up what comes before it (at
-// most 256 x 256 counts from the cache, one expert per thread). Within a
-// block, wave w owns a contiguous quarter, walks it 64 choices at a time and
-// ranks equal experts by eight ballots over the expert's bits, so that the
-// order is that of the tokens whatever runs when.
+// most 256 x 256 counts from the cache; four threads per expert share them).
+// Within a block, wave w owns a contiguous sixteenth, walks it 64 choices at a
+// time (four loads in flight) and ranks equal experts by eight ballots over
+// the expert's bits, so that the order is that of the tokens whatever runs
+// when. Bound by latency: 2048 choices are a handful of dependent loads and
+// barriers.
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 256;
-constexpr int kPlanPiece = 2048;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanPiece = 4096;
 
 struct PlanArgs {
   const int32_t* idx;
   int tokens, topk;
   int64_t ldidx;
   int groups, pad, cap;
-  int piece;                         // choices per block
+  int piece;                         // choices per block, a multiple of 4096
   int32_t *counts, *row_off, *src, *pos, *ws;
 };
 
-__device__ __forceinline__ int choice(const PlanArgs& p, int i) {
-  const int t = i / p.topk;
-  const int e = p.idx[(int64_t)t * p.ldidx + (i - t * p.topk)];
-  return e >= 0 && e < p.groups ? e : -1;
+// Experts of choices i0 + 64 u + lane (u = 0 .. 3), -1 for dropped ones and past end.
+__device__ __forceinline__ void choices4(const PlanArgs& p, int i0, int end, int (&e)[4]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = i0 + 64 * u + lane;
+    e[u] = -1;
+    if (i < end) {
+      const int t = i / p.topk;
+      e[u] = p.ldidx == p.topk ? p.idx[i] : p.idx[(int64_t)t * p.ldidx + (i - t * p.topk)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) e[u] = e[u] >= 0 && e[u] < p.groups ? e[u] : -1;
 }
 
 __global__ __launch_bounds__(kPlanThreads) void moe_histogram_kernel(PlanArgs p) {
   __shared__ int hist[256];
-  hist[threadIdx.x] = 0;
+  const int t = threadIdx.x;
+  if (t < 256) hist[t] = 0;
   __syncthreads();
   const int total = p.tokens * p.topk;
   const int lo = blockIdx.x * p.piece, hi = min(lo + p.piece, total);
-  for (int i = lo + (int)threadIdx.x; i < hi; i += kPlanThreads) {
-    const int e = choice(p, i);
-    if (e >= 0) atomicAdd(&hist[e], 1);
+  for (int i0 = lo + (t >> 6) * 256; i0 < hi; i0 += kPlanWaves * 256) {
+    int e[4];
+    choices4(p, i0, hi, e);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e[u] >= 0) atomicAdd(&hist[e[u]], 1);
   }
   __syncthreads();
-  p.ws[blockIdx.x * 256 + threadIdx.x] = hist[threadIdx.x];
+  if (t < 256) p.ws[blockIdx.x * 256 + t] = hist[t];
 }
 
 __global__ __launch_bounds__(kPlanThreads) void moe_place_kernel(PlanArgs p) {
-  constexpr int kWaves = kPlanThreads / 64;
-  __shared__ int next[kWaves][256];       // next free row of (wave, expert)
-  __shared__ int scan[256];               // end of each expert's padded rows
+  __shared__ int next[kPlanWaves][256];   // choices of (wave, expert), then the next free row
+  __shared__ int sums[2][4][256];         // choices before this block and in all, by quarter of the blocks
+  __shared__ int ends[256];               // end of each expert's padded rows
   __shared__ int filled[256];             // end of its real rows
+  __shared__ int wtotal[4];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int total = p.tokens * p.topk;
   const int nb = gridDim.x, blk = blockIdx.x;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) next[w][t] = 0;
+  for (int w = 0; w < kPlanWaves / 4; ++w) next[w * 4 + (t >> 8)][t & 255] = 0;
+
+  // what the other blocks have
+  int before = 0, all = 0;
+  if (nb > 1) {
+#pragma unroll 8
+    for (int b = t >> 8; b < nb; b += 4) {
+      const int c = p.ws[b * 256 + (t & 255)];
+      before += b < blk ? c : 0;
+      all += c;
+    }
+    sums[0][t >> 8][t & 255] = before;
+    sums[1][t >> 8][t & 255] = all;
+  }
   __syncthreads();
 
   // this block's choices per wave and expert
   const int lo = blk * p.piece, hi = min(lo + p.piece, total);
-  const int part = p.piece / kWaves;
+  const int part = p.piece / kPlanWaves;
   const int wlo = lo + wave * part, whi = min(wlo + part, hi);
-  for (int i = wlo + lane; i < whi; i += 64) {
-    const int e = choice(p, i);
-    if (e >= 0) atomicAdd(&next[wave][e], 1);
+  int first_e[4] = {-1, -1, -1, -1};                 // the first 256 stay in registers
+  for (int i0 = wlo; i0 < whi; i0 += 256) {
+    int e[4];
+    choices4(p, i0, whi, e);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i0 == wlo) first_e[u] = e[u];
+      if (e[u] >= 0) atomicAdd(&next[wave][e[u]], 1);
+    }
   }
   __syncthreads();
 
-  // expert t: choices before this block, and in all
-  int before = 0, all = 0;
-  if (nb == 1) {
+  // thread e < 256: offsets of expert e, by a scan over the waves' 64 experts each
+  int padded = 0, scan = 0;
+  if (t < 256) {
+    if (nb > 1) {
+      before = sums[0][0][t] + sums[0][1][t] + sums[0][2][t] + sums[0][3][t];
+      all = sums[1][0][t] + sums[1][1][t] + sums[1][2][t] + sums[1][3][t];
+    } else {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) all += next[w][t];
-  } else {
-#pragma unroll 8
-    for (int b = 0; b < nb; ++b) {
-      const int c = p.ws[b * 256 + t];
-      before += b < blk ? c : 0;
-      all += c;
+      for (int w = 0; w < kPlanWaves; ++w) all += next[w][t];
     }
+    padded = (all + p.pad - 1) / p.pad * p.pad;
+    scan = padded;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(scan, d);
+      if (lane >= d) scan += v;
+    }
+    if (lane == 63) wtotal[wave] = scan;
   }
-  // padded offsets: exclusive scan over the experts
-  const int padded = (all + p.pad - 1) / p.pad * p.pad;
-  scan[t] = padded;
   __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const int v = t >= d ? scan[t - d] : 0;
-    __syncthreads();
-    scan[t] += v;
-    __syncthreads();
-  }
-  const int first = scan[t] - padded;
-  int at = first + before;
+  if (t < 256) {
+    for (int w = 0; w < wave; ++w) scan += wtotal[w];
+    const int first = scan - padded;
+    ends[t] = scan;
+    filled[t] = first + all;
+    int at = first + before;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int c = next[w][t];
-    next[w][t] = at;
-    at += c;
-  }
-  if (blk == 0) {
-    if (t < p.groups) {
-      p.counts[t] = all;
-      p.row_off[t] = first;
+    for (int w = 0; w < kPlanWaves; ++w) {
+      const int c = next[w][t];
+      next[w][t] = at;
+      at += c;
     }
-    if (t == 255) p.row_off[p.groups] = scan[255];
+    if (blk == 0) {
+      if (t < p.groups) {
+        p.counts[t] = all;
+        p.row_off[t] = first;
+      }
+      if (t == 255) p.row_off[p.groups] = scan;
+    }
   }
+  __syncthreads();
+
   // rows without a token: the padding of the experts dealt to this wave, and
   // this block's share of what lies behind the last expert
-  filled[t] = first + all;
-  __syncthreads();
-  for (int e = blk + nb * wave; e < p.groups; e += nb * kWaves)
-    for (int r = filled[e] + lane; r < scan[e]; r += 64) p.src[r] = -1;
-  for (int64_t r = (int64_t)scan[255] + blk * kPlanThreads + t; r < p.cap; r += (int64_t)nb * kPlanThreads) p.src[r] = -1;
+  for (int e = blk + nb * wave; e < p.groups; e += nb * kPlanWaves)
+    for (int r = filled[e] + lane; r < ends[e]; r += 64) p.src[r] = -1;
+  for (int64_t r = (int64_t)ends[255] + blk * kPlanThreads + t; r < p.cap; r += (int64_t)nb * kPlanThreads)
+    p.src[r] = FP8BQ_ROW_UNUSED;
 
   // places, in order
-  for (int i0 = wlo; i0 < whi; i0 += 64) {
-    const int i = i0 + lane;
-    const int e = i < whi ? choice(p, i) : -1;
-    uint64_t same = __ballot(e >= 0);
+  for (int i0 = wlo; i0 < whi; i0 += 256) {
+    int e4[4] = {first_e[0], first_e[1], first_e[2], first_e[3]};
+    if (i0 != wlo) choices4(p, i0, whi, e4);
 #pragma unroll
-    for (int bit = 0; bit < 8; ++bit) {
-      const uint64_t m = __ballot((e >> bit) & 1);
-      same &= ((e >> bit) & 1) ? m : ~m;
-    }
-    const uint64_t below = same & ((1ull << lane) - 1);
-    const int rank = __popcll(below);
-    int row = -1;
-    if (e >= 0) row = next[wave][e] + rank;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before the first of its kind adds
-    if (e >= 0 && below == 0) next[wave][e] += __popcll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (i < whi) {
-      p.pos[i] = row;
-      if (row >= 0) p.src[row] = i / p.topk;
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 64 * u + lane, e = e4[u];
+      uint64_t same = __ballot(e >= 0);
+#pragma unroll
+      for (int bit = 0; bit < 8; ++bit) {
+        const uint64_t m = __ballot((e >> bit) & 1);
+        same &= ((e >> bit) & 1) ? m : ~m;
+      }
+      const uint64_t below = same & ((1ull << lane) - 1);
+      int row = -1;
+      if (e >= 0) row = next[wave][e] + __popcll(below);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // every lane has read before the first of its kind adds
+      if (e >= 0 && below == 0) next[wave][e] += __popcll(same);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (i < whi) {
+        p.pos[i] = row;
+        if (row >= 0) p.src[row] = i / p.topk;
+      }
     }
   }
 }
@@ -149,7 +192,7 @@ hipError_t launch_moe_plan(const int32_t* idx, int tokens, int topk, int64_t ldi
   PlanArgs p{idx, tokens, topk, ldidx, groups, pad, cap, kPlanPiece, counts, row_off, src, pos, ws};
   const int total = tokens * topk;
   if ((total + kPlanPiece - 1) / kPlanPiece > kMoePlanMaxBlocks)
-    p.piece = ((total + kMoePlanMaxBlocks - 1) / kMoePlanMaxBlocks + 255) / 256 * 256;
+    p.piece = ((total + kMoePlanMaxBlocks - 1) / kMoePlanMaxBlocks + kPlanPiece - 1) / kPlanPiece * kPlanPiece;
   const int nb = (total + p.piece - 1) / p.piece;
   if (nb > 1) {
     moe_histogram_kernel<<<nb, kPlanThreads, 0, stream>>>(p);
@@ -198,12 +241,34 @@ __device__ __forceinline__ void seq_range(const MoeBalanceArgs& a, int s, int64_
   }
 }
 
-// Whether a token has a choice inside [0, experts) (all lanes of the wave).
-__device__ __forceinline__ bool is_real(const MoeBalanceArgs& a, int64_t t) {
-  bool any = false;
-  for (int j = threadIdx.x & 63; j < a.topk; j += 64) {
+// One token's row: lane l holds logits of experts l, l + 64, ... and choices l,
+// l + 64, ... (the first of them here, the rest where topk > 64). Loaded for two
+// tokens at a time, before anything is used.
+template <int T, int VPL>
+struct TokenRow {
+  float v[VPL];
+  int first;
+  __device__ __forceinline__ void load(const MoeBalanceArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 63;
+    first = lane < a.topk ? a.idx[t * a.ldidx + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      v[i] = lane + 64 * i < a.experts ? logit<T>(a.logits, t * a.ldl + lane + 64 * i) : 0.f;
+  }
+};
+
+// Whether a token has a choice inside [0, experts) (all lanes of the wave);
+// each such choice is given to count(e).
+template <class F>
+__device__ __forceinline__ bool real_token(const MoeBalanceArgs& a, int64_t t, int first, F&& count) {
+  bool any = first >= 0 && first < a.experts;
+  if (any) count(first);
+  for (int j = 64 + (threadIdx.x & 63); j < a.topk; j += 64) {
     const int e = a.idx[t * a.ldidx + j];
-    any |= e >= 0 && e < a.experts;
+    if (e >= 0 && e < a.experts) {
+      any = true;
+      count(e);
+    }
   }
   return __any(any);
 }
@@ -248,7 +313,7 @@ constexpr int kBalWaves = 4;
 // it need be for the tokens at hand.
 int balance_pieces(int64_t tokens, int64_t sequences) {
   int64_t c = 1024 / sequences;
-  const int64_t per = (tokens / sequences + 4 * kBalWaves - 1) / (4 * kBalWaves);
+  const int64_t per = (tokens / sequences + 2 * kBalWaves - 1) / (2 * kBalWaves);
   c = c < per ? c : per;
   return (int)(c < 1 ? 1 : c > 256 ? 256 : c);
 }
@@ -294,20 +359,21 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBala
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
   int real = 0;
-  for (int64_t t = t0 + wave; t < t1; t += kBalWaves) {
-    if (!is_real(a, t)) continue;
+  auto take = [&](TokenRow<T, VPL>& row, int64_t t) {
+    if (!real_token(a, t, row.first, [&](int e) { atomicAdd(&hist[e], 1); })) return;
     ++real;
-    for (int j = lane; j < a.topk; j += 64) {
-      const int e = a.idx[t * a.ldidx + j];
-      if (e >= 0 && e < a.experts) atomicAdd(&hist[e], 1);
-    }
-    float v[VPL], open[VPL];
+    float open[VPL];
+    probabilities<SIG, VPL>(row.v, open, a.experts);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      v[i] = lane + 64 * i < a.experts ? logit<T>(a.logits, t * a.ldl + lane + 64 * i) : 0.f;
-    probabilities<SIG, VPL>(v, open, a.experts);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] += v[i];
+    for (int i = 0; i < VPL; ++i) acc[i] += row.v[i];
+  };
+  for (int64_t t = t0 + wave; t < t1; t += 2 * kBalWaves) {
+    TokenRow<T, VPL> x, y;
+    x.load(a, t);
+    const bool two = t + kBalWaves < t1;             // uniform in the wave
+    if (two) y.load(a, t + kBalWaves);
+    take(x, t);
+    if (two) take(y, t + kBalWaves);
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) sums[wave][lane + 64 * i] = acc[i];
@@ -328,54 +394,84 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBala
   }
 }
 
-// One block per sequence adds up its pieces (256 threads over experts), writes
-// counts and real, and its loss; the last block to finish adds the sequences'
-// losses in order.
-__global__ __launch_bounds__(256) void balance_final_kernel(MoeBalanceArgs a, int pieces, void* ws, float* loss,
-                                                            int32_t* counts, int32_t* real_out) {
-  __shared__ double red[256];
-  __shared__ int last;
-  const int tid = threadIdx.x, s = blockIdx.x;
+// One block per sequence adds up its pieces: wave w takes pieces w, w + 16, ...
+// (a lane the experts l, l + 64, ...), the waves meet in LDS in their order. It
+// writes counts and real, and its loss; the last block to finish adds the
+// sequences' losses in order.
+constexpr int kFinalWaves = 16;
+__global__ __launch_bounds__(64 * kFinalWaves) void balance_final_kernel(MoeBalanceArgs a, int pieces, void* ws,
+                                                                         float* loss, int32_t* counts,
+                                                                         int32_t* real_out) {
+  __shared__ float psum[kFinalWaves][64];
+  __shared__ int csum[kFinalWaves][64];
+  __shared__ double red[64 * kFinalWaves];
+  __shared__ int last, nreal;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, s = blockIdx.x;
   const BalanceWs w = balance_ws(ws, a.experts, a.sequences, pieces);
   const int64_t row0 = (int64_t)s * pieces;
-  int real = 0;
-  for (int c = 0; c < pieces; ++c) real += w.real[row0 + c];
-  double dot = 0.0;
-  for (int e = tid; e < a.experts; e += 256) {
-    double p = 0.0;
-    int n = 0;
-#pragma unroll 8
-    for (int c = 0; c < pieces; ++c) {
-      p += (double)w.psum[(row0 + c) * a.experts + e];
-      n += w.cnt[(row0 + c) * a.experts + e];
-    }
-    counts[(int64_t)s * a.experts + e] = n;
-    dot += p * n;
-  }
-  red[tid] = dot;
+  if (tid == 0) nreal = 0;
   __syncthreads();
-  for (int d = 128; d >= 1; d >>= 1) {
-    if (tid < d) red[tid] += red[tid + d];
+  int real = 0;
+  for (int c = tid; c < pieces; c += 64 * kFinalWaves) real += w.real[row0 + c];
+  if (real) atomicAdd(&nreal, real);
+  double dot = 0.0;                                    // of expert e0 + lane, in wave 0
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    const int e = e0 + lane;
+    float p = 0.f;
+    int n = 0;
+    if (e < a.experts) {
+#pragma unroll 4
+      for (int c = wave; c < pieces; c += kFinalWaves) {
+        p += w.psum[(row0 + c) * a.experts + e];
+        n += w.cnt[(row0 + c) * a.experts + e];
+      }
+    }
+    psum[wave][lane] = p;
+    csum[wave][lane] = n;
+    __syncthreads();
+    if (wave == 0 && e < a.experts) {
+      double ps = 0.0;
+      int ns = 0;
+#pragma unroll
+      for (int v = 0; v < kFinalWaves; ++v) {
+        ps += (double)psum[v][lane];
+        ns += csum[v][lane];
+      }
+      counts[(int64_t)s * a.experts + e] = ns;
+      dot += ps * ns;
+    }
     __syncthreads();
   }
+  auto block_sum = [&](double v) {                     // in a fixed order; the sum in red[0]
+    red[tid] = v;
+    __syncthreads();
+    for (int d = 32 * kFinalWaves; d >= 1; d >>= 1) {
+      if (tid < d) red[tid] += red[tid + d];
+      __syncthreads();
+    }
+  };
+  if (wave == 0) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
+  }
   if (tid == 0) {
-    real_out[s] = real;
-    const double r = (double)real;
-    const double l = real ? red[0] * a.experts / ((double)a.topk * r * r) : 0.0;
-    __hip_atomic_store(&w.seq_loss[s], (float)l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == a.sequences - 1;
+    real_out[s] = nreal;
+    const double r = (double)nreal;
+    const double l = nreal ? dot * a.experts / ((double)a.topk * r * r) : 0.0;
+    if (a.sequences == 1) {
+      *loss = (float)(l * (double)a.coef);
+      last = 0;
+    } else {
+      __hip_atomic_store(&w.seq_loss[s], (float)l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == a.sequences - 1;
+    }
   }
   __syncthreads();
   if (!last) return;
   double sum = 0.0;
-  for (int i = tid; i < a.sequences; i += 256)
+  for (int i = tid; i < a.sequences; i += 64 * kFinalWaves)
     sum += (double)__hip_atomic_load(&w.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  red[tid] = sum;
-  __syncthreads();
-  for (int d = 128; d >= 1; d >>= 1) {
-    if (tid < d) red[tid] += red[tid + d];
-    __syncthreads();
-  }
+  block_sum(sum);
   if (tid == 0) *loss = (float)(red[0] * (double)a.coef / a.sequences);
 }
 
@@ -409,12 +505,10 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_grad_kernel(MoeBalance
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
     f[i] = lane + 64 * i < a.experts ? scale * counts[(int64_t)s * a.experts + lane + 64 * i] : 0.f;
-  for (int64_t t = t0 + wave; t < t1; t += kBalWaves) {
-    const bool ok = is_real(a, t);
-    float v[VPL], open[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      v[i] = lane + 64 * i < a.experts ? logit<T>(a.logits, t * a.ldl + lane + 64 * i) : 0.f;
+  auto take = [&](TokenRow<T, VPL>& row, int64_t t) {
+    const bool ok = real_token(a, t, row.first, [](int) {});
+    float (&v)[VPL] = row.v;
+    float open[VPL];
     probabilities<SIG, VPL>(v, open, a.experts);
     float dot = 0.f;
 #pragma unroll
@@ -426,6 +520,14 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_grad_kernel(MoeBalance
       if constexpr (SIG) d *= open[i];
       if (lane + 64 * i < a.experts) put<T>(dlogits, t * lddl + lane + 64 * i, ok ? d : 0.f);
     }
+  };
+  for (int64_t t = t0 + wave; t < t1; t += 2 * kBalWaves) {
+    TokenRow<T, VPL> x, y;
+    x.load(a, t);
+    const bool two = t + kBalWaves < t1;             // uniform in the wave
+    if (two) y.load(a, t + kBalWaves);
+    take(x, t);
+    if (two) take(y, t + kBalWaves);
   }
 }
 
@@ -434,7 +536,7 @@ hipError_t run_balance(const MoeBalanceArgs& a, float* loss, int32_t* counts, in
   const int pieces = balance_pieces(a.tokens, a.sequences);
   balance_partial_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences), 64 * kBalWaves, 0, st>>>(a, pieces, ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  balance_final_kernel<<<a.sequences, 256, 0, st>>>(a, pieces, ws, loss, counts, real);
+  balance_final_kernel<<<a.sequences, 64 * kFinalWaves, 0, st>>>(a, pieces, ws, loss, counts, real);
   return hipGetLastError();
 }
 template <int T, bool SIG, int VPL>

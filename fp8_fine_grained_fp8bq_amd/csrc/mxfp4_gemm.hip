@@ -11,6 +11,9 @@
 // first operand: lane l's sixteen results are row l % 32 of A and, register r,
 // column 8 (r / 4) + 4 (l / 32) + r % 4 of B.
 #include <utility>
+#ifdef MX_PROBE
+#include <cstdlib>
+#endif
 
 #include "gemm_kernels.h"
 #include "mxfp4.h"
@@ -126,19 +129,33 @@ __global__ __launch_bounds__(64 * WAVES) void mx_stream_kernel(MxGemmArgs p) {
   v16f acc;
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int c = c0 + wave; c < c1; c += WAVES) {
-    uint4 av[4], bv[4];
+  // two chunks' loads in flight per wave
+  struct Chunk { uint4 a[4], b[4]; int ea, eb; };
+  auto load = [&](Chunk& k, int c) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      bv[t] = *reinterpret_cast<const uint4*>(pb + (int64_t)c * 128 + t * 16);
-      av[t] = *reinterpret_cast<const uint4*>(pa + (int64_t)c * 128 + t * 16);
+      k.b[t] = *reinterpret_cast<const uint4*>(pb + (int64_t)c * 128 + t * 16);
+      k.a[t] = *reinterpret_cast<const uint4*>(pa + (int64_t)c * 128 + t * 16);
     }
-    const int ea = *reinterpret_cast<const int*>(psa + (int64_t)c * p.ldsa * 8);
-    const int eb = *reinterpret_cast<const int*>(psb + (int64_t)c * p.ldsb * 8);
-    acc = mfma<0>(bv[0], av[0], acc, eb, ea);
-    acc = mfma<1>(bv[1], av[1], acc, eb, ea);
-    acc = mfma<2>(bv[2], av[2], acc, eb, ea);
-    acc = mfma<3>(bv[3], av[3], acc, eb, ea);
+    k.ea = *reinterpret_cast<const int*>(psa + (int64_t)c * p.ldsa * 8);
+    k.eb = *reinterpret_cast<const int*>(psb + (int64_t)c * p.ldsb * 8);
+  };
+  auto use = [&](const Chunk& k) {
+    acc = mfma<0>(k.b[0], k.a[0], acc, k.eb, k.ea);
+    acc = mfma<1>(k.b[1], k.a[1], acc, k.eb, k.ea);
+    acc = mfma<2>(k.b[2], k.a[2], acc, k.eb, k.ea);
+    acc = mfma<3>(k.b[3], k.a[3], acc, k.eb, k.ea);
+  };
+  for (int c = c0 + wave; c < c1; c += 2 * WAVES) {
+    Chunk x, y;
+    load(x, c);
+    if (c + WAVES < c1) {                          // uniform
+      load(y, c + WAVES);
+      use(x);
+      use(y);
+    } else {
+      use(x);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) part[wave][i][lane] = acc[i];
@@ -354,6 +371,12 @@ struct MxLoader {
   }
 };
 
+// Waits until at most N of the wave's vector memory operations are left.
+template <int N>
+__device__ __forceinline__ void wait_loads_left() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+
 // Stores one 32 x 32 subtile (lane: row l % 32; register r: column
 // 8 (r / 4) + 4 (l / 32) + r % 4). vec: 16-byte aligned rows, the whole subtile
 // inside. bf16: v_permlane32_swap puts the two lane halves' four columns side
@@ -432,10 +455,10 @@ __device__ __forceinline__ void store_subtile(const MxGemmArgs& p, int64_t base,
   }
 }
 
-template <int MODE, bool F32, int TM, int TN>
+template <int MODE, bool F32, int TM, int TN, int NST>
 __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) {
   using C = TileCfg<TM, TN>;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * C::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NST * C::kStage];
   __shared__ MxTables tab;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -482,14 +505,29 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
     return *reinterpret_cast<const int*>(st + C::kSbOff + ((wave_n * TN + j) * 32 + r32) * 8 + 4 * h);
   };
 
+  // Loads a wave has in flight beyond the next step's when a step's barrier is
+  // reached; half the waves bring no scales of a small tile.
+  const bool scales = (wave & 1) * 128 < (wave < 2 ? C::kBM : C::kBN);
+  auto wait_next = [&] {
+    if constexpr (NST == 2) wait_loads_left<0>();
+    else if (scales) wait_loads_left<(NST - 2) * C::kParts>();
+    else wait_loads_left<(NST - 2) * (C::kParts - 1)>();
+  };
 #pragma unroll
-  for (int q = 0; q < C::kParts; ++q) ld.part(q, 0);
-  ld.advance();
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  for (int st = 0; st < NST; ++st) {
 #pragma unroll
-  for (int q = 0; q < C::kParts; ++q) ld.part(q, 1);
-  ld.advance();
+    for (int q = 0; q < C::kParts; ++q) ld.part(q, st);
+    ld.advance();
+    if (st == 0 && NST == 2) {
+      wait_loads_left<0>();
+      __syncthreads();
+    }
+  }
+  if constexpr (NST > 2) {
+    if (scales) wait_loads_left<(NST - 1) * C::kParts>();
+    else wait_loads_left<(NST - 1) * (C::kParts - 1)>();
+    __syncthreads();
+  }
 
   v4i af[4][TM], bf[4][TN];
   int ea[TM], eb[TN], ean[TM], ebn[TN];
@@ -508,10 +546,11 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
 
   v16f acc[TM][TN];
   constexpr int kNT = TM * TN, kReads = TM + TN;
-  int s = 0;
+  int cs = 0;                                                  // the step's stage
   auto step = [&](bool wait_loads) {
-    const uint8_t* st = smem + (s & 1) * C::kStage;
-    const uint8_t* nst = smem + ((s + 1) & 1) * C::kStage;
+    const int ns = cs + 1 < NST ? cs + 1 : 0;
+    const uint8_t* st = smem + cs * C::kStage;
+    const uint8_t* nst = smem + ns * C::kStage;
     for_each_const([&](auto tc) {
       constexpr int t = decltype(tc)::value / kNT, u = decltype(tc)::value % kNT;
       constexpr int i = u / TN, j = u % TN;
@@ -530,7 +569,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
       }
       if constexpr (t == 0 && u == kNT - 1) {
         __builtin_amdgcn_s_waitcnt(0xC07F);                   // slice 3 has been read
-        if (wait_loads) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (NST > 2 || wait_loads) wait_next();
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < TM; ++q) ean[q] = a_scale(nst, q);
@@ -542,7 +581,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
         constexpr int at = (t - 1) * kNT + u;
 #pragma unroll
         for (int q = 0; q < C::kParts; ++q)
-          if (q * (2 * kNT) / C::kParts == at) ld.part(q, s & 1);
+          if (q * (2 * kNT) / C::kParts == at) ld.part(q, cs);
       }
       if constexpr (t == 3 && u == 0) ld.advance();
       __builtin_amdgcn_sched_barrier(0);
@@ -551,7 +590,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
     for (int q = 0; q < TM; ++q) ea[q] = ean[q];
 #pragma unroll
     for (int q = 0; q < TN; ++q) eb[q] = ebn[q];
-    ++s;
+    cs = ns;
   };
 
 #pragma clang loop unroll(disable)
@@ -583,26 +622,84 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");            // the repeated loads land before the LDS is released
 }
 
-template <int MODE, bool F32, int TM, int TN>
+template <int MODE, bool F32, int TM, int TN, int NST>
 hipError_t run_tile(const MxGemmArgs& p, hipStream_t st) {
   using C = TileCfg<TM, TN>;
   constexpr int kEsz = F32 ? 4 : 2;
   const int64_t tm = (p.m + C::kBM - 1) / C::kBM + (MODE == MX_ROWS ? p.groups : 0);
   const int64_t tiles = tm * ((p.n + C::kBN - 1) / C::kBN) * (MODE == MX_K ? p.groups : 1);
-  const int64_t cus = 256 * (C::kStage * 2 > 80 * 1024 ? 1 : 2);
+  const int64_t cus = 256 * (160 * 1024 / (C::kStage * NST + (MODE == MX_DENSE ? 0 : 4096)));
   const unsigned grid = (unsigned)(tiles < cus ? tiles : cus);
   const int vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * kEsz % 16 == 0 && p.m * p.ldo * kEsz % 16 == 0;
-  mx_tile_kernel<MODE, F32, TM, TN><<<grid, 256, 0, st>>>(p, vec);
+  mx_tile_kernel<MODE, F32, TM, TN, NST><<<grid, 256, 0, st>>>(p, vec);
   return hipGetLastError();
+}
+
+// Which kernel. A product's time is close to rounds x (chunks x step + store)
+// + launch, where a round is one tile on each of the 256 CUs (several
+// workgroups of the small tilings share a CU; their steps then take turns).
+// Step and store times in units of 10 ns, from products of 1 x 2048 x 7168 to
+// 16384 x 18432 x 7168; a tile twice as large takes less than twice the step, as
+// long as there are enough of them. Measured (us, bf16 out):
+//                       stream   64x64  64x128 128x128 128x256 256x256
+//   1 x 2048 x 7168        6.6    11.8    14.2    17.5    26.0    37.7
+//   48 x 18432 x 7168     38.8    18.2    16.0    19.2    27.9    38.9
+//   2048 x 2048 x 2048    42.8    13.2    10.8    10.1    13.3    17.9
+//   4096 x 2048 x 7168   226.6    54.5    45.5    37.2    37.2    47.5
+//   4096 x 7168 x 2048   271.1    62.4    51.6    46.6    46.9    42.5
+//   16384 x 18432 x 7168 9062     2077    1573    1193    1129     956
+struct Tiling { int bm, bn, step, store; };
+constexpr Tiling kTilings[] = {{32, 32, 25, 0}, {64, 64, 33, 40}, {64, 128, 42, 70}, {128, 128, 57, 130},
+                               {128, 256, 100, 250}, {256, 256, 170, 500}};
+
+// The tiling with the least estimated time for `groups` products of rows x n x
+// chunks each (an expert's rows are taken as their average: only the device
+// knows the counts).
+int pick_tiling(int64_t groups, int64_t rows, int64_t n, int64_t chunks) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 6; ++i) {
+    const Tiling& t = kTilings[i];
+    const int64_t tiles = groups * ((rows + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
+    const double time = (double)((tiles + 255) / 256) * (double)(chunks * t.step + t.store);
+    if (i == 0 || time < least) {
+      best = i;
+      least = time;
+    }
+  }
+  return best;
 }
 
 template <int MODE, bool F32>
 hipError_t run(const MxGemmArgs& p, hipStream_t st) {
-  if (p.m / (MODE == MX_ROWS ? p.groups : 1) > 64 && p.n > 64) return run_tile<MODE, F32, 4, 4>(p, st);
-  constexpr int kWaves = 4;
+  // Experts: their rows (or chunks of K) as the average of what the buffers
+  // hold. Rows count half of that: a plan's buffer has room for every choice of
+  // every token, many of which may be other GPUs' experts, and too large a tile
+  // costs more than too small a one (8 experts with 57 .. 232 rows in a buffer
+  // of 2048, n = 2048, k = 7168: 20.8 us with 64 x 128, 33.5 with 128 x 128).
+  const int64_t g = MODE == MX_DENSE ? 1 : p.groups;
+  const int64_t rows = MODE == MX_ROWS ? (p.m + 2 * g - 1) / (2 * g) : p.m;
+  const int64_t chunks = MODE == MX_K ? (p.chunks + g - 1) / g : p.chunks;
+  int pick = pick_tiling(g, rows, p.n, chunks);
+  // one 128 x 128 tile per CU or less: a third stage hides more latency (1000 x
+  // 4096 x 7168: 22.6 against 25.9 us); with more, two workgroups per CU do
+  // better (4096 x 2048 x 7168: 37.2 against 40.7)
+  const bool deep = g * ((rows + 127) / 128) * ((p.n + 127) / 128) <= 256;
+#ifdef MX_PROBE
+  if (const char* f = getenv("MX_FORCE")) pick = atoi(f);
+  if (pick == 6) return run_tile<MODE, F32, 2, 4, 3>(p, st);
+  if (pick == 7) return run_tile<MODE, F32, 4, 2, 2>(p, st);
+#endif
+  switch (pick) {
+    case 1: return run_tile<MODE, F32, 1, 1, 3>(p, st);
+    case 2: return run_tile<MODE, F32, 1, 2, 3>(p, st);
+    case 3: return deep ? run_tile<MODE, F32, 2, 2, 3>(p, st) : run_tile<MODE, F32, 2, 2, 2>(p, st);
+    case 4: return run_tile<MODE, F32, 2, 4, 2>(p, st);
+    case 5: return run_tile<MODE, F32, 4, 4, 2>(p, st);
+  }
   const unsigned mt = (unsigned)((p.m + 31) / 32) + (MODE == MX_ROWS ? (unsigned)p.groups : 0u);
   const dim3 grid((unsigned)((p.n + 31) / 32), mt, MODE == MX_K ? (unsigned)p.groups : 1u);
-  mx_stream_kernel<MODE, F32, kWaves><<<grid, 64 * kWaves, 0, st>>>(p);
+  mx_stream_kernel<MODE, F32, 4><<<grid, 64 * 4, 0, st>>>(p);
   return hipGetLastError();
 }
 

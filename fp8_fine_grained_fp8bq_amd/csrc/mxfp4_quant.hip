@@ -97,12 +97,15 @@ constexpr int kXor1 = 0xB1, kXor2 = 0x4E;            // quad_perm [1,0,3,2], [2,
 constexpr int kRor4 = 0x124, kRor8 = 0x128;          // row_ror: rotate a row of 16 lanes
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// The source row of row r of the quantised matrix; ok = false for a zero row.
+// The source row of row r of the quantised matrix; ok = false for a zero row,
+// skip = true for one that the row form leaves alone.
 template <bool IDX>
-__device__ __forceinline__ int64_t source(const MxQuantArgs& p, int64_t r, bool& ok) {
+__device__ __forceinline__ int64_t source(const MxQuantArgs& p, int64_t r, bool& ok, bool& skip) {
   ok = r < p.rows;
+  skip = !ok;
   if constexpr (IDX) {
     const int32_t t = ok ? p.src[r] : -1;
+    skip = skip || t == FP8BQ_ROW_UNUSED;
     ok = t >= 0 && t < p.xrows;
     return ok ? t : 0;
   }
@@ -111,59 +114,73 @@ __device__ __forceinline__ int64_t source(const MxQuantArgs& p, int64_t r, bool&
 
 // Row form. 16 lanes take one 256-element chunk of a row, 16 elements each (32
 // contiguous bytes of bf16), so a tile is a pair of lanes and a lane's codes
-// are one 8-byte store; a block takes 16 rows of one chunk, the chunks of a row
-// run fastest over the grid. A lane pair's scale byte is shifted to its place
-// in the chunk's eight; OR over the lanes of each half row gives dwords.
+// are one 8-byte store; each lane takes the same place of two neighbouring
+// chunks, all loads before any arithmetic. A block takes 16 rows of a chunk
+// pair, the pairs of a row run fastest over the grid. A lane pair's scale byte
+// is shifted to its place in the chunk's eight; OR over the lanes of each half
+// row gives dwords.
 template <int T, bool NOSAT, bool IDX, bool VEC>
 __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks) {
   const int t = threadIdx.x, l16 = t & 15;
-  const int chunk = (int)(blockIdx.x % (unsigned)chunks);
-  const int64_t r = (int64_t)(blockIdx.x / (unsigned)chunks) * 16 + (t >> 4);
-  bool ok;
-  const int64_t xr = source<IDX>(p, r, ok);
+  const unsigned pairs = (unsigned)(chunks + 1) / 2;
+  const int chunk0 = 2 * (int)(blockIdx.x % pairs);
+  const int64_t r = (int64_t)(blockIdx.x / pairs) * 16 + (t >> 4);
+  bool ok, skip;
+  const int64_t xr = source<IDX>(p, r, ok, skip);
   constexpr int kDw = 16 * Elem<T>::kBytes / 4;
-  uint32_t w[kDw];
+  uint32_t w[2][kDw];
   const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
-  load_row<T, 16, VEC>(row, (int64_t)chunk * 256 + l16 * 16, p.cols, ok, w);
-  float v[16];
-  unpack<T>(w, v);
-  uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max2(amax, mx_mag(v[i]));
-  amax = max2(amax, dpp<kXor1>(amax));
-  const uint32_t byte = mx_scale_byte<NOSAT>(amax);
-  uint32_t sc = (l16 & 1) ? 0u : byte << (8 * ((l16 >> 1) & 3));
-  sc |= dpp<kXor2>(sc);
-  sc |= dpp<kRor4>(sc) & ((l16 & 7) < 4 ? 0u : 0xFFFFFFFFu);   // lane 4 (12) gathers lanes 0 .. 3 (8 .. 11)
-  if (r >= p.rows) return;
-  const uint2 codes = make_uint2(mx_codes8(v, byte), mx_codes8(v + 8, byte));
-  *reinterpret_cast<uint2*>(p.q + r * p.ldq + chunk * 128 + l16 * 8) = codes;
-  if ((l16 & 7) == 4) *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + r) * 8 + (l16 >> 3) * 4) = sc;
+  for (int u = 0; u < 2; ++u) load_row<T, 16, VEC>(row, (int64_t)(chunk0 + u) * 256 + l16 * 16, p.cols, ok, w[u]);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int chunk = chunk0 + u;
+    float v[16];
+    unpack<T>(w[u], v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = max2(amax, mx_mag(v[i]));
+    amax = max2(amax, dpp<kXor1>(amax));
+    const uint32_t byte = mx_scale_byte<NOSAT>(amax);
+    uint32_t sc = (l16 & 1) ? 0u : byte << (8 * ((l16 >> 1) & 3));
+    sc |= dpp<kXor2>(sc);
+    sc |= dpp<kRor4>(sc) & ((l16 & 7) < 4 ? 0u : 0xFFFFFFFFu);   // lane 4 (12) gathers lanes 0 .. 3 (8 .. 11)
+    if (skip || chunk >= chunks) continue;
+    const uint2 codes = make_uint2(mx_codes8(v, byte), mx_codes8(v + 8, byte));
+    *reinterpret_cast<uint2*>(p.q + r * p.ldq + chunk * 128 + l16 * 8) = codes;
+    if ((l16 & 7) == 4) *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + r) * 8 + (l16 >> 3) * 4) = sc;
+  }
 }
 
 // Column form, and (ROWS) the row form beside it from the same read. A block
 // stages 128 rows of 256 bytes (128 columns, 64 of fp32) in LDS; then thread
 // (column dword, row tile) walks 32 rows of its dword: consecutive lanes on
 // consecutive dwords, no bank conflict, 16 bytes of codes per column. The four
-// row tiles' scale bytes of a column meet in LDS for one 4-byte store. Blocks
-// run over the rows first, so that the 64-byte pieces of a column's codes
-// that neighbouring blocks write meet in the cache. The grid covers whole
-// 256-element chunks in both directions: what lies past the matrix is zeros.
+// row tiles' scale bytes of a column meet in LDS for one 4-byte store. The
+// grid covers whole 256 x 256 squares of the matrix (what lies past it is
+// zeros); the blocks of a square run on one XCD, one after the other, so that
+// the 64-byte pieces of code rows that they write meet as full lines in its L2.
+// The squares run over the rows first.
 template <int T, bool NOSAT, bool IDX, bool VEC, bool ROWS>
-__global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p) {
+__global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p, unsigned rsq, unsigned csq) {
   constexpr int kPer = 4 / Elem<T>::kBytes;             // elements per dword
   constexpr int kCols = 64 * kPer;
   constexpr int kLane = 4 * kPer;                       // elements of a lane's 16 bytes
   __shared__ uint32_t tile[128][64];
   __shared__ uint8_t scales[kCols][4];
   const int t = threadIdx.x, l16 = t & 15;
-  const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * kCols;
+  constexpr int kSub = 2 * 256 / kCols;                 // blocks of a square
+  const unsigned g = blockIdx.x / (8 * kSub), in = blockIdx.x % (8 * kSub);
+  const unsigned here = min(rsq * csq - 8 * g, 8u);     // squares of this group of (up to) eight, one per XCD
+  const unsigned sq = 8 * g + in % here, sub = in / here;
+  const int64_t r0 = (int64_t)(sq % rsq) * 256 + (sub & 1) * 128, c0 = (int64_t)(sq / rsq) * 256 + (sub >> 1) * kCols;
 
   uint32_t w[8][4];
+  bool skip[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     bool ok;
-    const int64_t xr = source<IDX>(p, r0 + i * 16 + (t >> 4), ok);
+    const int64_t xr = source<IDX>(p, r0 + i * 16 + (t >> 4), ok, skip[i]);
     const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
     load_row<T, kLane, VEC>(row, c0 + l16 * kLane, p.cols, ok, w[i]);
   }
@@ -197,14 +214,14 @@ __global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p) {
         uint32_t sc = byte << (8 * (l16 >> 2));
         sc |= dpp<kRor4>(sc);
         sc |= dpp<kRor8>(sc);
-        if (r < p.rows) {
+        if (!skip[i]) {
           *reinterpret_cast<uint32_t*>(p.q + r * p.ldq + c0 / 2 + l16 * 4) = code;
           if (l16 == 0) *reinterpret_cast<uint32_t*>(p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32) = sc;
         }
       } else {
         uint32_t sc = byte << (8 * (l16 >> 3));
         sc |= dpp<kRor8>(sc);
-        if (r < p.rows) {
+        if (!skip[i]) {
           *reinterpret_cast<uint16_t*>(p.q + r * p.ldq + c0 / 2 + l16 * 2) = (uint16_t)code;
           if (l16 == 0) *reinterpret_cast<uint16_t*>(p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32) = (uint16_t)sc;
         }
@@ -240,39 +257,51 @@ __global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p) {
         *reinterpret_cast<const uint32_t*>(scales[t]);
 }
 
-// Read-back: 16 lanes take a chunk of a row, 16 codes each.
+// Read-back: 32 lanes take a chunk of a row, 8 codes each, so that a wave's
+// stores of bf16 are contiguous; four rows per thread, all loads first.
 template <int T, bool VEC>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ q, int64_t rows, int64_t cols,
                                                          int64_t ldq, const uint8_t* __restrict__ s, int64_t lds,
                                                          typename Elem<T>::type* __restrict__ y, int64_t ldy,
                                                          int chunks) {
-  const int t = threadIdx.x, l16 = t & 15;
+  const int t = threadIdx.x, l32 = t & 31;
   const int chunk = (int)(blockIdx.x % (unsigned)chunks);
-  const int64_t r = (int64_t)(blockIdx.x / (unsigned)chunks) * 16 + (t >> 4);
-  const int64_t c = (int64_t)chunk * 256 + l16 * 16;
-  if (r >= rows || c >= cols) return;
-  const uint2 codes = *reinterpret_cast<const uint2*>(q + r * ldq + chunk * 128 + l16 * 8);
-  const float sc = mx_scale(s[((int64_t)chunk * lds + r) * 8 + (l16 >> 1)]);
-  typename Elem<T>::type o[16];
+  const int64_t r0 = (int64_t)(blockIdx.x / (unsigned)chunks) * 32 + (t >> 5);
+  const int64_t c = (int64_t)chunk * 256 + l32 * 8;
+  if (c >= cols) return;
+  uint32_t codes[4], byte[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t code = ((i < 8 ? codes.x : codes.y) >> (4 * (i & 7))) & 15u;
-    // E2M1 to fp32: exponent field 0 holds 0 and 0.5, else (1 + m / 2) * 2^(e - 1)
-    const uint32_t em = code & 7u;
-    const uint32_t mag = em >= 2 ? (em << 22) + (126u << 23) : (em ? 126u << 23 : 0u);
-    o[i] = Elem<T>::round(__uint_as_float(mag | ((code & 8u) << 28)) * sc);
+  for (int u = 0; u < 4; ++u) {
+    const int64_t r = min(r0 + 8 * u, rows - 1);
+    codes[u] = *reinterpret_cast<const uint32_t*>(q + r * ldq + chunk * 128 + l32 * 4);
+    byte[u] = s[((int64_t)chunk * lds + r) * 8 + (l32 >> 2)];
   }
-  auto* dst = y + r * ldy + c;
-  if (VEC && c + 16 <= cols) {
-    constexpr int kVecs = 16 * Elem<T>::kBytes / 16;
-    uint4 u[kVecs];
-    __builtin_memcpy(u, o, sizeof(u));
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4*>(dst)[i] = u[i];
-  } else {
+  for (int u = 0; u < 4; ++u) {
+    const int64_t r = r0 + 8 * u;
+    if (r >= rows) return;
+    const float sc = mx_scale(byte[u]);
+    typename Elem<T>::type o[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < cols) dst[i] = o[i];
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t code = (codes[u] >> (4 * i)) & 15u;
+      // E2M1 to fp32: exponent field 0 holds 0 and 0.5, else (1 + m / 2) * 2^(e - 1)
+      const uint32_t em = code & 7u;
+      const uint32_t mag = em >= 2 ? (em << 22) + (126u << 23) : (em ? 126u << 23 : 0u);
+      o[i] = Elem<T>::round(__uint_as_float(mag | ((code & 8u) << 28)) * sc);
+    }
+    auto* dst = y + r * ldy + c;
+    if (VEC && c + 8 <= cols) {
+      constexpr int kVecs = 8 * Elem<T>::kBytes / 16;
+      uint4 v[kVecs];
+      __builtin_memcpy(v, o, sizeof(v));
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4*>(dst)[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < cols) dst[i] = o[i];
+    }
   }
 }
 
@@ -281,11 +310,12 @@ hipError_t run_quant(const MxQuantArgs& a, hipStream_t st) {
   const int cchunks = (int)((a.cols + 255) / 256);
   if (a.qt) {
     constexpr int kCols = 64 * 4 / Elem<T>::kBytes;
-    const dim3 grid((unsigned)((a.rows + 255) / 256 * 2), (unsigned)(cchunks * (256 / kCols)));
-    if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, 256, 0, st>>>(a);
-    else mx_quant_cols_kernel<T, NOSAT, IDX, VEC, false><<<grid, 256, 0, st>>>(a);
+    const unsigned rsq = (unsigned)((a.rows + 255) / 256);
+    const unsigned grid = rsq * (unsigned)cchunks * (2 * 256 / kCols);
+    if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, 256, 0, st>>>(a, rsq, cchunks);
+    else mx_quant_cols_kernel<T, NOSAT, IDX, VEC, false><<<grid, 256, 0, st>>>(a, rsq, cchunks);
   } else {
-    const unsigned blocks = (unsigned)((a.rows + 15) / 16) * (unsigned)cchunks;
+    const unsigned blocks = (unsigned)((a.rows + 15) / 16) * (unsigned)((cchunks + 1) / 2);
     mx_quant_rows_kernel<T, NOSAT, IDX, VEC><<<blocks, 256, 0, st>>>(a, cchunks);
   }
   return hipGetLastError();
@@ -312,7 +342,7 @@ hipError_t run_dequant(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq
                        void* y, int64_t ldy, hipStream_t st) {
   using E = typename Elem<T>::type;
   const int chunks = (int)((cols + 255) / 256);
-  const unsigned blocks = (unsigned)((rows + 15) / 16) * (unsigned)chunks;
+  const unsigned blocks = (unsigned)((rows + 31) / 32) * (unsigned)chunks;
   E* out = static_cast<E*>(y);
   if (reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * Elem<T>::kBytes % 16 == 0)
     mx_dequant_kernel<T, true><<<blocks, 256, 0, st>>>(q, rows, cols, ldq, s, lds, out, ldy, chunks);

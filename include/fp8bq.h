@@ -444,8 +444,12 @@ int fp8bq_quant_mxfp4_1x32(const void* x, int xtype, int64_t rows, int64_t cols,
  * The same of rows picked by an index: row r of the quantised matrix
  * [rows, cols] is x[src[r]], x [xrows, cols]; a src[r] outside [0, xrows)
  * stands for a row of zeros. This is the dispatch of tokens to experts: src is
- * what fp8bq_moe_plan writes. src: device int32 [rows].
+ * what fp8bq_moe_plan writes. src: device int32 [rows]. Where src[r] is
+ * FP8BQ_ROW_UNUSED the row form leaves row r's codes and scales as they were (a
+ * plan's buffer has many such rows behind the last expert); the column form
+ * takes it for zeros like any other entry outside.
  */
+enum { FP8BQ_ROW_UNUSED = -2 };
 int fp8bq_dispatch_mxfp4_1x32(const void* x, int xtype, int64_t xrows, int64_t cols, int64_t ldx,
                               const int32_t* src, int64_t rows, void* q, int64_t ldq, void* s, int64_t lds,
                               void* qt, int64_t ldqt, void* st, int64_t ldst, int flags, void* stream);
@@ -528,9 +532,9 @@ int fp8bq_grouped_wgrad_mxfp4(int32_t groups, const int32_t* row_off, int64_t m,
  * pad      rows of each expert are padded to a multiple of it, 1 .. 1024.
  * counts   int32 [groups]: choices of each expert.
  * row_off  int32 [groups + 1]: offsets of the experts' padded rows.
- * src      int32 [cap]: token of each dispatched row, -1 for padding and for
- *          the rows behind the last expert. cap >= tokens * topk +
- *          groups * (pad - 1) always suffices, and is required.
+ * src      int32 [cap]: token of each dispatched row, -1 for padding,
+ *          FP8BQ_ROW_UNUSED for the rows behind the last expert. cap >=
+ *          tokens * topk + groups * (pad - 1) always suffices, and is required.
  * pos      int32 [tokens, topk] (contiguous): dispatched row of each choice,
  *          -1 for a dropped one.
  * workspace  FP8BQ_MOE_PLAN_WORKSPACE_BYTES of device memory, 4-byte aligned,

@@ -7,7 +7,8 @@ import numpy as np
 
 
 def plan(idx: np.ndarray, groups: int, pad: int, cap: int):
-    """(counts, row_off, src, pos) of idx [tokens, topk]; entries outside [0, groups) are dropped."""
+    """(counts, row_off, src, pos) of idx [tokens, topk]; entries outside [0, groups) are dropped. src is -1 for padding
+    and -2 behind the last group."""
     counts = [0] * groups
     for e in idx.flatten():
         if 0 <= e < groups:
@@ -16,6 +17,7 @@ def plan(idx: np.ndarray, groups: int, pad: int, cap: int):
     for c in counts:
         off.append(off[-1] + -(-c // pad) * pad)
     src = np.full(cap, -1, np.int32)
+    src[off[-1]:] = -2
     pos = np.full(idx.shape, -1, np.int32)
     free = list(off[:-1])
     for t in range(idx.shape[0]):

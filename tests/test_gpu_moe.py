@@ -50,7 +50,7 @@ def test_plan_of_strided_choices_and_many():
     order = np.argsort(flat, kind="stable")[:ok.sum()]
     assert np.array_equal(got[0].cpu().numpy(), np.bincount(flat, minlength=65)[:64])
     src = got[2].cpu().numpy()
-    assert np.array_equal(src[:len(order)], order // 8) and (src[len(order):] == -1).all()
+    assert np.array_equal(src[:len(order)], order // 8) and (src[len(order):] == fb.ROW_UNUSED).all()
     pos = got[3].cpu().numpy().flatten()
     assert np.array_equal(pos[order], np.arange(len(order))) and (pos[~ok.flatten()] == -1).all()
 

@@ -127,6 +127,28 @@ def test_dispatch(xrows, cols, rows, dtype):
     same(q, s, mxfp4.quantise(xs), "rows only")
 
 
+def test_dispatch_leaves_unused_rows():
+    """Rows marked unused keep their bytes in the row form and are zeros in the column form."""
+    import torch
+    x = matrix(22, 30, 300)
+    src = torch.tensor([3, -2, 29, -1, -2, -2], dtype=torch.int32, device="cuda")
+    xs = np.zeros((6, 300))
+    xs[0], xs[2] = f64(x)[3], f64(x)[29]
+    wq, ws = mxfp4.quantise(xs)
+    for both in (False, True):
+        q = torch.full((6, 256), 0xAB, dtype=torch.uint8, device="cuda")
+        s = torch.full((2, 6, 8), 0xCD, dtype=torch.uint8, device="cuda")
+        qt = torch.empty((300, 128), dtype=torch.uint8, device="cuda")
+        st = torch.empty((1, 300, 8), dtype=torch.uint8, device="cuda")
+        fb.fp8bq_dispatch_mxfp4_1x32(x.data_ptr(), fb.BF16, 30, 300, 300, src.data_ptr(), 6, q.data_ptr(), 256,
+                                     s.data_ptr(), 6, *((qt.data_ptr(), 128, st.data_ptr(), 300) if both else (None, 0, None, 0)),
+                                     0, torch.cuda.current_stream().cuda_stream)
+        used = [0, 2, 3]
+        assert np.array_equal(q[used].cpu().numpy(), wq[used]) and np.array_equal(s[:, used].cpu().numpy(), ws[:, used])
+        assert (q[[1, 4, 5]] == 0xAB).all() and (s[:, [1, 4, 5]] == 0xCD).all()
+    same(qt, st, mxfp4.quantise(xs.T), "columns")
+
+
 def test_outputs_stay_inside_their_buffers():
     """Larger leading dimensions through the C entry: nothing between the rows or behind the last is written."""
     import torch

@@ -71,7 +71,7 @@ def test_plan_by_hand():
     idx = np.array([[1, 0], [1, 5], [-1, 1]], np.int32)
     counts, off, src, pos = moe.plan(idx, 3, 2, 9)
     assert counts.tolist() == [1, 3, 0] and off.tolist() == [0, 2, 6, 6]
-    assert src.tolist() == [0, -1, 0, 1, 2, -1, -1, -1, -1] and pos.tolist() == [[2, 0], [3, -1], [-1, 4]]
+    assert src.tolist() == [0, -1, 0, 1, 2, -1, -2, -2, -2] and pos.tolist() == [[2, 0], [3, -1], [-1, 4]]
 
 
 def test_balance_by_hand():
