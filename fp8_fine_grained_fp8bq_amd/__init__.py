@@ -100,7 +100,7 @@ def lib() -> ctypes.CDLL:
         L.fp8bq_grouped_gemm_decode_noalloc.restype = ctypes.c_int
         mx = [vp, i64, vp, i64]                 # codes, ld, scales, ld
         L.fp8bq_quant_mxfp4_1x32.argtypes = [vp, i32, i64, i64, i64, *mx, *mx, i32, vp]
-        L.fp8bq_dispatch_mxfp4_1x32.argtypes = [vp, i32, i64, i64, i64, vp, i64, *mx, *mx, i32, vp]
+        L.fp8bq_dispatch_mxfp4_1x32.argtypes = [vp, i32, i64, i64, i64, vp, i64, *mx, *mx, i32, vp, vp]
         L.fp8bq_dequant_mxfp4_1x32.argtypes = [vp, i64, i64, i64, vp, i64, vp, i32, i64, vp]
         L.fp8bq_gemm_mxfp4.argtypes = [i64, i64, i64, *mx, *mx, vp, i32, i64, vp]
         L.fp8bq_grouped_gemm_mxfp4.argtypes = [ctypes.c_int32, vp, i64, i64, i64, *mx, *mx, vp, i32, i64, vp]
@@ -432,10 +432,10 @@ def fp8bq_quant_mxfp4_1x32(x, xtype, rows, cols, ldx, q, ldq, s, lds, qt, ldqt, 
 
 
 def fp8bq_dispatch_mxfp4_1x32(x, xtype, xrows, cols, ldx, src, rows, q, ldq, s, lds, qt, ldqt, st, ldst, flags=0,
-                              stream=0):
+                              workspace=None, stream=0):
     return _check("fp8bq_dispatch_mxfp4_1x32",
                   lib().fp8bq_dispatch_mxfp4_1x32(x, xtype, xrows, cols, ldx, src, rows, q, ldq, s, lds, qt, ldqt, st,
-                                                  ldst, flags, stream))
+                                                  ldst, flags, workspace, stream))
 
 
 def fp8bq_dequant_mxfp4_1x32(q, rows, cols, ldq, s, lds, y, ytype, ldy, stream=0):

@@ -220,15 +220,34 @@ __device__ __forceinline__ void put(void* base, int64_t i, float v) {
   else static_cast<_Float16*>(base)[i] = (_Float16)v;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// Sum and maximum over the wave, on every lane: DPP within 16-lane rows (lane
+// ^ 1, ^ 2, mirrored halves, mirrored rows), then swaps of whole rows; one or
+// two instructions a step and no LDS.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, F&& f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, [](float a, float b) { return a + b; }); }
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
+
+// e^x for x <= 0: 2^t of t = x log2(e), times 1 + what t's rounding left over
+// (which is up to |x| 2^-24 of the result).
+__device__ __forceinline__ float exp_neg(float x) {
+  const float t = x * 0x1.715476p+0f;
+  const float rest = __builtin_fmaf(x, 0x1.715476p+0f, -t) + x * 0x1.4ae0bep-26f;
+  const float r = __builtin_amdgcn_exp2f(t);
+  return t < -126.f ? 0.f : __builtin_fmaf(r, rest * 0x1.62e430p-1f, r);
 }
 
 // Tokens of sequence s, clamped into the batch; s == sequences: nothing here.
@@ -283,7 +302,7 @@ __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       // sigmoid and its complement from the same exponential, neither by subtraction
-      const float z = expf(-fabsf(v[i])), inv = 1.f / (1.f + z);
+      const float z = exp_neg(-fabsf(v[i])), inv = 1.f / (1.f + z);
       const float big = inv, small = z * inv;
       const bool in = lane + 64 * i < experts;
       open[i] = v[i] >= 0.f ? small : big;
@@ -297,7 +316,7 @@ __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL
     m = wave_max(m);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = lane + 64 * i < experts && m > -INFINITY ? expf(v[i] - m) : 0.f;
+      v[i] = lane + 64 * i < experts && m > -INFINITY ? exp_neg(v[i] - m) : 0.f;
       sum += v[i];
     }
   }
@@ -307,13 +326,14 @@ __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL
   for (int i = 0; i < VPL; ++i) v[i] *= inv;
 }
 
-constexpr int kBalWaves = 4;
+constexpr int kBalWaves = 16;     // of the forward kernel: few, large partial results
+constexpr int kGradWaves = 4;
 
-// Pieces a sequence is cut into: about 1024 blocks in all, none shorter than
-// it need be for the tokens at hand.
-int balance_pieces(int64_t tokens, int64_t sequences) {
-  int64_t c = 1024 / sequences;
-  const int64_t per = (tokens / sequences + 2 * kBalWaves - 1) / (2 * kBalWaves);
+// Pieces a sequence is cut into for blocks of `waves` waves: about 4096 waves
+// in all, at least two tokens each.
+int balance_pieces(int64_t tokens, int64_t sequences, int waves) {
+  int64_t c = 4096 / waves / sequences;
+  const int64_t per = (tokens / sequences + 2 * waves - 1) / (2 * waves);
   c = c < per ? c : per;
   return (int)(c < 1 ? 1 : c > 256 ? 256 : c);
 }
@@ -479,7 +499,7 @@ __global__ __launch_bounds__(64 * kFinalWaves) void balance_final_kernel(MoeBala
 // dloss * coef / S * experts * c / (topk * n^2) stay in registers. Block row
 // `sequences` clears the tokens outside every sequence.
 template <int T, bool SIG, int VPL>
-__global__ __launch_bounds__(64 * kBalWaves) void balance_grad_kernel(MoeBalanceArgs a, int pieces, const float* dloss,
+__global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanceArgs a, int pieces, const float* dloss,
                                                                       const int32_t* counts, const int32_t* real,
                                                                       void* dlogits, int64_t lddl) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -488,7 +508,7 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_grad_kernel(MoeBalance
     int64_t lo, hi, end;
     seq_range(a, 0, lo, end);
     seq_range(a, a.sequences - 1, end, hi);
-    for (int64_t t = (int64_t)blockIdx.x * kBalWaves + wave; t < a.tokens; t += (int64_t)pieces * kBalWaves) {
+    for (int64_t t = (int64_t)blockIdx.x * kGradWaves + wave; t < a.tokens; t += (int64_t)pieces * kGradWaves) {
       if (t >= lo && t < hi) continue;
       for (int e = lane; e < a.experts; e += 64) put<T>(dlogits, t * lddl + e, 0.f);
     }
@@ -521,19 +541,19 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_grad_kernel(MoeBalance
       if (lane + 64 * i < a.experts) put<T>(dlogits, t * lddl + lane + 64 * i, ok ? d : 0.f);
     }
   };
-  for (int64_t t = t0 + wave; t < t1; t += 2 * kBalWaves) {
+  for (int64_t t = t0 + wave; t < t1; t += 2 * kGradWaves) {
     TokenRow<T, VPL> x, y;
     x.load(a, t);
-    const bool two = t + kBalWaves < t1;             // uniform in the wave
-    if (two) y.load(a, t + kBalWaves);
+    const bool two = t + kGradWaves < t1;             // uniform in the wave
+    if (two) y.load(a, t + kGradWaves);
     take(x, t);
-    if (two) take(y, t + kBalWaves);
+    if (two) take(y, t + kGradWaves);
   }
 }
 
 template <int T, bool SIG, int VPL>
 hipError_t run_balance(const MoeBalanceArgs& a, float* loss, int32_t* counts, int32_t* real, void* ws, hipStream_t st) {
-  const int pieces = balance_pieces(a.tokens, a.sequences);
+  const int pieces = balance_pieces(a.tokens, a.sequences, kBalWaves);
   balance_partial_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences), 64 * kBalWaves, 0, st>>>(a, pieces, ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   balance_final_kernel<<<a.sequences, 64 * kFinalWaves, 0, st>>>(a, pieces, ws, loss, counts, real);
@@ -542,8 +562,8 @@ hipError_t run_balance(const MoeBalanceArgs& a, float* loss, int32_t* counts, in
 template <int T, bool SIG, int VPL>
 hipError_t run_grad(const MoeBalanceArgs& a, const float* dloss, const int32_t* counts, const int32_t* real,
                     void* dlogits, int64_t lddl, hipStream_t st) {
-  const int pieces = balance_pieces(a.tokens, a.sequences);
-  balance_grad_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences + 1), 64 * kBalWaves, 0, st>>>(a, pieces, dloss, counts,
+  const int pieces = balance_pieces(a.tokens, a.sequences, kGradWaves);
+  balance_grad_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences + 1), 64 * kGradWaves, 0, st>>>(a, pieces, dloss, counts,
                                                                                              real, dlogits, lddl);
   return hipGetLastError();
 }
@@ -580,7 +600,7 @@ struct Backward {
 }  // namespace
 
 int64_t moe_balance_workspace(int64_t tokens, int64_t experts, int64_t sequences) {
-  const int64_t rows = sequences * balance_pieces(tokens, sequences);
+  const int64_t rows = sequences * balance_pieces(tokens, sequences, kBalWaves);
   return 4 * (rows * (2 * experts + 1) + sequences + 1);
 }
 

@@ -9,8 +9,6 @@
 namespace fp8bq {
 namespace {
 
-typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
-
 template <int T> struct Elem;
 template <> struct Elem<FP8BQ_BF16> {
   using type = uint16_t;
@@ -45,18 +43,33 @@ template <> struct Elem<FP8BQ_FP32> {
   static __device__ __forceinline__ float round(float v) { return v; }
 };
 
-// The values of the dwords w (two 16-bit elements each, or one fp32).
+// fp32 magnitude bits of the largest magnitude in the dwords w (two 16-bit
+// elements each, or one fp32).
 template <int T, int N>
-__device__ __forceinline__ void unpack(const uint32_t* w, float (&v)[N]) {
+__device__ __forceinline__ uint32_t amax_of(const uint32_t (&w)[N]) {
+  uint32_t m = 0;
   if constexpr (T == FP8BQ_FP32) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < N; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    return m;
   } else {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      v[2 * i] = Elem<T>::value((uint16_t)(w[i] & 0xFFFFu));
-      v[2 * i + 1] = Elem<T>::value((uint16_t)(w[i] >> 16));
-    }
+    for (int i = 0; i < N; ++i) m = mx_max_pairs(m, w[i]);
+    return mx_mag16<T == FP8BQ_BF16>(max(m & 0xFFFFu, m >> 16));
+  }
+}
+// Codes of the P-th eight elements in the dwords w (the missing ones of a
+// shorter w are zeros).
+template <int T, int P, int N>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[N], uint32_t byte) {
+  if constexpr (T == FP8BQ_FP32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 8 * P + i < N ? __uint_as_float(w[8 * P + i < N ? 8 * P + i : 0]) : 0.f;
+    return mx_codes8(v, byte);
+  } else {
+    const uint32_t p[4] = {w[4 * P], w[4 * P + 1], w[4 * P + 2], w[4 * P + 3]};
+    return mx_codes8<T == FP8BQ_BF16>(p, byte);
   }
 }
 
@@ -112,60 +125,106 @@ __device__ __forceinline__ int64_t source(const MxQuantArgs& p, int64_t r, bool&
   return ok ? r : 0;
 }
 
+// Dispatch by links: a row that several experts get is read and quantised once.
+// next[r] chains the rows that show the same source row (head[t] the first),
+// in an order that varies from call to call and does not matter: every row of
+// a chain gets the same bytes. Rows of zeros are written right here.
+__global__ __launch_bounds__(256) void mx_unlink_kernel(int32_t* head, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) head[i] = -1;
+}
+__global__ __launch_bounds__(256) void mx_link_kernel(MxQuantArgs p, int chunks, int32_t* head, int32_t* next) {
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int32_t t = r < p.rows ? p.src[r] : FP8BQ_ROW_UNUSED;
+  const bool zero = t != FP8BQ_ROW_UNUSED && (t < 0 || t >= p.xrows);
+  if (t >= 0 && t < p.xrows) next[r] = atomicExch(&head[t], (int32_t)r);
+  for (uint64_t left = __ballot(zero); left; left &= left - 1) {
+    const int64_t row = r - lane + __ffsll((unsigned long long)left) - 1;
+    for (int i = lane; i < chunks * 8; i += 64) {
+      *reinterpret_cast<uint4*>(p.q + row * p.ldq + i * 16) = make_uint4(0, 0, 0, 0);
+      p.s[((int64_t)(i >> 3) * p.lds + row) * 8 + (i & 7)] = 0;
+    }
+  }
+}
+
 // Row form. 16 lanes take one 256-element chunk of a row, 16 elements each (32
 // contiguous bytes of bf16), so a tile is a pair of lanes and a lane's codes
 // are one 8-byte store; each lane takes the same place of two neighbouring
 // chunks, all loads before any arithmetic. A block takes 16 rows of a chunk
 // pair, the pairs of a row run fastest over the grid. A lane pair's scale byte
 // is shifted to its place in the chunk's eight; OR over the lanes of each half
-// row gives dwords.
-template <int T, bool NOSAT, bool IDX, bool VEC>
-__global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks) {
+// row gives dwords. LINK: rows of x, each written along its chain.
+template <int T, bool NOSAT, bool IDX, bool VEC, bool LINK = false>
+__global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks, const int32_t* head = nullptr,
+                                                            const int32_t* next = nullptr) {
   const int t = threadIdx.x, l16 = t & 15;
   const unsigned pairs = (unsigned)(chunks + 1) / 2;
   const int chunk0 = 2 * (int)(blockIdx.x % pairs);
   const int64_t r = (int64_t)(blockIdx.x / pairs) * 16 + (t >> 4);
   bool ok, skip;
-  const int64_t xr = source<IDX>(p, r, ok, skip);
+  int64_t xr;
+  int32_t at = -1;
+  if constexpr (LINK) {
+    at = r < p.xrows ? head[r] : -1;
+    ok = at >= 0;                                       // a row that nobody gets is not read
+    skip = !ok;
+    xr = ok ? r : 0;
+  } else {
+    xr = source<IDX>(p, r, ok, skip);
+  }
   constexpr int kDw = 16 * Elem<T>::kBytes / 4;
   uint32_t w[2][kDw];
+  uint2 codes[2];
+  uint32_t scs[2];
   const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
 #pragma unroll
   for (int u = 0; u < 2; ++u) load_row<T, 16, VEC>(row, (int64_t)(chunk0 + u) * 256 + l16 * 16, p.cols, ok, w[u]);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int chunk = chunk0 + u;
-    float v[16];
-    unpack<T>(w[u], v);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max2(amax, mx_mag(v[i]));
+    uint32_t amax = amax_of<T>(w[u]);
     amax = max2(amax, dpp<kXor1>(amax));
     const uint32_t byte = mx_scale_byte<NOSAT>(amax);
     uint32_t sc = (l16 & 1) ? 0u : byte << (8 * ((l16 >> 1) & 3));
     sc |= dpp<kXor2>(sc);
     sc |= dpp<kRor4>(sc) & ((l16 & 7) < 4 ? 0u : 0xFFFFFFFFu);   // lane 4 (12) gathers lanes 0 .. 3 (8 .. 11)
-    if (skip || chunk >= chunks) continue;
-    const uint2 codes = make_uint2(mx_codes8(v, byte), mx_codes8(v + 8, byte));
-    *reinterpret_cast<uint2*>(p.q + r * p.ldq + chunk * 128 + l16 * 8) = codes;
-    if ((l16 & 7) == 4) *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + r) * 8 + (l16 >> 3) * 4) = sc;
+    codes[u] = make_uint2(codes_of<T, 0>(w[u], byte), codes_of<T, 1>(w[u], byte));
+    scs[u] = sc;
   }
+  if (skip) return;
+  int64_t to = LINK ? at : r;
+  do {
+    const int64_t following = LINK ? next[to] : -1;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int chunk = chunk0 + u;
+      if (chunk >= chunks) break;
+      *reinterpret_cast<uint2*>(p.q + to * p.ldq + chunk * 128 + l16 * 8) = codes[u];
+      if ((l16 & 7) == 4)
+        *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + to) * 8 + (l16 >> 3) * 4) = scs[u];
+    }
+    to = following;
+  } while (to >= 0);
 }
 
 // Column form, and (ROWS) the row form beside it from the same read. A block
 // stages 128 rows of 256 bytes (128 columns, 64 of fp32) in LDS; then thread
-// (column dword, row tile) walks 32 rows of its dword: consecutive lanes on
-// consecutive dwords, no bank conflict, 16 bytes of codes per column. The four
+// (column dword, row tile, half of the dword) walks 32 rows of its dword:
+// consecutive lanes on consecutive dwords, no bank conflict, 16 bytes of codes
+// per thread. The four
 // row tiles' scale bytes of a column meet in LDS for one 4-byte store. The
 // grid covers whole 256 x 256 squares of the matrix (what lies past it is
 // zeros); the blocks of a square run on one XCD, one after the other, so that
 // the 64-byte pieces of code rows that they write meet as full lines in its L2.
-// The squares run over the rows first.
+// The squares run over the columns first.
+constexpr int kColsThreads = 512;
 template <int T, bool NOSAT, bool IDX, bool VEC, bool ROWS>
-__global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p, unsigned rsq, unsigned csq) {
+__global__ __launch_bounds__(kColsThreads) void mx_quant_cols_kernel(MxQuantArgs p, unsigned rsq, unsigned csq) {
   constexpr int kPer = 4 / Elem<T>::kBytes;             // elements per dword
   constexpr int kCols = 64 * kPer;
   constexpr int kLane = 4 * kPer;                       // elements of a lane's 16 bytes
+  constexpr int kRounds = 128 * 16 / kColsThreads;      // rows per thread of the load
+  constexpr int kStep = kColsThreads / 16;
   __shared__ uint32_t tile[128][64];
   __shared__ uint8_t scales[kCols][4];
   const int t = threadIdx.x, l16 = t & 15;
@@ -173,35 +232,27 @@ __global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p, unsig
   const unsigned g = blockIdx.x / (8 * kSub), in = blockIdx.x % (8 * kSub);
   const unsigned here = min(rsq * csq - 8 * g, 8u);     // squares of this group of (up to) eight, one per XCD
   const unsigned sq = 8 * g + in % here, sub = in / here;
-  const int64_t r0 = (int64_t)(sq % rsq) * 256 + (sub & 1) * 128, c0 = (int64_t)(sq / rsq) * 256 + (sub >> 1) * kCols;
+  const int64_t r0 = (int64_t)(sq / csq) * 256 + (sub & 1) * 128, c0 = (int64_t)(sq % csq) * 256 + (sub >> 1) * kCols;
 
-  uint32_t w[8][4];
-  bool skip[8];
+  uint32_t w[kRounds][4];
+  bool skip[kRounds];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kRounds; ++i) {
     bool ok;
-    const int64_t xr = source<IDX>(p, r0 + i * 16 + (t >> 4), ok, skip[i]);
+    const int64_t xr = source<IDX>(p, r0 + i * kStep + (t >> 4), ok, skip[i]);
     const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
     load_row<T, kLane, VEC>(row, c0 + l16 * kLane, p.cols, ok, w[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<uint4*>(&tile[i * 16 + (t >> 4)][l16 * 4]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+  for (int i = 0; i < kRounds; ++i)
+    *reinterpret_cast<uint4*>(&tile[i * kStep + (t >> 4)][l16 * 4]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
 
   if constexpr (ROWS) {
     // a tile is 4 lanes (8 of fp32)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = r0 + i * 16 + (t >> 4);
-      float v[8];
-      if constexpr (kPer == 1) v[4] = v[5] = v[6] = v[7] = 0.f;
-      float u[kLane];
-      unpack<T>(w[i], u);
-#pragma unroll
-      for (int j = 0; j < kLane; ++j) v[j] = u[j];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int j = 0; j < kLane; ++j) amax = max2(amax, mx_mag(v[j]));
+    for (int i = 0; i < kRounds; ++i) {
+      const int64_t r = r0 + i * kStep + (t >> 4);
+      uint32_t amax = amax_of<T>(w[i]);
       amax = max2(amax, dpp<kXor1>(amax));
       amax = max2(amax, dpp<kXor2>(amax));
       if constexpr (kPer == 1) {                        // lanes 0 .. 3 and 4 .. 7 of each half row
@@ -209,7 +260,7 @@ __global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p, unsig
         amax = max2(amax, (l16 & 4) ? a : b);
       }
       const uint32_t byte = mx_scale_byte<NOSAT>(amax);
-      const uint32_t code = mx_codes8(v, byte);
+      const uint32_t code = codes_of<T, 0>(w[i], byte);
       if constexpr (kPer == 2) {
         uint32_t sc = byte << (8 * (l16 >> 2));
         sc |= dpp<kRor4>(sc);
@@ -230,26 +281,26 @@ __global__ __launch_bounds__(256) void mx_quant_cols_kernel(MxQuantArgs p, unsig
   }
   __syncthreads();
 
-  const int cd = t & 63, rt = t >> 6;
-  uint32_t d[32];
+  const int cd = t & 63, rt = (t >> 6) & 3, h = t >> 8;
+  if (h < kPer) {
+    uint32_t d[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) d[i] = tile[rt * 32 + i][cd];
+    for (int i = 0; i < 32; ++i) d[i] = tile[rt * 32 + i][cd];
+    // the 32 rows of this dword's h-th column: fp32 as they are, 16-bit ones regrouped two rows to a dword
+    constexpr int kDw = 32 / kPer;
+    const uint32_t pick = h ? 0x07060302u : 0x05040100u;
+    uint32_t v[kDw];
 #pragma unroll
-  for (int h = 0; h < kPer; ++h) {
-    float v[32];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if constexpr (kPer == 1) v[i] = __uint_as_float(d[i]);
-      else v[i] = Elem<T>::value((uint16_t)(d[i] >> (16 * h)));
-      amax = max2(amax, mx_mag(v[i]));
+    for (int i = 0; i < kDw; ++i) {
+      if constexpr (kPer == 1) v[i] = d[i];
+      else v[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], pick);
     }
-    const uint32_t byte = mx_scale_byte<NOSAT>(amax);
+    const uint32_t byte = mx_scale_byte<NOSAT>(amax_of<T>(v));
     scales[cd * kPer + h][rt] = (uint8_t)byte;
     const int64_t c = c0 + cd * kPer + h;
     if (c < p.cols)
       *reinterpret_cast<uint4*>(p.qt + c * p.ldqt + r0 / 2 + rt * 16) =
-          make_uint4(mx_codes8(v, byte), mx_codes8(v + 8, byte), mx_codes8(v + 16, byte), mx_codes8(v + 24, byte));
+          make_uint4(codes_of<T, 0>(v, byte), codes_of<T, 1>(v, byte), codes_of<T, 2>(v, byte), codes_of<T, 3>(v, byte));
   }
   __syncthreads();
   if (t < kCols && c0 + t < p.cols)
@@ -306,14 +357,22 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restri
 }
 
 template <int T, bool NOSAT, bool IDX, bool VEC>
-hipError_t run_quant(const MxQuantArgs& a, hipStream_t st) {
+hipError_t run_quant(const MxQuantArgs& a, int32_t* links, hipStream_t st) {
   const int cchunks = (int)((a.cols + 255) / 256);
   if (a.qt) {
     constexpr int kCols = 64 * 4 / Elem<T>::kBytes;
     const unsigned rsq = (unsigned)((a.rows + 255) / 256);
     const unsigned grid = rsq * (unsigned)cchunks * (2 * 256 / kCols);
-    if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, 256, 0, st>>>(a, rsq, cchunks);
-    else mx_quant_cols_kernel<T, NOSAT, IDX, VEC, false><<<grid, 256, 0, st>>>(a, rsq, cchunks);
+    if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, kColsThreads, 0, st>>>(a, rsq, cchunks);
+    else mx_quant_cols_kernel<T, NOSAT, IDX, VEC, false><<<grid, kColsThreads, 0, st>>>(a, rsq, cchunks);
+  } else if (IDX && links) {
+    int32_t *head = links, *next = links + a.xrows;
+    mx_unlink_kernel<<<(unsigned)((a.xrows + 255) / 256), 256, 0, st>>>(head, a.xrows);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    mx_link_kernel<<<(unsigned)((a.rows + 255) / 256), 256, 0, st>>>(a, cchunks, head, next);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const unsigned blocks = (unsigned)((a.xrows + 15) / 16) * (unsigned)((cchunks + 1) / 2);
+    mx_quant_rows_kernel<T, NOSAT, IDX, VEC, true><<<blocks, 256, 0, st>>>(a, cchunks, head, next);
   } else {
     const unsigned blocks = (unsigned)((a.rows + 15) / 16) * (unsigned)((cchunks + 1) / 2);
     mx_quant_rows_kernel<T, NOSAT, IDX, VEC><<<blocks, 256, 0, st>>>(a, cchunks);
@@ -322,18 +381,18 @@ hipError_t run_quant(const MxQuantArgs& a, hipStream_t st) {
 }
 
 template <int T>
-hipError_t pick_quant(const MxQuantArgs& a, bool nosat, hipStream_t st) {
+hipError_t pick_quant(const MxQuantArgs& a, bool nosat, int32_t* links, hipStream_t st) {
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * Elem<T>::kBytes % 16 == 0;
   const int sel = (nosat ? 4 : 0) + (a.src ? 2 : 0) + (vec ? 1 : 0);
   switch (sel) {
-    case 0: return run_quant<T, false, false, false>(a, st);
-    case 1: return run_quant<T, false, false, true>(a, st);
-    case 2: return run_quant<T, false, true, false>(a, st);
-    case 3: return run_quant<T, false, true, true>(a, st);
-    case 4: return run_quant<T, true, false, false>(a, st);
-    case 5: return run_quant<T, true, false, true>(a, st);
-    case 6: return run_quant<T, true, true, false>(a, st);
-    default: return run_quant<T, true, true, true>(a, st);
+    case 0: return run_quant<T, false, false, false>(a, links, st);
+    case 1: return run_quant<T, false, false, true>(a, links, st);
+    case 2: return run_quant<T, false, true, false>(a, links, st);
+    case 3: return run_quant<T, false, true, true>(a, links, st);
+    case 4: return run_quant<T, true, false, false>(a, links, st);
+    case 5: return run_quant<T, true, false, true>(a, links, st);
+    case 6: return run_quant<T, true, true, false>(a, links, st);
+    default: return run_quant<T, true, true, true>(a, links, st);
   }
 }
 
@@ -353,11 +412,11 @@ hipError_t run_dequant(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq
 
 }  // namespace
 
-hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, hipStream_t stream) {
+hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, int32_t* links, hipStream_t stream) {
   switch (xtype) {
-    case FP8BQ_BF16: return pick_quant<FP8BQ_BF16>(a, nosat, stream);
-    case FP8BQ_FP16: return pick_quant<FP8BQ_FP16>(a, nosat, stream);
-    default: return pick_quant<FP8BQ_FP32>(a, nosat, stream);
+    case FP8BQ_BF16: return pick_quant<FP8BQ_BF16>(a, nosat, links, stream);
+    case FP8BQ_FP16: return pick_quant<FP8BQ_FP16>(a, nosat, links, stream);
+    default: return pick_quant<FP8BQ_FP32>(a, nosat, links, stream);
   }
 }
 

@@ -29,7 +29,7 @@ def expect(L, status, fn, args, **change):
 
 
 QUANT = [A16, 0, 70, 300, 300, A16, 256, S8, 70, A16, 128, S8, 300, 0, None]
-DISPATCH = [A16, 0, 40, 300, 300, O4, 70, A16, 256, S8, 70, A16, 128, S8, 300, 0, None]
+DISPATCH = [A16, 0, 40, 300, 300, O4, 70, A16, 256, S8, 70, A16, 128, S8, 300, 0, None, None]
 DEQUANT = [A16, 70, 300, 256, S8, 70, A16, 0, 300, None]
 GEMM = [70, 90, 300, A16, 256, S8, 70, A16, 256, S8, 90, A16, 0, 90, None]
 GROUPED = [4, O4] + GEMM
@@ -66,6 +66,7 @@ def test_quant_refusals(L, fn, ok):
         expect(L, fb.E_INVAL, fn, ok, a5=None)
         expect(L, fb.E_INVAL, fn, ok, a2=0)
         expect(L, fb.E_ALIGN, fn, ok, a5=O4 + 2)
+        expect(L, fb.E_ALIGN, fn, ok, a16=O4 + 2)
 
 
 def test_dequant_refusals(L):

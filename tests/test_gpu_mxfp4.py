@@ -127,6 +127,35 @@ def test_dispatch(xrows, cols, rows, dtype):
     same(q, s, mxfp4.quantise(xs), "rows only")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("nosat", [False, True])
+@pytest.mark.parametrize("xrows,cols,rows", [(1, 40, 2), (1, 7168, 300), (50, 300, 257), (33, 513, 1000)])
+def test_dispatch_with_a_workspace(xrows, cols, rows, dtype, nosat):
+    """Each source row read once (rows >= 2 xrows): the same codes; unused rows keep their bytes, twice over."""
+    import torch
+    x = matrix(23, xrows, cols, dtype)
+    rng = np.random.default_rng(4)
+    src = rng.integers(-2, xrows + 2, rows).astype(np.int32)
+    xs = np.where(((src >= 0) & (src < xrows))[:, None], f64(x)[np.clip(src, 0, xrows - 1)], 0.0)
+    wq, ws = mxfp4.quantise(xs, nosat)
+    unused = src == -2
+    chunks = ws.shape[0]
+    d = torch.from_numpy(src).cuda()
+    work = torch.full((xrows + rows + 1,), 77, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        q = torch.full((rows, chunks * 128 + 16), 0xAB, dtype=torch.uint8, device="cuda")
+        s = torch.full((chunks, rows + 1, 8), 0xCD, dtype=torch.uint8, device="cuda")
+        fb.fp8bq_dispatch_mxfp4_1x32(x.data_ptr(), fb.BF16 if dtype == "bfloat16" else fb.FP16 if dtype == "float16" else fb.FP32,
+                                     xrows, cols, cols, d.data_ptr(), rows, q.data_ptr(), q.shape[1], s.data_ptr(), rows + 1,
+                                     None, 0, None, 0, fb.MX_NOSAT if nosat else 0, work.data_ptr(),
+                                     torch.cuda.current_stream().cuda_stream)
+        gq, gs = q.cpu().numpy(), s.cpu().numpy()
+        assert np.array_equal(gq[~unused, :chunks * 128], wq[~unused]) and np.array_equal(gs[:, :rows][:, ~unused], ws[:, ~unused])
+        assert (gq[unused] == 0xAB).all() and (gq[:, chunks * 128:] == 0xAB).all()
+        assert (gs[:, rows] == 0xCD).all() and (gs[:, :rows][:, unused] == 0xCD).all()
+        assert int(work[-1]) == 77
+
+
 def test_dispatch_leaves_unused_rows():
     """Rows marked unused keep their bytes in the row form and are zeros in the column form."""
     import torch
@@ -142,7 +171,7 @@ def test_dispatch_leaves_unused_rows():
         st = torch.empty((1, 300, 8), dtype=torch.uint8, device="cuda")
         fb.fp8bq_dispatch_mxfp4_1x32(x.data_ptr(), fb.BF16, 30, 300, 300, src.data_ptr(), 6, q.data_ptr(), 256,
                                      s.data_ptr(), 6, *((qt.data_ptr(), 128, st.data_ptr(), 300) if both else (None, 0, None, 0)),
-                                     0, torch.cuda.current_stream().cuda_stream)
+                                     0, None, torch.cuda.current_stream().cuda_stream)
         used = [0, 2, 3]
         assert np.array_equal(q[used].cpu().numpy(), wq[used]) and np.array_equal(s[:, used].cpu().numpy(), ws[:, used])
         assert (q[[1, 4, 5]] == 0xAB).all() and (s[:, [1, 4, 5]] == 0xCD).all()
