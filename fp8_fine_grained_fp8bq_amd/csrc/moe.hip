@@ -207,17 +207,74 @@ hipError_t launch_moe_plan(const int32_t* idx, int tokens, int topk, int64_t ldi
 // ---------------------------------------------------------------------------
 namespace {
 
+template <int T> struct Logit { using type = uint16_t; };
+template <> struct Logit<FP8BQ_FP32> { using type = float; };
 template <int T>
-__device__ __forceinline__ float logit(const void* base, int64_t i) {
-  if constexpr (T == FP8BQ_FP32) return static_cast<const float*>(base)[i];
-  else if constexpr (T == FP8BQ_BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[i] << 16);
-  else return (float)static_cast<const _Float16*>(base)[i];
+__device__ __forceinline__ float logit_value(typename Logit<T>::type b) {
+  if constexpr (T == FP8BQ_FP32) {
+    return b;
+  } else if constexpr (T == FP8BQ_BF16) {
+    return __uint_as_float((uint32_t)b << 16);
+  } else {
+    _Float16 h;
+    __builtin_memcpy(&h, &b, 2);
+    return (float)h;
+  }
 }
 template <int T>
-__device__ __forceinline__ void put(void* base, int64_t i, float v) {
-  if constexpr (T == FP8BQ_FP32) static_cast<float*>(base)[i] = v;
-  else if constexpr (T == FP8BQ_BF16) static_cast<__bf16*>(base)[i] = (__bf16)v;
-  else static_cast<_Float16*>(base)[i] = (_Float16)v;
+__device__ __forceinline__ typename Logit<T>::type logit_round(float v) {
+  typename Logit<T>::type r;
+  if constexpr (T == FP8BQ_FP32) {
+    r = v;
+  } else if constexpr (T == FP8BQ_BF16) {
+    const __bf16 b = (__bf16)v;
+    __builtin_memcpy(&r, &b, 2);
+  } else {
+    const _Float16 h = (_Float16)v;
+    __builtin_memcpy(&r, &h, 2);
+  }
+  return r;
+}
+
+// Which experts a lane holds: VPL neighbours (PACK: the experts are a multiple
+// of VPL and rows are aligned, a lane moves them in one or a few wide accesses),
+// or every 64th.
+template <int VPL, bool PACK>
+__device__ __forceinline__ int expert_of(int lane, int i) { return PACK ? lane * VPL + i : lane + 64 * i; }
+
+template <int T, int VPL, bool PACK>
+__device__ __forceinline__ void load_logits(const void* base, int64_t row, int experts, float (&v)[VPL]) {
+  using E = typename Logit<T>::type;
+  const int lane = threadIdx.x & 63;
+  const E* p = static_cast<const E*>(base) + row;
+  E raw[VPL];
+  if constexpr (PACK) {
+    constexpr int kBytes = VPL * sizeof(E);
+    if (lane * VPL < experts) __builtin_memcpy(raw, __builtin_assume_aligned(p + lane * VPL, kBytes < 16 ? kBytes : 16), kBytes);
+    else __builtin_memset(raw, 0, kBytes);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) raw[i] = lane + 64 * i < experts ? p[lane + 64 * i] : (E)0;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] = logit_value<T>(raw[i]);
+}
+template <int T, int VPL, bool PACK>
+__device__ __forceinline__ void store_logits(void* base, int64_t row, int experts, const float (&v)[VPL]) {
+  using E = typename Logit<T>::type;
+  const int lane = threadIdx.x & 63;
+  E* p = static_cast<E*>(base) + row;
+  E raw[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) raw[i] = logit_round<T>(v[i]);
+  if constexpr (PACK) {
+    constexpr int kBytes = VPL * sizeof(E);
+    if (lane * VPL < experts) __builtin_memcpy(__builtin_assume_aligned(p + lane * VPL, kBytes < 16 ? kBytes : 16), raw, kBytes);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 64 * i < experts) p[lane + 64 * i] = raw[i];
+  }
 }
 
 // Sum and maximum over the wave, on every lane: DPP within 16-lane rows (lane
@@ -260,19 +317,17 @@ __device__ __forceinline__ void seq_range(const MoeBalanceArgs& a, int s, int64_
   }
 }
 
-// One token's row: lane l holds logits of experts l, l + 64, ... and choices l,
-// l + 64, ... (the first of them here, the rest where topk > 64). Loaded for two
-// tokens at a time, before anything is used.
-template <int T, int VPL>
+// One token's row: a lane's logits and its choices l, l + 64, ... (the first of
+// them here, the rest where topk > 64). Loaded for two tokens at a time,
+// before anything is used.
+template <int T, int VPL, bool PACK>
 struct TokenRow {
   float v[VPL];
   int first;
   __device__ __forceinline__ void load(const MoeBalanceArgs& a, int64_t t) {
     const int lane = threadIdx.x & 63;
     first = lane < a.topk ? a.idx[t * a.ldidx + lane] : -1;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      v[i] = lane + 64 * i < a.experts ? logit<T>(a.logits, t * a.ldl + lane + 64 * i) : 0.f;
+    load_logits<T, VPL, PACK>(a.logits, t * a.ldl, a.experts, v);
   }
 };
 
@@ -292,9 +347,8 @@ __device__ __forceinline__ bool real_token(const MoeBalanceArgs& a, int64_t t, i
   return __any(any);
 }
 
-// p of a token: lane l holds experts l, l + 64, .... v: logits in, p out;
-// open: 1 - sigmoid (SIGMOID).
-template <bool SIG, int VPL>
+// p of a token. v: logits in, p out; open: 1 - sigmoid (SIGMOID).
+template <bool SIG, int VPL, bool PACK>
 __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL], int experts) {
   const int lane = threadIdx.x & 63;
   float sum = 0.f;
@@ -304,7 +358,7 @@ __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL
       // sigmoid and its complement from the same exponential, neither by subtraction
       const float z = exp_neg(-fabsf(v[i])), inv = 1.f / (1.f + z);
       const float big = inv, small = z * inv;
-      const bool in = lane + 64 * i < experts;
+      const bool in = expert_of<VPL, PACK>(lane, i) < experts;
       open[i] = v[i] >= 0.f ? small : big;
       v[i] = in ? (v[i] >= 0.f ? big : small) : 0.f;
       sum += v[i];
@@ -312,11 +366,11 @@ __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL
   } else {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) m = fmaxf(m, lane + 64 * i < experts ? v[i] : -INFINITY);
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, expert_of<VPL, PACK>(lane, i) < experts ? v[i] : -INFINITY);
     m = wave_max(m);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = lane + 64 * i < experts && m > -INFINITY ? exp_neg(v[i] - m) : 0.f;
+      v[i] = expert_of<VPL, PACK>(lane, i) < experts && m > -INFINITY ? exp_neg(v[i] - m) : 0.f;
       sum += v[i];
     }
   }
@@ -339,13 +393,13 @@ int balance_pieces(int64_t tokens, int64_t sequences, int waves) {
 }
 
 // Workspace: per (sequence, piece): experts floats (sums of p), experts ints
-// (counts), one int (real tokens); then one float per sequence (its loss) and
-// the ticket.
+// (counts), one int (real tokens); then one float per (sequence, 64 experts),
+// its part of the loss, and the ticket.
 struct BalanceWs {
   float* psum;
   int32_t* cnt;
   int32_t* real;
-  float* seq_loss;
+  float* part;
   int32_t* ticket;
 };
 __host__ __device__ inline BalanceWs balance_ws(void* ws, int64_t experts, int64_t sequences, int64_t pieces) {
@@ -354,14 +408,14 @@ __host__ __device__ inline BalanceWs balance_ws(void* ws, int64_t experts, int64
   w.psum = static_cast<float*>(ws);
   w.cnt = reinterpret_cast<int32_t*>(w.psum + rows * experts);
   w.real = w.cnt + rows * experts;
-  w.seq_loss = reinterpret_cast<float*>(w.real + rows);
-  w.ticket = reinterpret_cast<int32_t*>(w.seq_loss + sequences);
+  w.part = reinterpret_cast<float*>(w.real + rows);
+  w.ticket = reinterpret_cast<int32_t*>(w.part + sequences * ((experts + 63) / 64));
   return w;
 }
 
-// Block (piece, sequence): a wave per token; lane l sums p of experts l, l + 64,
-// ... in registers, the waves meet in LDS.
-template <int T, bool SIG, int VPL>
+// Block (piece, sequence): a wave per token; a lane sums p of its experts in
+// registers, the waves meet in LDS.
+template <int T, bool SIG, int VPL, bool PACK>
 __global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBalanceArgs a, int pieces, void* ws) {
   __shared__ float sums[kBalWaves][VPL * 64];
   __shared__ int hist[VPL * 64];
@@ -379,16 +433,16 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBala
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
   int real = 0;
-  auto take = [&](TokenRow<T, VPL>& row, int64_t t) {
+  auto take = [&](TokenRow<T, VPL, PACK>& row, int64_t t) {
     if (!real_token(a, t, row.first, [&](int e) { atomicAdd(&hist[e], 1); })) return;
     ++real;
     float open[VPL];
-    probabilities<SIG, VPL>(row.v, open, a.experts);
+    probabilities<SIG, VPL, PACK>(row.v, open, a.experts);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] += row.v[i];
   };
   for (int64_t t = t0 + wave; t < t1; t += 2 * kBalWaves) {
-    TokenRow<T, VPL> x, y;
+    TokenRow<T, VPL, PACK> x, y;
     x.load(a, t);
     const bool two = t + kBalWaves < t1;             // uniform in the wave
     if (two) y.load(a, t + kBalWaves);
@@ -396,7 +450,7 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBala
     if (two) take(y, t + kBalWaves);
   }
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) sums[wave][lane + 64 * i] = acc[i];
+  for (int i = 0; i < VPL; ++i) sums[wave][expert_of<VPL, PACK>(lane, i)] = acc[i];
   if (lane == 0) reals[wave] = real;
   __syncthreads();
   const int64_t row = (int64_t)blockIdx.y * pieces + blockIdx.x;
@@ -414,91 +468,76 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_partial_kernel(MoeBala
   }
 }
 
-// One block per sequence adds up its pieces: wave w takes pieces w, w + 16, ...
-// (a lane the experts l, l + 64, ...), the waves meet in LDS in their order. It
-// writes counts and real, and its loss; the last block to finish adds the
-// sequences' losses in order.
+// Block (64 experts, sequence) adds up the pieces: wave w takes pieces w,
+// w + 16, ... (a lane an expert), the waves meet in LDS in their order. It
+// writes counts and real, and its part of the loss; the last block to finish
+// adds the parts in order.
 constexpr int kFinalWaves = 16;
 __global__ __launch_bounds__(64 * kFinalWaves) void balance_final_kernel(MoeBalanceArgs a, int pieces, void* ws,
                                                                          float* loss, int32_t* counts,
                                                                          int32_t* real_out) {
   __shared__ float psum[kFinalWaves][64];
-  __shared__ int csum[kFinalWaves][64];
+  __shared__ int csum[kFinalWaves][64], rsum[kFinalWaves];
   __shared__ double red[64 * kFinalWaves];
-  __shared__ int last, nreal;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, s = blockIdx.x;
+  __shared__ int last;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, s = blockIdx.y;
+  const int e = blockIdx.x * 64 + lane;
   const BalanceWs w = balance_ws(ws, a.experts, a.sequences, pieces);
   const int64_t row0 = (int64_t)s * pieces;
-  if (tid == 0) nreal = 0;
-  __syncthreads();
-  int real = 0;
-  for (int c = tid; c < pieces; c += 64 * kFinalWaves) real += w.real[row0 + c];
-  if (real) atomicAdd(&nreal, real);
-  double dot = 0.0;                                    // of expert e0 + lane, in wave 0
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    const int e = e0 + lane;
-    float p = 0.f;
-    int n = 0;
-    if (e < a.experts) {
+  float p = 0.f;
+  int n = 0, real = 0;
 #pragma unroll 4
-      for (int c = wave; c < pieces; c += kFinalWaves) {
-        p += w.psum[(row0 + c) * a.experts + e];
-        n += w.cnt[(row0 + c) * a.experts + e];
-      }
+  for (int c = wave; c < pieces; c += kFinalWaves) {
+    if (e < a.experts) {
+      p += w.psum[(row0 + c) * a.experts + e];
+      n += w.cnt[(row0 + c) * a.experts + e];
     }
-    psum[wave][lane] = p;
-    csum[wave][lane] = n;
-    __syncthreads();
-    if (wave == 0 && e < a.experts) {
-      double ps = 0.0;
-      int ns = 0;
-#pragma unroll
-      for (int v = 0; v < kFinalWaves; ++v) {
-        ps += (double)psum[v][lane];
-        ns += csum[v][lane];
-      }
-      counts[(int64_t)s * a.experts + e] = ns;
-      dot += ps * ns;
-    }
-    __syncthreads();
+    real += w.real[row0 + c];                          // the same on every lane
   }
-  auto block_sum = [&](double v) {                     // in a fixed order; the sum in red[0]
-    red[tid] = v;
-    __syncthreads();
-    for (int d = 32 * kFinalWaves; d >= 1; d >>= 1) {
-      if (tid < d) red[tid] += red[tid + d];
-      __syncthreads();
-    }
-  };
+  psum[wave][lane] = p;
+  csum[wave][lane] = n;
+  if (lane == 0) rsum[wave] = real;
+  __syncthreads();
   if (wave == 0) {
+    double ps = 0.0;
+    int ns = 0, rs = 0;
+#pragma unroll
+    for (int v = 0; v < kFinalWaves; ++v) {
+      ps += (double)psum[v][lane];
+      ns += csum[v][lane];
+      rs += rsum[v];
+    }
+    if (e < a.experts) counts[(int64_t)s * a.experts + e] = ns;
+    double dot = ps * ns;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) dot += __shfl_xor(dot, d);
-  }
-  if (tid == 0) {
-    real_out[s] = nreal;
-    const double r = (double)nreal;
-    const double l = nreal ? dot * a.experts / ((double)a.topk * r * r) : 0.0;
-    if (a.sequences == 1) {
-      *loss = (float)(l * (double)a.coef);
-      last = 0;
-    } else {
-      __hip_atomic_store(&w.seq_loss[s], (float)l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = __hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == a.sequences - 1;
+    if (lane == 0) {
+      if (blockIdx.x == 0) real_out[s] = rs;
+      const double part = rs ? dot * a.experts / ((double)a.topk * rs * rs) : 0.0;
+      __hip_atomic_store(&w.part[(int64_t)s * gridDim.x + blockIdx.x], (float)part, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+      const int blocks = (int)(gridDim.x * gridDim.y);
+      last = __hip_atomic_fetch_add(w.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == blocks - 1;
     }
   }
   __syncthreads();
   if (!last) return;
   double sum = 0.0;
-  for (int i = tid; i < a.sequences; i += 64 * kFinalWaves)
-    sum += (double)__hip_atomic_load(&w.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  block_sum(sum);
+  for (int i = tid; i < (int)(gridDim.x * gridDim.y); i += 64 * kFinalWaves)
+    sum += (double)__hip_atomic_load(&w.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  red[tid] = sum;
+  __syncthreads();
+  for (int d = 32 * kFinalWaves; d >= 1; d >>= 1) {
+    if (tid < d) red[tid] += red[tid + d];
+    __syncthreads();
+  }
   if (tid == 0) *loss = (float)(red[0] * (double)a.coef / a.sequences);
 }
 
 // Gradient. Block (piece, sequence), a wave per token; the lane's coefficients
 // dloss * coef / S * experts * c / (topk * n^2) stay in registers. Block row
 // `sequences` clears the tokens outside every sequence.
-template <int T, bool SIG, int VPL>
+template <int T, bool SIG, int VPL, bool PACK>
 __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanceArgs a, int pieces, const float* dloss,
                                                                       const int32_t* counts, const int32_t* real,
                                                                       void* dlogits, int64_t lddl) {
@@ -510,7 +549,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanc
     seq_range(a, a.sequences - 1, end, hi);
     for (int64_t t = (int64_t)blockIdx.x * kGradWaves + wave; t < a.tokens; t += (int64_t)pieces * kGradWaves) {
       if (t >= lo && t < hi) continue;
-      for (int e = lane; e < a.experts; e += 64) put<T>(dlogits, t * lddl + e, 0.f);
+      const float zero[VPL] = {};
+      store_logits<T, VPL, PACK>(dlogits, t * lddl, a.experts, zero);
     }
     return;
   }
@@ -524,12 +564,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanc
   float f[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    f[i] = lane + 64 * i < a.experts ? scale * counts[(int64_t)s * a.experts + lane + 64 * i] : 0.f;
-  auto take = [&](TokenRow<T, VPL>& row, int64_t t) {
+    f[i] = expert_of<VPL, PACK>(lane, i) < a.experts
+               ? scale * counts[(int64_t)s * a.experts + expert_of<VPL, PACK>(lane, i)] : 0.f;
+  auto take = [&](TokenRow<T, VPL, PACK>& row, int64_t t) {
     const bool ok = real_token(a, t, row.first, [](int) {});
     float (&v)[VPL] = row.v;
     float open[VPL];
-    probabilities<SIG, VPL>(v, open, a.experts);
+    probabilities<SIG, VPL, PACK>(v, open, a.experts);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) dot += v[i] * f[i];
@@ -538,11 +579,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanc
     for (int i = 0; i < VPL; ++i) {
       float d = v[i] * (f[i] - dot);
       if constexpr (SIG) d *= open[i];
-      if (lane + 64 * i < a.experts) put<T>(dlogits, t * lddl + lane + 64 * i, ok ? d : 0.f);
+      v[i] = ok ? d : 0.f;
     }
+    store_logits<T, VPL, PACK>(dlogits, t * lddl, a.experts, v);
   };
   for (int64_t t = t0 + wave; t < t1; t += 2 * kGradWaves) {
-    TokenRow<T, VPL> x, y;
+    TokenRow<T, VPL, PACK> x, y;
     x.load(a, t);
     const bool two = t + kGradWaves < t1;             // uniform in the wave
     if (two) y.load(a, t + kGradWaves);
@@ -551,49 +593,65 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanc
   }
 }
 
-template <int T, bool SIG, int VPL>
+template <int T, bool SIG, int VPL, bool PACK>
 hipError_t run_balance(const MoeBalanceArgs& a, float* loss, int32_t* counts, int32_t* real, void* ws, hipStream_t st) {
   const int pieces = balance_pieces(a.tokens, a.sequences, kBalWaves);
-  balance_partial_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences), 64 * kBalWaves, 0, st>>>(a, pieces, ws);
+  balance_partial_kernel<T, SIG, VPL, PACK><<<dim3(pieces, a.sequences), 64 * kBalWaves, 0, st>>>(a, pieces, ws);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  balance_final_kernel<<<a.sequences, 64 * kFinalWaves, 0, st>>>(a, pieces, ws, loss, counts, real);
+  balance_final_kernel<<<dim3((a.experts + 63) / 64, a.sequences), 64 * kFinalWaves, 0, st>>>(a, pieces, ws, loss, counts, real);
   return hipGetLastError();
 }
-template <int T, bool SIG, int VPL>
+template <int T, bool SIG, int VPL, bool PACK>
 hipError_t run_grad(const MoeBalanceArgs& a, const float* dloss, const int32_t* counts, const int32_t* real,
                     void* dlogits, int64_t lddl, hipStream_t st) {
   const int pieces = balance_pieces(a.tokens, a.sequences, kGradWaves);
-  balance_grad_kernel<T, SIG, VPL><<<dim3(pieces, a.sequences + 1), 64 * kGradWaves, 0, st>>>(a, pieces, dloss, counts,
+  balance_grad_kernel<T, SIG, VPL, PACK><<<dim3(pieces, a.sequences + 1), 64 * kGradWaves, 0, st>>>(a, pieces, dloss, counts,
                                                                                              real, dlogits, lddl);
   return hipGetLastError();
 }
 
-// f<T, SIG, VPL>() for the call's type, score and experts per lane.
+// f<T, SIG, VPL, PACK>() for the call's type, score, experts per lane and alignment.
+template <int T, bool SIG, int VPL, class F>
+hipError_t by_layout(const MoeBalanceArgs& a, const void* also, int64_t also_ld, F&& f) {
+  constexpr int kBytes = VPL * (T == FP8BQ_FP32 ? 4 : 2), kAlign = kBytes < 16 ? kBytes : 16;
+  constexpr int64_t kElem = T == FP8BQ_FP32 ? 4 : 2;
+  if constexpr (VPL > 1) {
+    if (a.experts % VPL == 0 && reinterpret_cast<uintptr_t>(a.logits) % kAlign == 0 && a.ldl * kElem % kAlign == 0 &&
+        reinterpret_cast<uintptr_t>(also) % kAlign == 0 && also_ld * kElem % kAlign == 0)
+      return f.template operator()<T, SIG, VPL, true>();
+  }
+  return f.template operator()<T, SIG, VPL, false>();
+}
 template <int T, bool SIG, class F>
-hipError_t by_width(int experts, F&& f) {
-  if (experts <= 64) return f.template operator()<T, SIG, 1>();
-  if (experts <= 128) return f.template operator()<T, SIG, 2>();
-  if (experts <= 256) return f.template operator()<T, SIG, 4>();
-  if (experts <= 512) return f.template operator()<T, SIG, 8>();
-  return f.template operator()<T, SIG, 16>();
+hipError_t by_width(const MoeBalanceArgs& a, const void* also, int64_t also_ld, F&& f) {
+  if (a.experts <= 64) return by_layout<T, SIG, 1>(a, also, also_ld, f);
+  if (a.experts <= 128) return by_layout<T, SIG, 2>(a, also, also_ld, f);
+  if (a.experts <= 256) return by_layout<T, SIG, 4>(a, also, also_ld, f);
+  if (a.experts <= 512) return by_layout<T, SIG, 8>(a, also, also_ld, f);
+  return by_layout<T, SIG, 16>(a, also, also_ld, f);
 }
 template <class F>
-hipError_t by_kind(int ltype, bool sigmoid, int experts, F&& f) {
+hipError_t by_kind(const MoeBalanceArgs& a, int ltype, bool sigmoid, const void* also, int64_t also_ld, F&& f) {
   switch (ltype) {
-    case FP8BQ_BF16: return sigmoid ? by_width<FP8BQ_BF16, true>(experts, f) : by_width<FP8BQ_BF16, false>(experts, f);
-    case FP8BQ_FP16: return sigmoid ? by_width<FP8BQ_FP16, true>(experts, f) : by_width<FP8BQ_FP16, false>(experts, f);
-    default: return sigmoid ? by_width<FP8BQ_FP32, true>(experts, f) : by_width<FP8BQ_FP32, false>(experts, f);
+    case FP8BQ_BF16:
+      return sigmoid ? by_width<FP8BQ_BF16, true>(a, also, also_ld, f) : by_width<FP8BQ_BF16, false>(a, also, also_ld, f);
+    case FP8BQ_FP16:
+      return sigmoid ? by_width<FP8BQ_FP16, true>(a, also, also_ld, f) : by_width<FP8BQ_FP16, false>(a, also, also_ld, f);
+    default:
+      return sigmoid ? by_width<FP8BQ_FP32, true>(a, also, also_ld, f) : by_width<FP8BQ_FP32, false>(a, also, also_ld, f);
   }
 }
 struct Forward {
   const MoeBalanceArgs& a; float* loss; int32_t* counts; int32_t* real; void* ws; hipStream_t st;
-  template <int T, bool SIG, int VPL> hipError_t operator()() { return run_balance<T, SIG, VPL>(a, loss, counts, real, ws, st); }
+  template <int T, bool SIG, int VPL, bool PACK> hipError_t operator()() {
+    return run_balance<T, SIG, VPL, PACK>(a, loss, counts, real, ws, st);
+  }
 };
 struct Backward {
   const MoeBalanceArgs& a; const float* dloss; const int32_t* counts; const int32_t* real; void* dlogits; int64_t lddl;
   hipStream_t st;
-  template <int T, bool SIG, int VPL> hipError_t operator()() {
-    return run_grad<T, SIG, VPL>(a, dloss, counts, real, dlogits, lddl, st);
+  template <int T, bool SIG, int VPL, bool PACK> hipError_t operator()() {
+    return run_grad<T, SIG, VPL, PACK>(a, dloss, counts, real, dlogits, lddl, st);
   }
 };
 
@@ -601,18 +659,18 @@ struct Backward {
 
 int64_t moe_balance_workspace(int64_t tokens, int64_t experts, int64_t sequences) {
   const int64_t rows = sequences * balance_pieces(tokens, sequences, kBalWaves);
-  return 4 * (rows * (2 * experts + 1) + sequences + 1);
+  return 4 * (rows * (2 * experts + 1) + sequences * ((experts + 63) / 64) + 1);
 }
 
 hipError_t launch_moe_balance(const MoeBalanceArgs& a, int ltype, bool sigmoid, float* loss, int32_t* counts,
                               int32_t* real, void* ws, hipStream_t stream) {
-  return by_kind(ltype, sigmoid, a.experts, Forward{a, loss, counts, real, ws, stream});
+  return by_kind(a, ltype, sigmoid, nullptr, 0, Forward{a, loss, counts, real, ws, stream});
 }
 
 hipError_t launch_moe_balance_grad(const MoeBalanceArgs& a, int ltype, bool sigmoid, const float* dloss,
                                    const int32_t* counts, const int32_t* real, void* dlogits, int64_t lddl,
                                    hipStream_t stream) {
-  return by_kind(ltype, sigmoid, a.experts, Backward{a, dloss, counts, real, dlogits, lddl, stream});
+  return by_kind(a, ltype, sigmoid, dlogits, lddl, Backward{a, dloss, counts, real, dlogits, lddl, stream});
 }
 
 }  // namespace fp8bq
