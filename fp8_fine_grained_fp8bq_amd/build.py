@@ -1,20 +1,24 @@
-"""Builds libfp8bq.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Builds libfp8bq.so (HIP kernels + C ABI) for gfx950 with hipcc, and the tensor
+layer's extension module _tensors.so with g++, in-tree.
 
 Usage: python -m fp8_fine_grained_fp8bq_amd.build   (or call build()).
 """
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp8bq.so")
 PROBE_LIB = os.path.join(PKG, "libfp8bq_probe.so")
+TENSORS_LIB = os.path.join(PKG, "_tensors.so")
 
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "gemm_quant.hip", "gemm_grouped.hip", "gemm_decode.hip",
            "api_mxfp4.cpp", "mxfp4_quant.hip", "mxfp4_gemm.hip", "moe.hip"]
@@ -38,10 +42,21 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
+def tensors_command(out: str) -> list:
+    """The g++ line of the extension module: host code over torch's headers, linked
+    to libfp8bq.so beside it."""
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wno-deprecated-declarations",
+            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include",
+            "-I/opt/rocm/include", f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(ROOT, 'include')}",
+            os.path.join(CSRC, "torch_tensors.cpp"), "-o", out, f"-L{PKG}", "-l:libfp8bq.so", f"-L{torch}/lib", "-lc10",
+            "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source into libfp8bq.so and the probes into
-    libfp8bq_probe.so (always recompiles). The sources compile in parallel to
-    objects, which are then linked."""
+    libfp8bq_probe.so, then the extension module (always recompiles). The sources
+    compile in parallel to objects, which are then linked."""
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
     compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
@@ -71,6 +86,14 @@ def build(verbose: bool = False) -> str:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError(f"hipcc link failed with exit code {res.returncode}")
         os.replace(tmp, lib)
+    cmd = tensors_command(TENSORS_LIB + ".tmp")
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"g++ failed on torch_tensors.cpp with exit code {res.returncode}")
+    os.replace(TENSORS_LIB + ".tmp", TENSORS_LIB)
     return LIB
 
 
