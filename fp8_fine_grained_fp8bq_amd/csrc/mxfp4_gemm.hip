@@ -187,8 +187,14 @@ __global__ __launch_bounds__(64 * WAVES) void mx_stream_kernel(MxGemmArgs p) {
 // next, so that every LDS read has a slice or more to land:
 //   slice 0: reads slice 3 of this step, then the one barrier of the step
 //            (every wave has read all of this stage, the other one has landed);
-//   slices 1 .. 3: read slices 0 .. 2 of the next step, and slice 1 on issues
-//            the loads of the step after it into this step's stage.
+//   slices 1 .. 3: read slices 0 .. 2 of the next step, and send the loads of
+//            NST steps on into this step's stage, spread evenly.
+// Eight waves of half the tile each (two per SIMD, half the accumulators) took
+// the same time: the step of 64 MFMAs (2048 cycles) takes 2280 without its 68
+// loads of 1 KB and 2630 .. 2700 with them, whichever way they are spread, at a
+// clock of 1.6 .. 1.7 GHz that the power budget sets (with all-zero codes the
+// same kernel runs 25% faster; MFMAs alone on random codes reach 6.8 of the
+// nominal 9.9 PFLOP/s at 1.7 GHz).
 // The accumulators sit in the AGPRs (256 of them at TM = TN = 4), tied to the
 // MFMA statements as in the power-of-two FP8 kernel.
 // ---------------------------------------------------------------------------
@@ -205,21 +211,32 @@ struct TileCfg {
   static constexpr int kParts = kRoundsA + kRoundsB + 1;
 };
 
-// acc += over slice T; the hazard wait states as mfma_scaled of the FP8 kernels.
+// acc += over slice T. The compiler does not see the instruction's hazards: an
+// operand that a VALU instruction has just written needs two wait states.
+// Fragments come from LDS reads (waited for by the compiler); the exponents
+// and the cleared accumulators come from VALU moves, which exponents_ready()
+// follows. (A wait before every MFMA instead costs 2 .. 3%: 987 against 970 us on
+// 16384 x 18432 x 7168.) tests/test_mfma_hazards.py checks the built code.
 template <int T>
 __device__ __forceinline__ void mfma_slice(v16f& acc, const v4i& b, const v4i& a, int sb, int sa) {
   if constexpr (T == 0)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
                  : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
   else if constexpr (T == 1)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
                  : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
   else if constexpr (T == 2)
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
                  : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
   else
-    asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
                  : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+}
+
+__device__ __forceinline__ void exponents_ready() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 3" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 struct MxTile {
@@ -518,16 +535,10 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
 #pragma unroll
     for (int q = 0; q < C::kParts; ++q) ld.part(q, st);
     ld.advance();
-    if (st == 0 && NST == 2) {
-      wait_loads_left<0>();
-      __syncthreads();
-    }
   }
-  if constexpr (NST > 2) {
-    if (scales) wait_loads_left<(NST - 1) * C::kParts>();
-    else wait_loads_left<(NST - 1) * (C::kParts - 1)>();
-    __syncthreads();
-  }
+  if (scales) wait_loads_left<(NST - 1) * C::kParts>();
+  else wait_loads_left<(NST - 1) * (C::kParts - 1)>();
+  __syncthreads();
 
   v4i af[4][TM], bf[4][TN];
   int ea[TM], eb[TN], ean[TM], ebn[TN];
@@ -576,20 +587,21 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
 #pragma unroll
         for (int q = 0; q < TN; ++q) ebn[q] = b_scale(nst, q);
       }
-      // the cursor's loads over slices 1 and 2
-      if constexpr (t == 1 || t == 2) {
-        constexpr int at = (t - 1) * kNT + u;
+      // the cursor's loads over slices 1 .. 3
+      if constexpr (t >= 1) {
+        constexpr int at = (t - 1) * kNT + u, slots = 3 * kNT;
 #pragma unroll
         for (int q = 0; q < C::kParts; ++q)
-          if (q * (2 * kNT) / C::kParts == at) ld.part(q, cs);
+          if (q * slots / C::kParts == at) ld.part(q, cs);
       }
-      if constexpr (t == 3 && u == 0) ld.advance();
+      if constexpr (t == 3 && u == kNT - 1) ld.advance();
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, 4 * kNT>{});
 #pragma unroll
     for (int q = 0; q < TM; ++q) ea[q] = ean[q];
 #pragma unroll
     for (int q = 0; q < TN; ++q) eb[q] = ebn[q];
+    exponents_ready();
     cs = ns;
   };
 
@@ -603,6 +615,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    exponents_ready();
 #pragma clang loop unroll(disable)
     for (int c = 0; c < nc; ++c) step(c != 0 || tk == 0);
     mfma_results_ready();
