@@ -400,14 +400,15 @@ __device__ __forceinline__ void wait_loads_left() {
 // brought onto one row by row swaps (v_permlane32_swap, v_permlane16_swap), and
 // eight by a rotation within 16-lane rows.
 
-// 16 bytes per lane; fp32 results (gradients, read much later) past the caches:
-// 32 gradients of 1024 x 2048 take 84 instead of 92 us; bf16 outputs do better
-// in them (4096 x 7168 x 2048: 42.2 against 45.9).
+// 16 bytes per lane. Whole lines are stored past the caches (LINE): 54066 rows
+// of 8 experts, n = 2048, k = 7168: 367 against 383 us; 32 fp32 gradients of 1024 x
+// 2048: 59 against 91 (with half lines 84); 4096 x 7168 x 2048: 40.5 against 41.7
+// (with half lines 45.9).
 typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
-template <bool F32>
+template <bool LINE>
 __device__ __forceinline__ void put16(void* p, const uint32_t (&v)[4]) {
   const u32x4s w = {v[0], v[1], v[2], v[3]};
-  if constexpr (F32) __builtin_nontemporal_store(w, static_cast<u32x4s*>(p));
+  if constexpr (LINE) __builtin_nontemporal_store(w, static_cast<u32x4s*>(p));
   else *static_cast<u32x4s*>(p) = w;
 }
 
@@ -463,11 +464,11 @@ __device__ __forceinline__ void store_bf16(uint16_t* out, int64_t ldo, const v16
     regroup_bf16(acc1, x1, y1);
     uint16_t* p = out + (lane & 7) * ldo + 32 * ((lane >> 3) & 1) + 16 * g + 8 * h;
     halves(x0, x1, a, b);
-    put16<false>(p, a);
-    put16<false>(p + 8 * ldo, b);
+    put16<true>(p, a);
+    put16<true>(p + 8 * ldo, b);
     halves(y0, y1, a, b);
-    put16<false>(p + 16 * ldo, a);
-    put16<false>(p + 24 * ldo, b);
+    put16<true>(p + 16 * ldo, a);
+    put16<true>(p + 24 * ldo, b);
   } else {
     uint16_t* p = out + (lane & 15) * ldo + 16 * g + 8 * h;
     put16<false>(p, x0);
