@@ -42,7 +42,7 @@ int check_codes(const char* who, const char* name, const void* q, int64_t ldq, c
   if (ldq < 128 * chunks_of(k))
     return entry_fail(FP8BQ_E_INVAL, "%s: ld of %s (%lld bytes) < 128 * ceil(k / 256)", who, name, (long long)ldq);
   if (lds < rows) return entry_fail(FP8BQ_E_INVAL, "%s: scale ld of %s must be >= its rows", who, name);
-  if (ldq >= kMaxLd || lds >= kMaxSide) return entry_fail(FP8BQ_E_SHAPE, "%s: ld of %s too large", who, name);
+  if (ldq >= kMaxLd || lds >= kMaxSide / 8) return entry_fail(FP8BQ_E_SHAPE, "%s: ld of %s too large", who, name);
   if (!aligned(q, 16) || ldq % 16 || !aligned(s, 8))
     return entry_fail(FP8BQ_E_ALIGN, "%s: codes of %s must be 16-byte aligned with ld a multiple of 16, scales 8-byte "
                       "aligned", who, name);
@@ -91,9 +91,9 @@ int gemm(const char* who, fp8bq::MxMode mode, int32_t groups, const int32_t* row
     if (groups < 1 || groups > 256) return entry_fail(FP8BQ_E_SHAPE, "%s: groups must be 1 .. 256, got %d", who, groups);
     if (!aligned(row_off, 4)) return entry_fail(FP8BQ_E_ALIGN, "%s: row_off must be 4-byte aligned", who);
   }
-  // 256 x 256 outputs per tile at the largest, 32 x 32 at the smallest: tile counts and grids fit 31 bits
+  // tile counts (32 x 32 at the smallest) fit 31 bits
   if (m >= ((int64_t)1 << 28) || n >= ((int64_t)1 << 28) || k >= ((int64_t)1 << 28) || ldo >= ((int64_t)1 << 28) ||
-      (m / 32 + 257) > (((int64_t)1 << 31) - 1) / (n / 32 + 1))
+      m / 32 + 257 > (((int64_t)1 << 31) - 1) / (n / 32 + 1) / (mode == fp8bq::MX_K ? groups : 1))
     return entry_fail(FP8BQ_E_SHAPE, "%s: too large", who);
   if (int e = check_codes(who, "a", a, lda, sa, ldsa, m, k)) return e;
   if (int e = check_codes(who, "b", b, ldb, sb, ldsb, n, k)) return e;

@@ -11,9 +11,6 @@
 // first operand: lane l's sixteen results are row l % 32 of A and, register r,
 // column 8 (r / 4) + 4 (l / 32) + r % 4 of B.
 #include <utility>
-#ifdef MX_PROBE
-#include <cstdlib>
-#endif
 
 #include "gemm_kernels.h"
 #include "mxfp4.h"
@@ -96,14 +93,16 @@ __global__ __launch_bounds__(64 * WAVES) void mx_stream_kernel(MxGemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
 
-  const int64_t n0 = (int64_t)blockIdx.x * 32;
-  int64_t m0 = (int64_t)blockIdx.y * 32, m_end = min(m0 + 32, p.m);
+  const unsigned tiles_n = (unsigned)((p.n + 31) / 32);
+  const int tm = (int)(blockIdx.x / tiles_n);
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 32;
+  int64_t m0 = (int64_t)tm * 32, m_end = min(m0 + 32, p.m);
   const uint8_t* b = p.b;
   const uint8_t* sb = p.sb;
   int64_t out_base = 0;
   int c0 = 0, c1 = p.chunks;
   if constexpr (MODE == MX_ROWS) {
-    const RowTile t = find_tile<32>(p.row_off, p.groups, p.m, blockIdx.y);
+    const RowTile t = find_tile<32>(p.row_off, p.groups, p.m, tm);
     if (t.e < 0) return;
     m0 = t.m0;
     m_end = t.m_end;
@@ -111,7 +110,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx_stream_kernel(MxGemmArgs p) {
     sb += (int64_t)t.e * p.chunks * p.ldsb * 8;
   }
   if constexpr (MODE == MX_K) {
-    const int e = blockIdx.z;
+    const int e = blockIdx.y;
     int64_t lo, hi;
     group_range(p.row_off, e, (int64_t)p.chunks * 256, lo, hi);
     c0 = (int)(lo / 256);
@@ -326,8 +325,9 @@ struct MxLoader {
   const MxWalk<MODE, TM, TN>& wk;
   const uint32_t smem;
   const int wave;
-  uint32_t voff_a[C::kRoundsA], voff_b[C::kRoundsB], voff_s, step_s;
+  uint32_t voff_a[C::kRoundsA], voff_b[C::kRoundsB], voff_s;
   u32x4 rs_a, rs_b, rs_s;
+  const uint8_t *s_at, *s_end;           // the scales' resource spans a whole array, which may exceed its 4 GiB
   int tk = 0, c = 0, nc = 0;
 
   __device__ __forceinline__ MxLoader(const MxGemmArgs& p_, const MxWalk<MODE, TM, TN>& wk_, uint32_t smem_, int wave_,
@@ -340,7 +340,6 @@ struct MxLoader {
 #pragma unroll
     for (int i = 0; i < C::kRoundsB; ++i) voff_b[i] = (32 * i + row) * (uint32_t)p.ldb + g16;
     voff_s = (uint32_t)((wave & 1) * 128 + 2 * lane) * 8;
-    step_s = (uint32_t)(wave < 2 ? p.ldsa : p.ldsb) * 8;
     while (tk < wk.mine && wk.tile(tk).nc == 0) ++tk;      // K groups without rows
     open();
   }
@@ -358,17 +357,22 @@ struct MxLoader {
     const int64_t k0 = (int64_t)t.c0 * 128;
     rs_a = make_rsrc(p.a + t.m0 * p.lda + k0, p.a + (p.m - 1) * p.lda + (int64_t)p.chunks * 128);
     rs_b = make_rsrc(b + t.n0 * p.ldb + k0, b + (p.n - 1) * p.ldb + (int64_t)p.chunks * 128);
-    if (wave < 2)
-      rs_s = make_rsrc(p.sa + ((int64_t)t.c0 * p.ldsa + t.m0) * 8, p.sa + ((int64_t)(p.chunks - 1) * p.ldsa + p.m) * 8);
-    else
-      rs_s = make_rsrc(sb + ((int64_t)t.c0 * p.ldsb + t.n0) * 8, sb + ((int64_t)(p.chunks - 1) * p.ldsb + p.n) * 8);
+    if (wave < 2) {
+      s_at = p.sa + ((int64_t)t.c0 * p.ldsa + t.m0) * 8;
+      s_end = p.sa + ((int64_t)(p.chunks - 1) * p.ldsa + p.m) * 8;
+    } else {
+      s_at = sb + ((int64_t)t.c0 * p.ldsb + t.n0) * 8;
+      s_end = sb + ((int64_t)(p.chunks - 1) * p.ldsb + p.n) * 8;
+    }
+    rs_s = make_rsrc(s_at, s_end);
   }
   __device__ __forceinline__ void advance() {
     if (c + 1 < nc) {
       ++c;
       bump_rsrc(rs_a, 128);
       bump_rsrc(rs_b, 128);
-      bump_rsrc(rs_s, step_s);
+      s_at += (wave < 2 ? p.ldsa : p.ldsb) * 8;
+      rs_s = make_rsrc(s_at, s_end);
       return;
     }
     int next = tk + 1;
@@ -724,13 +728,14 @@ constexpr Tiling kTilings[] = {{32, 32, 25, 0}, {64, 64, 33, 40}, {64, 128, 42, 
 // chunks each (an expert's rows are taken as their average: only the device
 // knows the counts).
 int pick_tiling(int64_t groups, int64_t rows, int64_t n, int64_t chunks) {
-  int best = 0;
+  int best = 5;
   double least = 0;
   for (int i = 0; i < 6; ++i) {
     const Tiling& t = kTilings[i];
     const int64_t tiles = groups * ((rows + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
     const double time = (double)((tiles + 255) / 256) * (double)(chunks * t.step + t.store);
-    if (i == 0 || time < least) {
+    if (i == 0 && tiles > 65536) continue;           // one workgroup per tile: keep the launch's thread count in range
+    if (least == 0 || time < least) {
       best = i;
       least = time;
     }
@@ -753,11 +758,6 @@ hipError_t run(const MxGemmArgs& p, hipStream_t st) {
   // 4096 x 7168: 22.6 against 25.9 us); with more, two workgroups per CU do
   // better (4096 x 2048 x 7168: 37.2 against 40.7)
   const bool deep = g * ((rows + 127) / 128) * ((p.n + 127) / 128) <= 256;
-#ifdef MX_PROBE
-  if (const char* f = getenv("MX_FORCE")) pick = atoi(f);
-  if (pick == 6) return run_tile<MODE, F32, 2, 4, 3>(p, st);
-  if (pick == 7) return run_tile<MODE, F32, 4, 2, 2>(p, st);
-#endif
   switch (pick) {
     case 1: return run_tile<MODE, F32, 1, 1, 3>(p, st);
     case 2: return run_tile<MODE, F32, 1, 2, 3>(p, st);
@@ -766,7 +766,7 @@ hipError_t run(const MxGemmArgs& p, hipStream_t st) {
     case 5: return run_tile<MODE, F32, 4, 4, 2>(p, st);
   }
   const unsigned mt = (unsigned)((p.m + 31) / 32) + (MODE == MX_ROWS ? (unsigned)p.groups : 0u);
-  const dim3 grid((unsigned)((p.n + 31) / 32), mt, MODE == MX_K ? (unsigned)p.groups : 1u);
+  const dim3 grid((unsigned)((p.n + 31) / 32) * mt, MODE == MX_K ? (unsigned)p.groups : 1u);
   mx_stream_kernel<MODE, F32, 4><<<grid, 64 * 4, 0, st>>>(p);
   return hipGetLastError();
 }

@@ -57,7 +57,7 @@ def test_plan_of_strided_choices_and_many():
 
 CASES = [(1, 1, 1, [0, 1]), (5, 2, 1, [0, 5]), (64, 60, 6, [0, 64]), (333, 64, 6, [0, 100, 100, 290]),
          (200, 256, 8, [10, 11, 60, 190]), (300, 160, 3, [0, 300]), (128, 400, 4, [0, 64, 128]), (90, 1000, 8, [5, 80]),
-         (700, 8, 2, list(range(0, 701, 7)))]
+         (700, 8, 2, list(range(0, 701, 7))), (50, 100, 70, [0, 50]), (9, 130, 128, [0, 3, 3, 9])]
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])

@@ -194,3 +194,18 @@ def test_outputs_stay_inside_their_buffers():
     assert np.array_equal(qt[:cols, :128].cpu().numpy(), wantt[0]) and np.array_equal(st[:, :cols].cpu().numpy(), wantt[1])
     assert (q[:, 256:] == 0xAB).all() and (q[rows:] == 0xAB).all() and (s[:, rows:] == 0xCD).all()
     assert (qt[:, 128:] == 0xAB).all() and (qt[cols:] == 0xAB).all() and (st[:, cols:] == 0xCD).all()
+
+
+def test_more_than_2_31_elements():
+    """Rows behind 2^31 elements (and 4 GiB) in both forms: the same bytes as those of the last rows alone."""
+    import torch
+    rows, cols = 300_032, 7168
+    log(f"quant {rows}x{cols}")
+    x = torch.randn((rows // 64, cols), dtype=torch.bfloat16, device="cuda").repeat(64, 1)
+    q, s, qt, st = fb.quant_mxfp4_1x32(x, colwise=True)
+    last = 512
+    lq, ls, lqt, lst = fb.quant_mxfp4_1x32(x[-last:].contiguous(), colwise=True)
+    assert (q[-last:] == lq).all() and (s[:, -last:] == ls).all()
+    assert (qt[:, -last // 2:] == lqt).all() and (st[-last // 256:] == lst).all()
+    y = fb.dequant_mxfp4_1x32(q, s, cols)
+    assert (y[-last:] == fb.dequant_mxfp4_1x32(lq, ls, cols)).all()

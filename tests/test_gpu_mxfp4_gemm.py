@@ -234,3 +234,42 @@ def test_other_stream_and_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert (out == step(new)).all()
+
+
+def _raw(rows, chunks, seed):
+    """Random codes and scales made on the device."""
+    import torch
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    q = torch.randint(0, 256, (rows, chunks * 128), dtype=torch.uint8, device="cuda", generator=gen)
+    s = torch.randint(120, 130, (chunks, rows, 8), dtype=torch.uint8, device="cuda", generator=gen)
+    return q, s
+
+
+@pytest.mark.parametrize("m,n,chunks", [(2_200_000, 8, 1), (34_000_000, 5, 1), (70_000, 40, 260)])
+def test_tall_products(m, n, chunks):
+    """Many tiles of few columns; operands and offsets past 2 and 4 GiB: rows at both ends and around the powers of two
+    against the product of those rows alone."""
+    import torch
+    log(f"tall product {m}x{n}, {chunks} chunks")
+    a, sa = _raw(m, chunks, 1)
+    b, sb = _raw(n, chunks, 2)
+    out = fb.gemm_mxfp4(a, sa, b, sb, dtype=torch.float32)
+    k = chunks * 256
+    vb = codes(b, sb, k)
+    for at in sorted({0, m // 3, m - 64, min(m - 64, (1 << 24) - 32), min(m - 64, (1 << 25) - 32)}):
+        va = codes(a[at:at + 64], sa[:, at:at + 64].contiguous(), k)
+        check_product(f64(out[at:at + 64]), va, vb, k, "float32")
+
+
+def test_wide_product():
+    """A weight of millions of rows against one token."""
+    import torch
+    m, n, chunks = 1, 3_000_000, 1
+    a, sa = _raw(m, chunks, 3)
+    b, sb = _raw(n, chunks, 4)
+    out = fb.gemm_mxfp4(a, sa, b, sb)
+    va = codes(a, sa, 256)
+    for at in (0, n // 2 + 7, n - 64):
+        vb = codes(b[at:at + 64], sb[:, at:at + 64].contiguous(), 256)
+        check_product(f64(out[:, at:at + 64]), va, vb, 256, "bfloat16")
