@@ -194,6 +194,13 @@ __global__ __launch_bounds__(64 * WAVES) void mx_stream_kernel(MxGemmArgs p) {
 // clock of 1.6 .. 1.7 GHz that the power budget sets (with all-zero codes the
 // same kernel runs 25% faster; MFMAs alone on random codes reach 6.8 of the
 // nominal 9.9 PFLOP/s at 1.7 GHz).
+// SPLIT: four waves compute and four more only load. A 1 KB load holds its wave
+// up for 64 .. 90 cycles when four waves load at once (the CU takes in about 64
+// bytes a cycle), two or three MFMAs' time; where a tile's step has few MFMAs to
+// hide that behind (48 x 18432 x 7168 in tiles of 64 x 128: 14.9 against 17.2 us
+// without; 8 experts' 822 rows: 21.0 against 22.1), and there are too few tiles
+// for a second workgroup on the CU to fill the gaps, the loads get their own
+// waves. The large tiles leave no registers for that.
 // The accumulators sit in the AGPRs (256 of them at TM = TN = 4), tied to the
 // MFMA statements as in the power-of-two FP8 kernel.
 // ---------------------------------------------------------------------------
@@ -236,6 +243,12 @@ __device__ __forceinline__ void exponents_ready() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 3" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// Waits until at most N of the wave's vector memory operations are left.
+template <int N>
+__device__ __forceinline__ void wait_loads_left() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
 }
 
 struct MxTile {
@@ -387,16 +400,11 @@ struct MxLoader {
     if (q < C::kRoundsA) dma16_buf(rs_a, voff_a[q], base + (32 * q + 8 * wave) * 128);
     else if (q < C::kRoundsA + C::kRoundsB)
       dma16_buf(rs_b, voff_b[q - C::kRoundsA], base + C::kBOff + (32 * (q - C::kRoundsA) + 8 * wave) * 128);
-    else if ((wave & 1) * 128 < (wave < 2 ? C::kBM : C::kBN))
+    else if (brings_scales())
       dma16_buf(rs_s, voff_s, base + (wave < 2 ? C::kSaOff : C::kSbOff) + (wave & 1) * 1024);
   }
+  __device__ __forceinline__ bool brings_scales() const { return (wave & 1) * 128 < (wave < 2 ? C::kBM : C::kBN); }
 };
-
-// Waits until at most N of the wave's vector memory operations are left.
-template <int N>
-__device__ __forceinline__ void wait_loads_left() {
-  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
-}
 
 // ---- epilogue ------------------------------------------------------------------
 // Lanes hold columns 8 q + 4 h .. + 3 (q = 0 .. 3, h = l / 32) of row l % 32; the
@@ -521,8 +529,8 @@ __device__ __forceinline__ void store_edge(const MxGemmArgs& p, int64_t base, in
   }
 }
 
-template <int MODE, bool F32, int TM, int TN, int NST>
-__global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) {
+template <int MODE, bool F32, int TM, int TN, int NST, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? 512 : 256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) {
   using C = TileCfg<TM, TN>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NST * C::kStage];
   __shared__ MxTables tab;
@@ -534,8 +542,10 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
   if constexpr (MODE != MX_DENSE) {
     int64_t lo = 0, hi = 0;
     if (tid < p.groups) group_range(p.row_off, tid, MODE == MX_ROWS ? p.m : (int64_t)p.chunks * 256, lo, hi);
-    tab.lo[tid] = (int)(MODE == MX_ROWS ? lo : lo / 256);
-    tab.hi[tid] = (int)(MODE == MX_ROWS ? hi : hi / 256);
+    if (tid < 256) {
+      tab.lo[tid] = (int)(MODE == MX_ROWS ? lo : lo / 256);
+      tab.hi[tid] = (int)(MODE == MX_ROWS ? hi : hi / 256);
+    }
     if constexpr (MODE == MX_ROWS) {
       const int mine = (int)((hi - lo + C::kBM - 1) / C::kBM);
       int sum = mine;
@@ -544,18 +554,56 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
         const int v = __shfl_up(sum, d);
         if (lane >= d) sum += v;
       }
-      __shared__ int wsum[4];
+      __shared__ int wsum[8];
       if (lane == 63) wsum[wave] = sum;
       __syncthreads();
       for (int w = 0; w < wave; ++w) sum += wsum[w];
-      tab.before[tid + 1] = sum;
+      if (tid < 256) tab.before[tid + 1] = sum;
       if (tid == 0) tab.before[0] = 0;
     }
     __syncthreads();
   }
   const MxWalk<MODE, TM, TN> wk(p, tab);
   if (wk.mine == 0) return;                                   // uniform
-  MxLoader<MODE, TM, TN> ld(p, wk, lds_addr(smem), wave, lane);
+  // Loads a wave has in flight beyond the next step's when a step's barrier is
+  // reached; half the waves bring no scales of a small tile.
+  auto left = [](bool scales, auto stages) {
+    constexpr int n = decltype(stages)::value;
+    if (scales) wait_loads_left<n * C::kParts>();
+    else wait_loads_left<n * (C::kParts - 1)>();
+  };
+  MxLoader<MODE, TM, TN> ld(p, wk, lds_addr(smem), wave & 3, lane);
+  const bool scales = ld.brings_scales();
+  auto wait_next = [&] { left(scales, std::integral_constant<int, NST - 2>{}); };
+  if (!SPLIT || wave >= 4) {
+#pragma unroll
+    for (int st = 0; st < NST; ++st) {
+#pragma unroll
+      for (int q = 0; q < C::kParts; ++q) ld.part(q, st);
+      ld.advance();
+    }
+    left(scales, std::integral_constant<int, NST - 1>{});
+  }
+  __syncthreads();
+  if (SPLIT && wave >= 4) {
+    // a loading wave: the compute waves' barriers, each followed by the loads into the stage that it has freed
+    int cs = 0;
+#pragma clang loop unroll(disable)
+    for (int tk = 0; tk < wk.mine; ++tk) {
+      const int nc = wk.tile(tk).nc;
+#pragma clang loop unroll(disable)
+      for (int c = 0; c < nc; ++c) {
+        wait_next();
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < C::kParts; ++q) ld.part(q, cs);
+        ld.advance();
+        cs = cs + 1 < NST ? cs + 1 : 0;
+      }
+    }
+    wait_loads_left<0>();                                     // the repeated loads land before the LDS is released
+    return;
+  }
 
   // LDS offset of this lane's codes of slice t in a 32-row subtile: logical slot 4 h + t
   uint32_t off[4];
@@ -570,24 +618,6 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
   auto b_scale = [&](const uint8_t* st, int j) {
     return *reinterpret_cast<const int*>(st + C::kSbOff + ((wave_n * TN + j) * 32 + r32) * 8 + 4 * h);
   };
-
-  // Loads a wave has in flight beyond the next step's when a step's barrier is
-  // reached; half the waves bring no scales of a small tile.
-  const bool scales = (wave & 1) * 128 < (wave < 2 ? C::kBM : C::kBN);
-  auto wait_next = [&] {
-    if constexpr (NST == 2) wait_loads_left<0>();
-    else if (scales) wait_loads_left<(NST - 2) * C::kParts>();
-    else wait_loads_left<(NST - 2) * (C::kParts - 1)>();
-  };
-#pragma unroll
-  for (int st = 0; st < NST; ++st) {
-#pragma unroll
-    for (int q = 0; q < C::kParts; ++q) ld.part(q, st);
-    ld.advance();
-  }
-  if (scales) wait_loads_left<(NST - 1) * C::kParts>();
-  else wait_loads_left<(NST - 1) * (C::kParts - 1)>();
-  __syncthreads();
 
   v4i af[4][TM], bf[4][TN];
   int ea[TM], eb[TN], ean[TM], ebn[TN];
@@ -629,7 +659,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
       }
       if constexpr (t == 0 && u == kNT - 1) {
         __builtin_amdgcn_s_waitcnt(0xC07F);                   // slice 3 has been read
-        if (NST > 2 || wait_loads) wait_next();
+        if (!SPLIT && (NST > 2 || wait_loads)) wait_next();
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < TM; ++q) ean[q] = a_scale(nst, q);
@@ -637,13 +667,13 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
         for (int q = 0; q < TN; ++q) ebn[q] = b_scale(nst, q);
       }
       // the cursor's loads over slices 1 .. 3
-      if constexpr (t >= 1) {
+      if constexpr (t >= 1 && !SPLIT) {
         constexpr int at = (t - 1) * kNT + u, slots = 3 * kNT;
 #pragma unroll
         for (int q = 0; q < C::kParts; ++q)
           if (q * slots / C::kParts == at) ld.part(q, cs);
       }
-      if constexpr (t == 3 && u == kNT - 1) ld.advance();
+      if constexpr (t == 3 && u == kNT - 1 && !SPLIT) ld.advance();
       __builtin_amdgcn_sched_barrier(0);
     }, std::make_integer_sequence<int, 4 * kNT>{});
 #pragma unroll
@@ -668,7 +698,7 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
 #pragma clang loop unroll(disable)
     for (int c = 0; c < nc; ++c) step(c != 0 || tk == 0);
     mfma_results_ready();
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the loads the next tile's first step reads
+    if constexpr (!SPLIT) wait_loads_left<0>();               // the loads the next tile's first step reads
     const MxTile done = wk.tile(tk);
     const int el = lane_fresh();
     const int64_t base = MODE == MX_K ? (int64_t)done.e * p.m * p.ldo : 0;
@@ -691,10 +721,10 @@ __global__ __launch_bounds__(256) void mx_tile_kernel(MxGemmArgs p, int vec_ok) 
         }
       }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");            // the repeated loads land before the LDS is released
+  if constexpr (!SPLIT) wait_loads_left<0>();                 // the repeated loads land before the LDS is released
 }
 
-template <int MODE, bool F32, int TM, int TN, int NST>
+template <int MODE, bool F32, int TM, int TN, int NST, bool SPLIT>
 hipError_t run_tile(const MxGemmArgs& p, hipStream_t st) {
   using C = TileCfg<TM, TN>;
   constexpr int kEsz = F32 ? 4 : 2;
@@ -703,7 +733,7 @@ hipError_t run_tile(const MxGemmArgs& p, hipStream_t st) {
   const int64_t cus = 256 * (160 * 1024 / (C::kStage * NST + (MODE == MX_DENSE ? 0 : 4096)));
   const unsigned grid = (unsigned)(tiles < cus ? tiles : cus);
   const int vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo * kEsz % 16 == 0 && p.m * p.ldo * kEsz % 16 == 0;
-  mx_tile_kernel<MODE, F32, TM, TN, NST><<<grid, 256, 0, st>>>(p, vec);
+  mx_tile_kernel<MODE, F32, TM, TN, NST, SPLIT><<<grid, SPLIT ? 512 : 256, 0, st>>>(p, vec);
   return hipGetLastError();
 }
 
@@ -754,16 +784,16 @@ hipError_t run(const MxGemmArgs& p, hipStream_t st) {
   const int64_t rows = MODE == MX_ROWS ? (p.m + 2 * g - 1) / (2 * g) : p.m;
   const int64_t chunks = MODE == MX_K ? (p.chunks + g - 1) / g : p.chunks;
   int pick = pick_tiling(g, rows, p.n, chunks);
-  // one 128 x 128 tile per CU or less: a third stage hides more latency (1000 x
-  // 4096 x 7168: 22.6 against 25.9 us); with more, two workgroups per CU do
-  // better (4096 x 2048 x 7168: 37.2 against 40.7)
+  // one 128 x 128 tile per CU or less: loading waves and a third stage hide more
+  // latency (1000 x 4096 x 7168: 22.5 against 25.9 us); with more, two workgroups
+  // per CU do better (4096 x 2048 x 7168: 37.2 against 38.8)
   const bool deep = g * ((rows + 127) / 128) * ((p.n + 127) / 128) <= 256;
   switch (pick) {
-    case 1: return run_tile<MODE, F32, 1, 1, 3>(p, st);
-    case 2: return run_tile<MODE, F32, 1, 2, 3>(p, st);
-    case 3: return deep ? run_tile<MODE, F32, 2, 2, 3>(p, st) : run_tile<MODE, F32, 2, 2, 2>(p, st);
-    case 4: return run_tile<MODE, F32, 2, 4, 2>(p, st);
-    case 5: return run_tile<MODE, F32, 4, 4, 2>(p, st);
+    case 1: return run_tile<MODE, F32, 1, 1, 3, true>(p, st);
+    case 2: return run_tile<MODE, F32, 1, 2, 3, true>(p, st);
+    case 3: return deep ? run_tile<MODE, F32, 2, 2, 3, true>(p, st) : run_tile<MODE, F32, 2, 2, 2, false>(p, st);
+    case 4: return run_tile<MODE, F32, 2, 4, 2, false>(p, st);
+    case 5: return run_tile<MODE, F32, 4, 4, 2, false>(p, st);
   }
   const unsigned mt = (unsigned)((p.m + 31) / 32) + (MODE == MX_ROWS ? (unsigned)p.groups : 0u);
   const dim3 grid((unsigned)((p.n + 31) / 32) * mt, MODE == MX_K ? (unsigned)p.groups : 1u);

@@ -107,7 +107,8 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E;            // quad_perm [1,0,3,2], [2,3,0,1]
-constexpr int kRor4 = 0x124, kRor8 = 0x128;          // row_ror: rotate a row of 16 lanes
+constexpr int kRor4 = 0x124;                         // row_ror: rotate a row of 16 lanes
+constexpr int kHalfMirror = 0x141;                   // lane 7 - i of each eight
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // The source row of row r of the quantised matrix; ok = false for a zero row,
@@ -208,26 +209,25 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int c
 }
 
 // Column form, and (ROWS) the row form beside it from the same read. A block
-// stages 128 rows of 256 bytes (128 columns, 64 of fp32) in LDS; then thread
+// stages 128 rows of 128 bytes (64 columns, 32 of fp32) in LDS; then thread
 // (column dword, row tile, half of the dword) walks 32 rows of its dword:
-// consecutive lanes on consecutive dwords, no bank conflict, 16 bytes of codes
-// per thread. The four
-// row tiles' scale bytes of a column meet in LDS for one 4-byte store. The
+// consecutive lanes on consecutive dwords, 16 bytes of codes per thread. The
+// four row tiles' scale bytes of a column meet in LDS for one 4-byte store. The
 // grid covers whole 256 x 256 squares of the matrix (what lies past it is
 // zeros); the blocks of a square run on one XCD, one after the other, so that
-// the 64-byte pieces of code rows that they write meet as full lines in its L2.
-// The squares run over the columns first.
-constexpr int kColsThreads = 512;
+// the pieces of code rows that they write (32 bytes of a row, 64 of a column)
+// meet as full lines in its L2. The squares run over the columns first.
+constexpr int kColsThreads = 256;
 template <int T, bool NOSAT, bool IDX, bool VEC, bool ROWS>
 __global__ __launch_bounds__(kColsThreads) void mx_quant_cols_kernel(MxQuantArgs p, unsigned rsq, unsigned csq) {
   constexpr int kPer = 4 / Elem<T>::kBytes;             // elements per dword
-  constexpr int kCols = 64 * kPer;
+  constexpr int kCols = 32 * kPer;
   constexpr int kLane = 4 * kPer;                       // elements of a lane's 16 bytes
-  constexpr int kRounds = 128 * 16 / kColsThreads;      // rows per thread of the load
-  constexpr int kStep = kColsThreads / 16;
-  __shared__ uint32_t tile[128][64];
+  constexpr int kRounds = 128 * 8 / kColsThreads;       // rows per thread of the load
+  constexpr int kStep = kColsThreads / 8;
+  __shared__ uint32_t tile[128][32];
   __shared__ uint8_t scales[kCols][4];
-  const int t = threadIdx.x, l16 = t & 15;
+  const int t = threadIdx.x, l8 = t & 7;
   constexpr int kSub = 2 * 256 / kCols;                 // blocks of a square
   const unsigned g = blockIdx.x / (8 * kSub), in = blockIdx.x % (8 * kSub);
   const unsigned here = min(rsq * csq - 8 * g, 8u);     // squares of this group of (up to) eight, one per XCD
@@ -239,49 +239,42 @@ __global__ __launch_bounds__(kColsThreads) void mx_quant_cols_kernel(MxQuantArgs
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     bool ok;
-    const int64_t xr = source<IDX>(p, r0 + i * kStep + (t >> 4), ok, skip[i]);
+    const int64_t xr = source<IDX>(p, r0 + i * kStep + (t >> 3), ok, skip[i]);
     const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
-    load_row<T, kLane, VEC>(row, c0 + l16 * kLane, p.cols, ok, w[i]);
+    load_row<T, kLane, VEC>(row, c0 + l8 * kLane, p.cols, ok, w[i]);
   }
 #pragma unroll
   for (int i = 0; i < kRounds; ++i)
-    *reinterpret_cast<uint4*>(&tile[i * kStep + (t >> 4)][l16 * 4]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+    *reinterpret_cast<uint4*>(&tile[i * kStep + (t >> 3)][l8 * 4]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
 
   if constexpr (ROWS) {
-    // a tile is 4 lanes (8 of fp32)
+    // a tile is 4 lanes (8 of fp32); its scale byte sits on all of them
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
-      const int64_t r = r0 + i * kStep + (t >> 4);
+      const int64_t r = r0 + i * kStep + (t >> 3);
       uint32_t amax = amax_of<T>(w[i]);
       amax = max2(amax, dpp<kXor1>(amax));
       amax = max2(amax, dpp<kXor2>(amax));
-      if constexpr (kPer == 1) {                        // lanes 0 .. 3 and 4 .. 7 of each half row
-        const uint32_t a = dpp<kRor4>(amax), b = dpp<0x12C>(amax);   // ror 4, ror 12
-        amax = max2(amax, (l16 & 4) ? a : b);
-      }
+      if constexpr (kPer == 1) amax = max2(amax, dpp<kHalfMirror>(amax));
       const uint32_t byte = mx_scale_byte<NOSAT>(amax);
       const uint32_t code = codes_of<T, 0>(w[i], byte);
+      uint8_t* sp = p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32;
       if constexpr (kPer == 2) {
-        uint32_t sc = byte << (8 * (l16 >> 2));
-        sc |= dpp<kRor4>(sc);
-        sc |= dpp<kRor8>(sc);
+        uint32_t sc = byte << (8 * (l8 >> 2));
+        sc |= dpp<kHalfMirror>(sc);
         if (!skip[i]) {
-          *reinterpret_cast<uint32_t*>(p.q + r * p.ldq + c0 / 2 + l16 * 4) = code;
-          if (l16 == 0) *reinterpret_cast<uint32_t*>(p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32) = sc;
+          *reinterpret_cast<uint32_t*>(p.q + r * p.ldq + c0 / 2 + l8 * 4) = code;
+          if (l8 == 0) *reinterpret_cast<uint16_t*>(sp) = (uint16_t)sc;
         }
-      } else {
-        uint32_t sc = byte << (8 * (l16 >> 3));
-        sc |= dpp<kRor8>(sc);
-        if (!skip[i]) {
-          *reinterpret_cast<uint16_t*>(p.q + r * p.ldq + c0 / 2 + l16 * 2) = (uint16_t)code;
-          if (l16 == 0) *reinterpret_cast<uint16_t*>(p.s + ((c0 / 256) * p.lds + r) * 8 + (c0 % 256) / 32) = (uint16_t)sc;
-        }
+      } else if (!skip[i]) {
+        *reinterpret_cast<uint16_t*>(p.q + r * p.ldq + c0 / 2 + l8 * 2) = (uint16_t)code;
+        if (l8 == 0) *sp = (uint8_t)byte;
       }
     }
   }
   __syncthreads();
 
-  const int cd = t & 63, rt = (t >> 6) & 3, h = t >> 8;
+  const int cd = t & 31, rt = (t >> 5) & 3, h = t >> 7;
   if (h < kPer) {
     uint32_t d[32];
 #pragma unroll
@@ -360,7 +353,7 @@ template <int T, bool NOSAT, bool IDX, bool VEC>
 hipError_t run_quant(const MxQuantArgs& a, int32_t* links, hipStream_t st) {
   const int cchunks = (int)((a.cols + 255) / 256);
   if (a.qt) {
-    constexpr int kCols = 64 * 4 / Elem<T>::kBytes;
+    constexpr int kCols = 32 * 4 / Elem<T>::kBytes;
     const unsigned rsq = (unsigned)((a.rows + 255) / 256);
     const unsigned grid = rsq * (unsigned)cchunks * (2 * 256 / kCols);
     if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, kColsThreads, 0, st>>>(a, rsq, cchunks);
