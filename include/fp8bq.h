@@ -1,6 +1,7 @@
 /*
  * fp8bq -- fine-grained FP8 (E4M3) quantisation and block-scaled FP8 GEMM for
- * AMD Instinct MI355X (gfx950).
+ * AMD Instinct MI355X (gfx950); further down, the same Linear in 4-bit
+ * microscaled form (MXFP4) and the routing of tokens to its experts.
  *
  * The operation is the FP8 mixed-precision Linear of the DeepSeek-V3 report
  * (Chinese translation, chapter 3 "Infrastructure"):
