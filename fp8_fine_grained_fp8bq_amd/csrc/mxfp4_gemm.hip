@@ -221,24 +221,29 @@ struct TileCfg {
 // operand that a VALU instruction has just written needs two wait states.
 // Fragments come from LDS reads (waited for by the compiler); the exponents
 // and the cleared accumulators come from VALU moves, which exponents_ready()
-// follows. (A wait before every MFMA instead costs 2 .. 3%: 987 against 970 us on
-// 16384 x 18432 x 7168.) tests/test_mfma_hazards.py checks the built code.
-template <int T>
+// follows. WAIT: the two states before every MFMA, for the small tiles, whose
+// registers the compiler may park in AGPRs and fetch back right before use; for
+// the large ones they would cost 2 .. 3% (987 against 970 us on 16384 x 18432 x
+// 7168). tests/test_mfma_hazards.py checks the built code of both.
+// One statement each, so that nothing comes between the wait and the MFMA.
+#define FP8BQ_MFMA(wait, sel) \
+  asm volatile(wait "v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 " sel " cbsz:4 blgp:4" \
+               : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa))
+#define FP8BQ_MFMA_SLICE(wait) \
+  if constexpr (T == 0) FP8BQ_MFMA(wait, "op_sel_hi:[0,0,0]"); \
+  else if constexpr (T == 1) FP8BQ_MFMA(wait, "op_sel:[1,1,0] op_sel_hi:[0,0,0]"); \
+  else if constexpr (T == 2) FP8BQ_MFMA(wait, "op_sel_hi:[1,1,0]"); \
+  else FP8BQ_MFMA(wait, "op_sel:[1,1,0] op_sel_hi:[1,1,0]")
+template <int T, bool WAIT>
 __device__ __forceinline__ void mfma_slice(v16f& acc, const v4i& b, const v4i& a, int sb, int sa) {
-  if constexpr (T == 0)
-    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
-  else if constexpr (T == 1)
-    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
-  else if constexpr (T == 2)
-    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
-                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
-  else
-    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
-                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  if constexpr (WAIT) {
+    FP8BQ_MFMA_SLICE("s_nop 1\n\t");
+  } else {
+    FP8BQ_MFMA_SLICE("");
+  }
 }
-
+#undef FP8BQ_MFMA_SLICE
+#undef FP8BQ_MFMA
 __device__ __forceinline__ void exponents_ready() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 3" ::: "memory");
@@ -644,7 +649,7 @@ __global__ __launch_bounds__(SPLIT ? 512 : 256) void mx_tile_kernel(MxGemmArgs p
     for_each_const([&](auto tc) {
       constexpr int t = decltype(tc)::value / kNT, u = decltype(tc)::value % kNT;
       constexpr int i = u / TN, j = u % TN;
-      mfma_slice<t>(acc[i][j], bf[t][j], af[t][i], eb[j], ea[i]);
+      mfma_slice<t, (TM * TN < 8)>(acc[i][j], bf[t][j], af[t][i], eb[j], ea[i]);
       // the fragments due in this slice, spread over its first MFMAs: slice 3 of this step (t = 0), else slice t - 1 of
       // the next
       constexpr int rs = (t + 3) & 3;
