@@ -50,7 +50,7 @@ def tensors_command(out: str) -> list:
             "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include",
             "-I/opt/rocm/include", f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(ROOT, 'include')}",
             os.path.join(CSRC, "torch_tensors.cpp"), "-o", out, f"-L{PKG}", "-l:libfp8bq.so", f"-L{torch}/lib", "-lc10",
-            "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+            "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False) -> str:
