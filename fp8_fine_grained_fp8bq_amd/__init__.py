@@ -43,6 +43,7 @@ MX_NOSAT = 0x20     # MXFP4 scales that never saturate an element
 SOFTMAX, SIGMOID = 0, 1
 ROW_UNUSED = -2     # in a dispatch's src: a row of no expert
 MOE_PLAN_WORKSPACE_BYTES = 256 * 256 * 4
+DISPATCH_WORKSPACE_ROW_BYTES = 36
 SCALE_POW2 = 0x10   # power-of-two scales (OR into the act mode / gemm op; `flags` elsewhere)
 
 EXPORTS = ("fp8bq_quant_act_1x128", "fp8bq_quant_w_128x128", "fp8bq_requant_t_128x1", "fp8bq_gemm",

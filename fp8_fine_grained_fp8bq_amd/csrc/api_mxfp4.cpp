@@ -9,6 +9,7 @@
 #include "entry.h"
 #include "mxfp4.h"
 
+static_assert(FP8BQ_DISPATCH_WORKSPACE_ROW_BYTES == 4 * (fp8bq::kMxDispatchSlots + 1), "workspace size in the header");
 static_assert(FP8BQ_MOE_PLAN_WORKSPACE_BYTES == fp8bq::kMoePlanMaxBlocks * 256 * 4, "workspace size in the header");
 
 namespace {
@@ -51,7 +52,7 @@ int check_codes(const char* who, const char* name, const void* q, int64_t ldq, c
 
 int quant(const char* who, const void* x, int xtype, int64_t xrows, int64_t cols, int64_t ldx, const int32_t* src,
           bool indexed, int64_t rows, void* q, int64_t ldq, void* s, int64_t lds, void* qt, int64_t ldqt, void* st,
-          int64_t ldst, int flags, void* links, void* stream) {
+          int64_t ldst, int flags, void* ws, void* stream) {
   if (!x || (indexed && !src)) return entry_fail(FP8BQ_E_INVAL, "%s: null pointer", who);
   if (bad_dtype(xtype)) return entry_fail(FP8BQ_E_INVAL, "%s: type must be BF16, FP16 or FP32, got %d", who, xtype);
   if (flags & ~FP8BQ_MX_NOSAT) return entry_fail(FP8BQ_E_INVAL, "%s: unknown flags %d", who, flags);
@@ -65,16 +66,16 @@ int quant(const char* who, const void* x, int xtype, int64_t xrows, int64_t cols
   if (qt || st)
     if (int e = check_codes(who, "the transposed form", qt, ldqt, st, ldst, cols, rows)) return e;
   if (too_large(xrows, cols)) return entry_fail(FP8BQ_E_SHAPE, "%s: too large", who);
-  if (!aligned(x, elem_bytes(xtype)) || !aligned(src, 4) || !aligned(links, 4))
-    return entry_fail(FP8BQ_E_ALIGN, "%s: x must be aligned to its element, src and workspace to 4 bytes", who);
+  if (!aligned(x, elem_bytes(xtype)) || !aligned(src, 4) || !aligned(ws, 16))
+    return entry_fail(FP8BQ_E_ALIGN, "%s: x must be aligned to its element, src to 4 bytes, workspace to 16", who);
   if (int e = fp8bq::entry_device()) return e;
   const fp8bq::MxQuantArgs a{x, xrows, rows, cols, ldx, src,
                              static_cast<uint8_t*>(q), ldq, static_cast<uint8_t*>(s), lds,
                              static_cast<uint8_t*>(qt), ldqt, static_cast<uint8_t*>(st), ldst};
-  // The linked form pays for two small launches and the walk of its chains.
-  const bool link = links && !qt && rows >= 2 * xrows;
+  // Reading each row once pays for two small launches and the slots.
+  const bool once = ws && !qt && rows >= 2 * xrows;
   return launched(fp8bq::launch_quant_mxfp4(a, xtype, (flags & FP8BQ_MX_NOSAT) != 0,
-                                            link ? static_cast<int32_t*>(links) : nullptr,
+                                            once ? static_cast<int32_t*>(ws) : nullptr,
                                             reinterpret_cast<hipStream_t>(stream)), who);
 }
 

@@ -21,9 +21,11 @@ struct MxQuantArgs {
   uint8_t* qt; int64_t ldqt;
   uint8_t* st; int64_t ldst;
 };
-// links: null, or (src given, only the row form wanted) xrows + rows words: each
-// x row is then read once and written to every row that shows it.
-hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, int32_t* links, hipStream_t stream);
+// ws: null, or (src given, only the row form wanted) xrows * (kMxDispatchSlots +
+// 1) words, 16-byte aligned: each x row is then read once and written to every
+// row that shows it.
+constexpr int kMxDispatchSlots = 8;
+hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, int32_t* ws, hipStream_t stream);
 hipError_t launch_dequant_mxfp4(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq, const uint8_t* s,
                                 int64_t lds, void* y, int ytype, int64_t ldy, hipStream_t stream);
 

@@ -126,86 +126,109 @@ __device__ __forceinline__ int64_t source(const MxQuantArgs& p, int64_t r, bool&
   return ok ? r : 0;
 }
 
-// Dispatch by links: a row that several experts get is read and quantised once.
-// next[r] chains the rows that show the same source row (head[t] the first),
-// in an order that varies from call to call and does not matter: every row of
-// a chain gets the same bytes. Rows of zeros are written right here.
-__global__ __launch_bounds__(256) void mx_unlink_kernel(int32_t* head, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) head[i] = -1;
+// Codes (8 bytes) and the scales' dword of the 16 elements w at place l16 of a
+// 256-element chunk (16 lanes): a tile is a pair of lanes; its scale byte is
+// shifted to its place in the chunk's eight, and OR over the lanes of each half
+// row gives dwords, valid on lanes 4 and 12. All 16 lanes take part.
+template <int T, bool NOSAT, int N>
+__device__ __forceinline__ void encode_piece(const uint32_t (&w)[N], int l16, uint2& codes, uint32_t& sc) {
+  uint32_t amax = amax_of<T>(w);
+  amax = max2(amax, dpp<kXor1>(amax));
+  const uint32_t byte = mx_scale_byte<NOSAT>(amax);
+  sc = (l16 & 1) ? 0u : byte << (8 * ((l16 >> 1) & 3));
+  sc |= dpp<kXor2>(sc);
+  sc |= dpp<kRor4>(sc) & ((l16 & 7) < 4 ? 0u : 0xFFFFFFFFu);   // lane 4 (12) gathers lanes 0 .. 3 (8 .. 11)
+  codes = make_uint2(codes_of<T, 0>(w, byte), codes_of<T, 1>(w, byte));
 }
-__global__ __launch_bounds__(256) void mx_link_kernel(MxQuantArgs p, int chunks, int32_t* head, int32_t* next) {
+__device__ __forceinline__ void write_piece(const MxQuantArgs& p, int64_t row, int chunk, int l16, uint2 codes, uint32_t sc) {
+  *reinterpret_cast<uint2*>(p.q + row * p.ldq + chunk * 128 + l16 * 8) = codes;
+  if ((l16 & 7) == 4) *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + row) * 8 + (l16 >> 3) * 4) = sc;
+}
+
+// Dispatch by slots: a row that several experts get is read and quantised once.
+// Slot table: for each row of x the first kSlots rows that show it (in an order
+// that varies from call to call and does not matter: they all get the same
+// bytes) and their number. A row of zeros is written here, and so is one that
+// finds its source's slots full (more than kSlots choices of a token).
+constexpr int kSlots = kMxDispatchSlots;
+__global__ __launch_bounds__(256) void mx_clear_kernel(int32_t* count, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) count[i] = 0;
+}
+template <int T, bool NOSAT, bool VEC>
+__global__ __launch_bounds__(256) void mx_slot_kernel(MxQuantArgs p, int chunks, int32_t* slots, int32_t* count) {
   const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, l16 = lane & 15;
   const int32_t t = r < p.rows ? p.src[r] : FP8BQ_ROW_UNUSED;
-  const bool zero = t != FP8BQ_ROW_UNUSED && (t < 0 || t >= p.xrows);
-  if (t >= 0 && t < p.xrows) next[r] = atomicExch(&head[t], (int32_t)r);
-  for (uint64_t left = __ballot(zero); left; left &= left - 1) {
-    const int64_t row = r - lane + __ffsll((unsigned long long)left) - 1;
-    for (int i = lane; i < chunks * 8; i += 64) {
-      *reinterpret_cast<uint4*>(p.q + row * p.ldq + i * 16) = make_uint4(0, 0, 0, 0);
-      p.s[((int64_t)(i >> 3) * p.lds + row) * 8 + (i & 7)] = 0;
+  const bool real = t >= 0 && t < p.xrows;
+  bool here = t != FP8BQ_ROW_UNUSED;
+  if (real) {
+    const int at = atomicAdd(&count[t], 1);
+    here = at >= kSlots;
+    if (!here) slots[(int64_t)t * kSlots + at] = (int32_t)r;
+  }
+  for (uint64_t left = __ballot(here); left; left &= left - 1) {   // the wave takes its lanes' rows in turn
+    const int from = __ffsll((unsigned long long)left) - 1;
+    const bool ok = __shfl((int)real, from) != 0;
+    const int64_t row = r - lane + from, xr = ok ? __shfl(t, from) : 0;
+    const auto* x = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
+    for (int c0 = 0; c0 < chunks; c0 += 4) {
+      const int chunk = c0 + (lane >> 4);
+      uint32_t w[16 * Elem<T>::kBytes / 4], sc;
+      load_row<T, 16, VEC>(x, (int64_t)chunk * 256 + l16 * 16, p.cols, ok, w);
+      uint2 codes;
+      encode_piece<T, NOSAT>(w, l16, codes, sc);
+      if (chunk < chunks) write_piece(p, row, chunk, l16, codes, sc);
     }
   }
 }
 
 // Row form. 16 lanes take one 256-element chunk of a row, 16 elements each (32
-// contiguous bytes of bf16), so a tile is a pair of lanes and a lane's codes
-// are one 8-byte store; each lane takes the same place of two neighbouring
-// chunks, all loads before any arithmetic. A block takes 16 rows of a chunk
-// pair, the pairs of a row run fastest over the grid. A lane pair's scale byte
-// is shifted to its place in the chunk's eight; OR over the lanes of each half
-// row gives dwords. LINK: rows of x, each written along its chain.
-template <int T, bool NOSAT, bool IDX, bool VEC, bool LINK = false>
-__global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks, const int32_t* head = nullptr,
-                                                            const int32_t* next = nullptr) {
+// contiguous bytes of bf16), so a lane's codes are one 8-byte store; each lane
+// takes the same place of two neighbouring chunks, all loads before any
+// arithmetic. A block takes 16 rows of a chunk pair, the pairs of a row run
+// fastest over the grid. SLOTS: rows of x, each written to the rows in its slots.
+template <int T, bool NOSAT, bool IDX, bool VEC, bool SLOTS = false>
+__global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks, const int32_t* slots = nullptr,
+                                                            const int32_t* count = nullptr) {
   const int t = threadIdx.x, l16 = t & 15;
   const unsigned pairs = (unsigned)(chunks + 1) / 2;
   const int chunk0 = 2 * (int)(blockIdx.x % pairs);
   const int64_t r = (int64_t)(blockIdx.x / pairs) * 16 + (t >> 4);
   bool ok, skip;
   int64_t xr;
-  int32_t at = -1;
-  if constexpr (LINK) {
-    at = r < p.xrows ? head[r] : -1;
-    ok = at >= 0;                                       // a row that nobody gets is not read
+  int n = 1;
+  if constexpr (SLOTS) {
+    n = r < p.xrows ? min(count[r], kSlots) : 0;
+    ok = n > 0;                                         // a row that nobody gets is not read
     skip = !ok;
     xr = ok ? r : 0;
   } else {
     xr = source<IDX>(p, r, ok, skip);
   }
-  constexpr int kDw = 16 * Elem<T>::kBytes / 4;
-  uint32_t w[2][kDw];
-  uint2 codes[2];
-  uint32_t scs[2];
+  uint32_t w[2][16 * Elem<T>::kBytes / 4];
   const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
 #pragma unroll
   for (int u = 0; u < 2; ++u) load_row<T, 16, VEC>(row, (int64_t)(chunk0 + u) * 256 + l16 * 16, p.cols, ok, w[u]);
+  int32_t to[SLOTS ? kSlots : 1];
+  if constexpr (SLOTS) {
+    static_assert(kSlots % 4 == 0, "slots are read four at a time");
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t amax = amax_of<T>(w[u]);
-    amax = max2(amax, dpp<kXor1>(amax));
-    const uint32_t byte = mx_scale_byte<NOSAT>(amax);
-    uint32_t sc = (l16 & 1) ? 0u : byte << (8 * ((l16 >> 1) & 3));
-    sc |= dpp<kXor2>(sc);
-    sc |= dpp<kRor4>(sc) & ((l16 & 7) < 4 ? 0u : 0xFFFFFFFFu);   // lane 4 (12) gathers lanes 0 .. 3 (8 .. 11)
-    codes[u] = make_uint2(codes_of<T, 0>(w[u], byte), codes_of<T, 1>(w[u], byte));
-    scs[u] = sc;
+    for (int i = 0; i < kSlots / 4; ++i)
+      *reinterpret_cast<int4*>(&to[4 * i]) = reinterpret_cast<const int4*>(slots + xr * kSlots)[i];
   }
-  if (skip) return;
-  int64_t to = LINK ? at : r;
-  do {
-    const int64_t following = LINK ? next[to] : -1;
+  uint2 codes[2];
+  uint32_t sc[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int chunk = chunk0 + u;
-      if (chunk >= chunks) break;
-      *reinterpret_cast<uint2*>(p.q + to * p.ldq + chunk * 128 + l16 * 8) = codes[u];
-      if ((l16 & 7) == 4)
-        *reinterpret_cast<uint32_t*>(p.s + ((int64_t)chunk * p.lds + to) * 8 + (l16 >> 3) * 4) = scs[u];
-    }
-    to = following;
-  } while (to >= 0);
+  for (int u = 0; u < 2; ++u) encode_piece<T, NOSAT>(w[u], l16, codes[u], sc[u]);
+  if (skip) return;
+#pragma unroll
+  for (int i = 0; i < (SLOTS ? kSlots : 1); ++i) {
+    if (i >= n) break;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (chunk0 + u < chunks) write_piece(p, SLOTS ? to[i] : r, chunk0 + u, l16, codes[u], sc[u]);
+  }
 }
 
 // Column form, and (ROWS) the row form beside it from the same read. A block
@@ -350,7 +373,7 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restri
 }
 
 template <int T, bool NOSAT, bool IDX, bool VEC>
-hipError_t run_quant(const MxQuantArgs& a, int32_t* links, hipStream_t st) {
+hipError_t run_quant(const MxQuantArgs& a, int32_t* ws, hipStream_t st) {
   const int cchunks = (int)((a.cols + 255) / 256);
   if (a.qt) {
     constexpr int kCols = 32 * 4 / Elem<T>::kBytes;
@@ -358,14 +381,14 @@ hipError_t run_quant(const MxQuantArgs& a, int32_t* links, hipStream_t st) {
     const unsigned grid = rsq * (unsigned)cchunks * (2 * 256 / kCols);
     if (a.q) mx_quant_cols_kernel<T, NOSAT, IDX, VEC, true><<<grid, kColsThreads, 0, st>>>(a, rsq, cchunks);
     else mx_quant_cols_kernel<T, NOSAT, IDX, VEC, false><<<grid, kColsThreads, 0, st>>>(a, rsq, cchunks);
-  } else if (IDX && links) {
-    int32_t *head = links, *next = links + a.xrows;
-    mx_unlink_kernel<<<(unsigned)((a.xrows + 255) / 256), 256, 0, st>>>(head, a.xrows);
+  } else if (IDX && ws) {
+    int32_t *slots = ws, *count = ws + a.xrows * kSlots;
+    mx_clear_kernel<<<(unsigned)((a.xrows + 255) / 256), 256, 0, st>>>(count, a.xrows);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    mx_link_kernel<<<(unsigned)((a.rows + 255) / 256), 256, 0, st>>>(a, cchunks, head, next);
+    mx_slot_kernel<T, NOSAT, VEC><<<(unsigned)((a.rows + 255) / 256), 256, 0, st>>>(a, cchunks, slots, count);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const unsigned blocks = (unsigned)((a.xrows + 15) / 16) * (unsigned)((cchunks + 1) / 2);
-    mx_quant_rows_kernel<T, NOSAT, IDX, VEC, true><<<blocks, 256, 0, st>>>(a, cchunks, head, next);
+    mx_quant_rows_kernel<T, NOSAT, IDX, VEC, true><<<blocks, 256, 0, st>>>(a, cchunks, slots, count);
   } else {
     const unsigned blocks = (unsigned)((a.rows + 15) / 16) * (unsigned)((cchunks + 1) / 2);
     mx_quant_rows_kernel<T, NOSAT, IDX, VEC><<<blocks, 256, 0, st>>>(a, cchunks);
@@ -374,18 +397,18 @@ hipError_t run_quant(const MxQuantArgs& a, int32_t* links, hipStream_t st) {
 }
 
 template <int T>
-hipError_t pick_quant(const MxQuantArgs& a, bool nosat, int32_t* links, hipStream_t st) {
+hipError_t pick_quant(const MxQuantArgs& a, bool nosat, int32_t* ws, hipStream_t st) {
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * Elem<T>::kBytes % 16 == 0;
   const int sel = (nosat ? 4 : 0) + (a.src ? 2 : 0) + (vec ? 1 : 0);
   switch (sel) {
-    case 0: return run_quant<T, false, false, false>(a, links, st);
-    case 1: return run_quant<T, false, false, true>(a, links, st);
-    case 2: return run_quant<T, false, true, false>(a, links, st);
-    case 3: return run_quant<T, false, true, true>(a, links, st);
-    case 4: return run_quant<T, true, false, false>(a, links, st);
-    case 5: return run_quant<T, true, false, true>(a, links, st);
-    case 6: return run_quant<T, true, true, false>(a, links, st);
-    default: return run_quant<T, true, true, true>(a, links, st);
+    case 0: return run_quant<T, false, false, false>(a, ws, st);
+    case 1: return run_quant<T, false, false, true>(a, ws, st);
+    case 2: return run_quant<T, false, true, false>(a, ws, st);
+    case 3: return run_quant<T, false, true, true>(a, ws, st);
+    case 4: return run_quant<T, true, false, false>(a, ws, st);
+    case 5: return run_quant<T, true, false, true>(a, ws, st);
+    case 6: return run_quant<T, true, true, false>(a, ws, st);
+    default: return run_quant<T, true, true, true>(a, ws, st);
   }
 }
 
@@ -405,11 +428,11 @@ hipError_t run_dequant(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq
 
 }  // namespace
 
-hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, int32_t* links, hipStream_t stream) {
+hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, int32_t* ws, hipStream_t stream) {
   switch (xtype) {
-    case FP8BQ_BF16: return pick_quant<FP8BQ_BF16>(a, nosat, links, stream);
-    case FP8BQ_FP16: return pick_quant<FP8BQ_FP16>(a, nosat, links, stream);
-    default: return pick_quant<FP8BQ_FP32>(a, nosat, links, stream);
+    case FP8BQ_BF16: return pick_quant<FP8BQ_BF16>(a, nosat, ws, stream);
+    case FP8BQ_FP16: return pick_quant<FP8BQ_FP16>(a, nosat, ws, stream);
+    default: return pick_quant<FP8BQ_FP32>(a, nosat, ws, stream);
   }
 }
 

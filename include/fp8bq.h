@@ -449,12 +449,14 @@ int fp8bq_quant_mxfp4_1x32(const void* x, int xtype, int64_t rows, int64_t cols,
  * FP8BQ_ROW_UNUSED the row form leaves row r's codes and scales as they were (a
  * plan's buffer has many such rows behind the last expert); the column form
  * takes it for zeros like any other entry outside.
- * workspace  NULL, or 4 * (xrows + rows) bytes of device memory, 4-byte aligned,
- *          contents irrelevant (one each for calls that run at the same time).
- *          With it, and where only the row form is wanted and rows >= 2 * xrows,
- *          each row of x is read and quantised once for all the rows that show
- *          it. The result is the same.
+ * workspace  NULL, or FP8BQ_DISPATCH_WORKSPACE_ROW_BYTES * xrows bytes of device
+ *          memory, 16-byte aligned, contents irrelevant (one each for calls
+ *          that run at the same time). With it, and where only the row form is
+ *          wanted and rows >= 2 * xrows, each row of x is read and quantised
+ *          once for (up to eight of) the rows that show it. The result is the
+ *          same.
  */
+enum { FP8BQ_DISPATCH_WORKSPACE_ROW_BYTES = 36 };
 enum { FP8BQ_ROW_UNUSED = -2 };
 int fp8bq_dispatch_mxfp4_1x32(const void* x, int xtype, int64_t xrows, int64_t cols, int64_t ldx,
                               const int32_t* src, int64_t rows, void* q, int64_t ldq, void* s, int64_t lds,

@@ -46,12 +46,12 @@ int64_t grouped_gemm_decode_workspace(int, const int64_t*, int64_t, int64_t) UNR
 hipError_t launch_grouped_gemm_decode_noalloc(int, const int64_t*, int64_t, int64_t, const uint8_t*, int64_t, const float*, int64_t, const uint8_t*, int64_t, const float*, int64_t, uint16_t*, int64_t, hipStream_t) UNREACHED
 
 #define REQUIRE(c) do { if (!(c)) { std::fprintf(stderr, "launcher got: not (%s)\n", #c); std::abort(); } } while (0)
-hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool, int32_t* links, hipStream_t) {
+hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool, int32_t* ws, hipStream_t) {
   REQUIRE(a.rows > 0 && a.cols > 0 && a.ldx >= a.cols && xtype >= 0 && xtype <= 2 && (a.q || a.qt));
   REQUIRE((a.rows + 15) / 16 * ((a.cols + 255) / 256) <= (1 << 24) && (a.cols + 255) / 256 <= 16383);
   REQUIRE(!a.q || (a.ldq >= (a.cols + 255) / 256 * 128 && a.lds >= a.rows && a.s));
   REQUIRE(!a.qt || (a.ldqt >= (a.rows + 255) / 256 * 128 && a.ldst >= a.cols && a.st));
-  REQUIRE(!links || (a.src && !a.qt && a.rows >= 2 * a.xrows));
+  REQUIRE(!ws || (a.src && !a.qt && a.rows >= 2 * a.xrows));
   ++g_launches;
   return hipSuccess;
 }

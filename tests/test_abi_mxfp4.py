@@ -66,7 +66,7 @@ def test_quant_refusals(L, fn, ok):
         expect(L, fb.E_INVAL, fn, ok, a5=None)
         expect(L, fb.E_INVAL, fn, ok, a2=0)
         expect(L, fb.E_ALIGN, fn, ok, a5=O4 + 2)
-        expect(L, fb.E_ALIGN, fn, ok, a16=O4 + 2)
+        expect(L, fb.E_ALIGN, fn, ok, a16=A16 + 8)
 
 
 def test_dequant_refusals(L):

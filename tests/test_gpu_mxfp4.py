@@ -131,7 +131,8 @@ def test_dispatch(xrows, cols, rows, dtype):
 @pytest.mark.parametrize("nosat", [False, True])
 @pytest.mark.parametrize("xrows,cols,rows", [(1, 40, 2), (1, 7168, 300), (50, 300, 257), (33, 513, 1000)])
 def test_dispatch_with_a_workspace(xrows, cols, rows, dtype, nosat):
-    """Each source row read once (rows >= 2 xrows): the same codes; unused rows keep their bytes, twice over."""
+    """Each source row read once (rows >= 2 xrows), also where more rows show it than it has slots: the same codes;
+    unused rows keep their bytes, twice over."""
     import torch
     x = matrix(23, xrows, cols, dtype)
     rng = np.random.default_rng(4)
@@ -141,7 +142,7 @@ def test_dispatch_with_a_workspace(xrows, cols, rows, dtype, nosat):
     unused = src == -2
     chunks = ws.shape[0]
     d = torch.from_numpy(src).cuda()
-    work = torch.full((xrows + rows + 1,), 77, dtype=torch.int32, device="cuda")
+    work = torch.full((xrows * fb.DISPATCH_WORKSPACE_ROW_BYTES // 4 + 1,), 77, dtype=torch.int32, device="cuda")
     for _ in range(2):
         q = torch.full((rows, chunks * 128 + 16), 0xAB, dtype=torch.uint8, device="cuda")
         s = torch.full((chunks, rows + 1, 8), 0xCD, dtype=torch.uint8, device="cuda")
