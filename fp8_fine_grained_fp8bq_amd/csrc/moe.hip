@@ -370,12 +370,13 @@ __device__ __forceinline__ void probabilities(float (&v)[VPL], float (&open)[VPL
     m = wave_max(m);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      v[i] = expert_of<VPL, PACK>(lane, i) < experts && m > -INFINITY ? exp_neg(v[i] - m) : 0.f;
+      // -inf is a masked expert, also where all are (m = -inf); a NaN stays one, also where nothing else is there
+      v[i] = expert_of<VPL, PACK>(lane, i) < experts && v[i] != -INFINITY ? exp_neg(v[i] - m) : 0.f;
       sum += v[i];
     }
   }
   sum = wave_sum(sum);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;      // NaN goes to every expert
 #pragma unroll
   for (int i = 0; i < VPL; ++i) v[i] *= inv;
 }

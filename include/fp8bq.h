@@ -570,8 +570,10 @@ int fp8bq_moe_plan(const int32_t* idx, int64_t tokens, int64_t topk, int64_t ldi
  * a sequence without real tokens adding zero.
  * logits   [tokens, experts] of ltype, ldl >= experts; experts 1 .. 1024.
  *          -inf masks an expert out of a token (p = 0; a token with every
- *          expert masked has p = 0 everywhere). NaN and +inf in a real token
- *          make the results NaN. Tokens that take no part are not looked at.
+ *          expert masked has p = 0 everywhere; sigmoids below 2^-126 count as
+ *          0). A NaN (of the softmax also +inf) in a real token makes the loss
+ *          and that token's gradients NaN. Tokens that take no part are not
+ *          looked at.
  * idx      int32 [tokens, topk], ldidx >= topk.
  * seq_off  DEVICE int32 [sequences + 1], non-decreasing, or NULL for one
  *          sequence of all tokens; clamped into [0, tokens]. Tokens outside
@@ -582,8 +584,8 @@ int fp8bq_moe_plan(const int32_t* idx, int64_t tokens, int64_t topk, int64_t ldi
  *          irrelevant; calls that run at the same time need one each.
  * Sums are float32 in a fixed order: the same result at every call.
  * Errors: E_INVAL (null, sizes, score, type), E_SHAPE (experts above 1024,
- *         more than 65535 sequences, tokens at or above 2^31), E_ALIGN,
- *         E_DEVICE, E_HIP.
+ *         more than 65534 sequences, tokens or tokens * topk at or above
+ *         2^31), E_ALIGN, E_DEVICE, E_HIP.
  */
 enum { FP8BQ_SOFTMAX = 0, FP8BQ_SIGMOID = 1 };
 int fp8bq_moe_balance_workspace_size(int64_t tokens, int64_t experts, int64_t sequences, int64_t* bytes);

@@ -126,6 +126,28 @@ def test_balance_masked_experts_and_strides(score):
     assert np.abs(g - wg).max() <= 100 * 2.0 ** -24 * np.abs(wg).max() * 10
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts", [5, 64, 200])
+def test_balance_shows_a_nan(score, experts):
+    """A token whose logits are NaN, one of them or all, makes the loss and its own gradients NaN and no others'."""
+    import torch
+    rng = np.random.default_rng(experts)
+    clean = rng.normal(size=(70, experts)).astype(np.float32)
+    idx = dev(rng.integers(0, experts, (70, 2)).astype(np.int32))
+    one = torch.ones((), device="cuda")
+    _, counts, real = fb.moe_balance(dev(clean), idx, 1.0, score)
+    want = fb.moe_balance_grad(one, dev(clean), idx, counts, real, 1.0, score)
+    for where in (slice(None), slice(experts - 1, experts)):
+        x = clean.copy()
+        x[33, where] = np.nan
+        loss, c, r = fb.moe_balance(dev(x), idx, 1.0, score)
+        assert torch.isnan(loss) and (c == counts).all() and (r == real).all()
+        g = fb.moe_balance_grad(one, dev(x), idx, counts, real, 1.0, score)
+        assert torch.isnan(g[33]).all()
+        keep = torch.arange(70, device="cuda") != 33
+        assert (g[keep] == want[keep]).all()
+
+
 def test_balance_gradient_against_differences():
     import torch
     rng = np.random.default_rng(6)
@@ -206,3 +228,35 @@ def test_chain_of_a_router_with_its_experts(tokens, topk, experts, n, k):
         check(*new, out)
         eager = step(*new)
         assert all((a == b).all() for a, b in zip(out, eager))
+
+
+def test_calls_on_two_streams_at_once():
+    """Plans, dispatches (each row read once) and balance losses of two batches, side by side on two streams, many
+    times over: each stream's results are those of the batch alone."""
+    import torch
+    tokens, topk, experts, k = 2048, 4, 16, 2048
+
+    def batch(seed):
+        rng = np.random.default_rng(seed)
+        logits = dev(rng.normal(size=(tokens, experts)).astype(np.float32))
+        return matrix(seed, tokens, k), logits, torch.topk(logits, topk, 1).indices.int()
+
+    def work(x, logits, idx):
+        _, off, src, pos = fb.moe_plan(idx, experts)
+        q, s, _, _ = fb.dispatch_mxfp4_1x32(x, src)
+        rows = pos.flatten().long()
+        loss, counts, _ = fb.moe_balance(logits, idx, 0.1)
+        return off, src, pos, q[rows], s[:, rows], loss, counts
+
+    batches = [batch(1), batch(2)]
+    want = [work(*b) for b in batches]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for b, st in zip(batches, streams):
+            with torch.cuda.stream(st):
+                got.append(work(*b))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all((a == b).all() for a, b in zip(g, w))
