@@ -118,8 +118,8 @@ int check_balance(const char* who, const void* logits, int ltype, int64_t tokens
     return entry_fail(FP8BQ_E_INVAL, "%s: sizes must be positive", who);
   if (!seq_off && sequences != 1) return entry_fail(FP8BQ_E_INVAL, "%s: null seq_off with %lld sequences", who, (long long)sequences);
   if (ldl < experts || ldidx < topk) return entry_fail(FP8BQ_E_INVAL, "%s: ld too small", who);
-  if (experts > 1024 || sequences > 65534 || tokens >= kMaxSide || topk > 65535 || ldl > INT64_MAX / 4 / tokens ||
-      ldidx > INT64_MAX / 4 / tokens)
+  if (experts > 1024 || sequences > 65534 || tokens >= kMaxSide || topk >= kMaxSide || tokens * topk >= kMaxSide ||
+      ldl > INT64_MAX / 4 / tokens || ldidx > INT64_MAX / 4 / tokens)
     return entry_fail(FP8BQ_E_SHAPE, "%s: too large", who);
   if (!aligned(logits, elem_bytes(ltype)) || !aligned(idx, 4) || !aligned(seq_off, 4))
     return entry_fail(FP8BQ_E_ALIGN, "%s: misaligned pointer", who);

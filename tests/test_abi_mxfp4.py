@@ -149,6 +149,8 @@ def test_balance_refusals(L, fn, ok):
     expect(L, fb.E_SHAPE, fn, ok, **{p(9): 65535})
     expect(L, fb.E_SHAPE, fn, ok, **{p(2): BIG})
     expect(L, fb.E_SHAPE, fn, ok, **{p(4): BIG})
+    expect(L, fb.E_SHAPE, fn, ok, **{p(2): 1 << 21, p(6): 1 << 10, p(7): 1 << 10})   # an expert's count past int32
+    expect(L, fb.E_SHAPE, fn, ok, **{p(6): BIG, p(7): BIG})
     if d:
         expect(L, fb.E_INVAL, fn, ok, a16=63)
 
