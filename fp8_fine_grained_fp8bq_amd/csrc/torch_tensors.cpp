@@ -392,7 +392,14 @@ PyObject* moe_balance_grad(PyObject* const* arg) {
 // ---- the module ----------------------------------------------------------------
 
 // No C++ exception leaves a function: refusals become ValueError, statuses the
-// package's Fp8bqError, anything else (torch running out of memory) RuntimeError.
+// package's Fp8bqError, no memory left torch's OutOfMemoryError, anything else
+// RuntimeError.
+PyObject* attribute(const char* module, const char* name) {
+  PyObject* m = PyImport_ImportModule(module);
+  PyObject* a = m ? PyObject_GetAttrString(m, name) : nullptr;
+  Py_XDECREF(m);
+  return a;
+}
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) return PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", N, n);
@@ -401,15 +408,15 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const Failed& f) {
-    PyObject* pkg = PyImport_ImportModule("fp8_fine_grained_fp8bq_amd");
-    PyObject* cls = pkg ? PyObject_GetAttrString(pkg, "Fp8bqError") : nullptr;
+    PyObject* cls = attribute("fp8_fine_grained_fp8bq_amd", "Fp8bqError");
     PyObject* err = cls ? PyObject_CallFunction(cls, "sis", f.fn, f.status, fp8bq_last_error()) : nullptr;
     if (err) PyErr_SetObject(cls, err);
     Py_XDECREF(err);
     Py_XDECREF(cls);
-    Py_XDECREF(pkg);
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(PyExc_MemoryError, e.what());
+    PyObject* cls = attribute("torch", "OutOfMemoryError");
+    if (cls) PyErr_SetString(cls, e.what());
+    Py_XDECREF(cls);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
