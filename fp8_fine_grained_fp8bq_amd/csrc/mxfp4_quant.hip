@@ -101,6 +101,27 @@ __device__ __forceinline__ void load_row(const typename Elem<T>::type* row, int6
   }
 }
 
+// The same where all of the wave's groups lie inside rows of whole 16-byte
+// pieces: plain loads, which stay in flight side by side (the branches of
+// load_row make the compiler wait for each before the next). The row of !ok is
+// any that can be read, to be followed by clear_row.
+template <int T, int N>
+__device__ __forceinline__ void load_whole(const typename Elem<T>::type* row, int64_t col,
+                                           uint32_t (&w)[N * Elem<T>::kBytes / 4]) {
+  constexpr int kVecs = N * Elem<T>::kBytes / 16;
+  const uint4* p = reinterpret_cast<const uint4*>(row + col);
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint4 u = p[i];
+    w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+  }
+}
+template <int N>
+__device__ __forceinline__ void clear_row(bool ok, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = ok ? w[i] : 0;
+}
+
 // DPP moves within 16-lane rows.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
@@ -206,10 +227,18 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int c
   } else {
     xr = source<IDX>(p, r, ok, skip);
   }
+  if (skip) return;                                     // all 16 lanes of the row
   uint32_t w[2][16 * Elem<T>::kBytes / 4];
   const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
+  if (VEC && ((int64_t)chunk0 + 2) * 256 <= p.cols) {   // uniform
 #pragma unroll
-  for (int u = 0; u < 2; ++u) load_row<T, 16, VEC>(row, (int64_t)(chunk0 + u) * 256 + l16 * 16, p.cols, ok, w[u]);
+    for (int u = 0; u < 2; ++u) load_whole<T, 16>(row, (int64_t)(chunk0 + u) * 256 + l16 * 16, w[u]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) clear_row(ok, w[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_row<T, 16, VEC>(row, (int64_t)(chunk0 + u) * 256 + l16 * 16, p.cols, ok, w[u]);
+  }
   int32_t to[SLOTS ? kSlots : 1];
   if constexpr (SLOTS) {
     static_assert(kSlots % 4 == 0, "slots are read four at a time");
@@ -221,7 +250,6 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int c
   uint32_t sc[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) encode_piece<T, NOSAT>(w[u], l16, codes[u], sc[u]);
-  if (skip) return;
 #pragma unroll
   for (int i = 0; i < (SLOTS ? kSlots : 1); ++i) {
     if (i >= n) break;
@@ -258,13 +286,20 @@ __global__ __launch_bounds__(kColsThreads) void mx_quant_cols_kernel(MxQuantArgs
   const int64_t r0 = (int64_t)(sq / csq) * 256 + (sub & 1) * 128, c0 = (int64_t)(sq % csq) * 256 + (sub >> 1) * kCols;
 
   uint32_t w[kRounds][4];
-  bool skip[kRounds];
+  bool ok[kRounds], skip[kRounds];
+  const typename Elem<T>::type* row[kRounds];
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    bool ok;
-    const int64_t xr = source<IDX>(p, r0 + i * kStep + (t >> 3), ok, skip[i]);
-    const auto* row = reinterpret_cast<const typename Elem<T>::type*>(p.x) + xr * p.ldx;
-    load_row<T, kLane, VEC>(row, c0 + l8 * kLane, p.cols, ok, w[i]);
+  for (int i = 0; i < kRounds; ++i)
+    row[i] = reinterpret_cast<const typename Elem<T>::type*>(p.x) +
+             source<IDX>(p, r0 + i * kStep + (t >> 3), ok[i], skip[i]) * p.ldx;
+  if (VEC && c0 + kCols <= p.cols) {                    // uniform
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) load_whole<T, kLane>(row[i], c0 + l8 * kLane, w[i]);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) clear_row(ok[i], w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) load_row<T, kLane, VEC>(row[i], c0 + l8 * kLane, p.cols, ok[i], w[i]);
   }
 #pragma unroll
   for (int i = 0; i < kRounds; ++i)
