@@ -749,12 +749,14 @@ hipError_t run_tile(const MxGemmArgs& p, hipStream_t st) {
 // 16384 x 18432 x 7168; a tile twice as large takes less than twice the step, as
 // long as there are enough of them. Measured (us, bf16 out):
 //                       stream   64x64  64x128 128x128 128x256 256x256
-//   1 x 2048 x 7168        6.6    11.8    14.2    17.5    26.0    37.7
-//   48 x 18432 x 7168     38.8    18.2    16.0    19.2    27.9    38.9
-//   2048 x 2048 x 2048    42.8    13.2    10.8    10.1    13.3    17.9
-//   4096 x 2048 x 7168   226.6    54.5    45.5    37.2    37.2    47.5
-//   4096 x 7168 x 2048   271.1    62.4    51.6    46.6    46.9    42.5
-//   16384 x 18432 x 7168 9062     2077    1573    1193    1129     956
+//   1 x 2048 x 7168        6.8    11.7    13.0    15.3    26.5    38.8
+//   48 x 18432 x 7168     39.5    17.9    14.9    17.0    29.7    40.0
+//   1000 x 4096 x 7168   114.5    32.7    28.6    21.2    31.1    42.4
+//   2048 x 2048 x 2048    41.1    13.7    12.8     9.2    12.5    17.5
+//   4096 x 2048 x 7168   226.9    62.0    52.8    38.3    35.6    45.1
+//   4096 x 7168 x 2048   271.4    70.0    63.4    48.3    47.3    42.5
+//   16384 x 18432 x 7168  9031    2102    1696    1227    1176     987
+// (64 x 64, 64 x 128 and up to 256 tiles of 128 x 128 with loading waves.)
 struct Tiling { int bm, bn, step, store; };
 constexpr Tiling kTilings[] = {{32, 32, 25, 0}, {64, 64, 33, 40}, {64, 128, 42, 70}, {128, 128, 57, 130},
                                {128, 256, 100, 250}, {256, 256, 170, 500}};

@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256) void mx_slot_kernel(MxQuantArgs p, int chunks,
 // contiguous bytes of bf16), so a lane's codes are one 8-byte store; each lane
 // takes the same place of two neighbouring chunks, all loads before any
 // arithmetic. A block takes 16 rows of a chunk pair, the pairs of a row run
-// fastest over the grid. SLOTS: rows of x, each written to the rows in its slots.
+// fastest over the grid. 16384 x 7168 bf16: 44 us, 6.7 TB/s. SLOTS: rows of x, each written to the rows in its slots.
 template <int T, bool NOSAT, bool IDX, bool VEC, bool SLOTS = false>
 __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int chunks, const int32_t* slots = nullptr,
                                                             const int32_t* count = nullptr) {
@@ -267,7 +267,11 @@ __global__ __launch_bounds__(256) void mx_quant_rows_kernel(MxQuantArgs p, int c
 // grid covers whole 256 x 256 squares of the matrix (what lies past it is
 // zeros); the blocks of a square run on one XCD, one after the other, so that
 // the pieces of code rows that they write (32 bytes of a row, 64 of a column)
-// meet as full lines in its L2. The squares run over the columns first.
+// meet as full lines in its L2. The squares run over the columns first. Bound
+// by its phases (a block reads, then computes, then writes) with eight blocks on
+// a CU: both forms of 16384 x 7168 bf16 in 72 us (5.0 TB/s; the row form alone 44,
+// 6.7), of 4096 x 7168 in 18. Persistent blocks that read the next tile during
+// this one's columns: 90 and 17.6; 128 x 128 tiles: 4.2 TB/s.
 constexpr int kColsThreads = 256;
 template <int T, bool NOSAT, bool IDX, bool VEC, bool ROWS>
 __global__ __launch_bounds__(kColsThreads) void mx_quant_cols_kernel(MxQuantArgs p, unsigned rsq, unsigned csq) {
