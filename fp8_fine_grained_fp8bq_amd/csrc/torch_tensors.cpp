@@ -153,14 +153,16 @@ struct Mx {
         (d && (qt.size(0) != groups || st.size(0) != groups)))
       refuse(name, ": codes ", qt.sizes(), " do not go with scales ", st.sizes());
     k = width * 2;
-    ldq = ld(qt);
+    // torch leaves the stride of a single row open: where every group is one row, the distance between groups counts
+    ldq = rows > 1 ? qt.stride(-2) : d && groups > 1 ? qt.stride(0) : width;
     lds = rows;
+    if (d && groups > 1 && (qt.stride(0) != rows * ldq || ldq < width))
+      refuse(name, ": the groups' codes must follow one another");
     if (!qt.is_contiguous() || !st.is_contiguous()) {
       if (qt.stride(-1) != 1 || st.stride(-1) != 1 || (rows > 1 && st.stride(-2) != 8) ||
           (chunks > 1 && st.stride(-3) % 8))
         refuse(name, ": codes must be row-major and scales [chunks, rows, 8] with rows contiguous");
-      if (d && (!st.is_contiguous() || (groups > 1 && qt.stride(0) != rows * ldq)))
-        refuse(name, ": the groups' codes and scales must follow one another");
+      if (d && !st.is_contiguous()) refuse(name, ": the groups' scales must follow one another");
       if (chunks > 1) lds = st.stride(-3) / 8;
     }
     q = qt.data_ptr();
