@@ -302,10 +302,12 @@ PyObject* grouped_wgrad(PyObject* const* arg) {
   int otype;
   const Tensor out = output(given, {groups, x.rows, y.rows}, dtype_arg(arg[6]), at::kFloat, on, otype);
   if (groups > 256) refuse("at most 256 groups, got ", groups);
-  if (groups > 1 && out.stride(0) != x.rows * ld(out)) refuse("the experts' gradients must follow one another in out");
+  const int64_t ldo = groups > 1 && x.rows == 1 ? out.stride(0) : ld(out);    // a single row's stride is open
+  if (groups > 1 && (out.stride(0) != x.rows * ldo || ldo < y.rows))
+    refuse("the experts' gradients must follow one another in out");
   check("fp8bq_grouped_wgrad_mxfp4",
         fp8bq_grouped_wgrad_mxfp4((int32_t)groups, off.data_ptr<int32_t>(), x.rows, y.rows, x.k, x.q, x.ldq, x.s, x.lds,
-                                  y.q, y.ldq, y.s, y.lds, out.data_ptr(), otype, ld(out), on.stream));
+                                  y.q, y.ldq, y.s, y.lds, out.data_ptr(), otype, ldo, on.stream));
   return wrap(out);
 }
 

@@ -6,7 +6,7 @@ import pytest
 
 import fp8_fine_grained_fp8bq_amd as fb
 from tests.gpu_util import log
-from tests.mx_util import check_product, f64, operand
+from tests.mx_util import check_product, codes, f64, operand, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,30 @@ def test_one_row_of_any_stride():
         out = fb.gemm_mxfp4(a.as_strided(a.shape, (stride, 1)), sa, b.as_strided(b.shape, (stride, 1)), sb,
                             dtype=torch.float32)
         check_product(f64(out), va, vb, k, "float32")
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n,gap", [(70, 0), (64, 8), (257, 3)])
+def test_gradients_of_one_row(n, gap, dtype):
+    """Experts' gradients [G, 1, n] in an output whose dimension of one has any stride: written at the distance between
+    groups, nothing between them touched."""
+    import torch
+    groups = 3
+    rng = np.random.default_rng(2)
+    rows = 256 * groups
+    off = torch.arange(0, rows + 1, 256, dtype=torch.int32, device="cuda")
+    a, sa, _, _ = fb.quant_mxfp4_1x32(torch.from_numpy(rng.normal(size=(1, rows))).float().cuda())
+    b, sb, _, _ = fb.quant_mxfp4_1x32(torch.from_numpy(rng.normal(size=(n, rows))).float().cuda())
+    va, vb = codes(a, sa, rows), codes(b, sb, rows)
+    for one in (n + gap, groups * (n + gap), 1, 5):
+        buf = torch.full((groups * (n + gap),), 768.0, dtype=torch_dtype(dtype), device="cuda")
+        out = buf.as_strided((groups, 1, n), (n + gap, one, 1))
+        fb.grouped_wgrad_mxfp4(off, a, sa, b, sb, out=out)
+        got = f64(out)
+        for e in range(groups):
+            part = slice(256 * e, 256 * e + 256)
+            check_product(got[e], va[:, part], vb[:, part], 256, dtype)
+        assert (buf.view(groups, n + gap)[:, n:] == 768.0).all()
+    for strides in ((0, n, 1), (n - 1, n, 1)):
+        with pytest.raises(ValueError, match="follow one another"):
+            fb.grouped_wgrad_mxfp4(off, a, sa, b, sb, out=buf.as_strided((groups, 1, n), strides))
