@@ -30,10 +30,15 @@ int launched(hipError_t e, const char* what) {
   return FP8BQ_OK;
 }
 
-// Grids of the quantisers: 16 rows of a chunk per 256-thread block, below 2^32
-// threads; at most 65532 blocks of 64 columns.
+// Grids have fewer than 2^32 threads, that is 2^24 blocks of 256. Row form and
+// read-back: at most one block for 16 rows of a chunk.
 bool too_large(int64_t rows, int64_t cols) {
   return rows >= kMaxSide || chunks_of(cols) > 16383 || ((rows - 1) / 16 + 1) * chunks_of(cols) >= ((int64_t)1 << 24);
+}
+// Column form: whole 256 x 256 squares in blocks of 128 rows of 128 bytes
+// (rows and cols as too_large leaves them).
+bool too_large_by_columns(int64_t rows, int64_t cols, int xtype) {
+  return ((rows - 1) / 256 + 1) * chunks_of(cols) * (4 * elem_bytes(xtype)) >= ((int64_t)1 << 24);
 }
 
 // One code matrix [rows, k] with its scales.
@@ -65,7 +70,8 @@ int quant(const char* who, const void* x, int xtype, int64_t xrows, int64_t cols
     if (int e = check_codes(who, "the row form", q, ldq, s, lds, rows, cols)) return e;
   if (qt || st)
     if (int e = check_codes(who, "the transposed form", qt, ldqt, st, ldst, cols, rows)) return e;
-  if (too_large(xrows, cols)) return entry_fail(FP8BQ_E_SHAPE, "%s: too large", who);
+  if (too_large(xrows, cols) || ((qt || st) && too_large_by_columns(rows, cols, xtype)))
+    return entry_fail(FP8BQ_E_SHAPE, "%s: too large", who);
   if (!aligned(x, elem_bytes(xtype)) || !aligned(src, 4) || !aligned(ws, 16))
     return entry_fail(FP8BQ_E_ALIGN, "%s: x must be aligned to its element, src to 4 bytes, workspace to 16", who);
   if (int e = fp8bq::entry_device()) return e;
