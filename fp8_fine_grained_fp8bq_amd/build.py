@@ -1,5 +1,6 @@
-"""Builds libfp8bq.so (HIP kernels + C ABI) for gfx950 with hipcc, and the tensor
-layer's extension module _tensors.so with g++, in-tree.
+"""Builds libfp8bq.so (HIP kernels + C ABI) for gfx950 with hipcc, and, where torch
+for ROCm and g++ are there, the tensor layer's extension module _tensors.so,
+in-tree.
 
 Usage: python -m fp8_fine_grained_fp8bq_amd.build   (or call build()).
 """
@@ -44,8 +45,12 @@ def hipcc() -> str:
 
 def tensors_command(out: str) -> list:
     """The g++ line of the extension module: host code over torch's headers, linked
-    to libfp8bq.so beside it."""
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    to libfp8bq.so beside it. Empty where g++ or a torch for ROCm is missing: the C
+    library and its pointer-level binding need neither."""
+    spec = importlib.util.find_spec("torch")
+    torch = list(spec.submodule_search_locations)[0] if spec is not None else ""
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_hip.so")) or shutil.which("g++") is None:
+        return []
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall", "-Wno-deprecated-declarations",
             "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-I{torch}/include", f"-I{torch}/include/torch/csrc/api/include",
             "-I/opt/rocm/include", f"-I{sysconfig.get_paths()['include']}", f"-I{os.path.join(ROOT, 'include')}",
@@ -55,7 +60,7 @@ def tensors_command(out: str) -> list:
 
 def build(verbose: bool = False) -> str:
     """Compile every source into libfp8bq.so and the probes into
-    libfp8bq_probe.so, then the extension module (always recompiles). The sources
+    libfp8bq_probe.so, then the extension module where torch is there (always recompiles). The sources
     compile in parallel to objects, which are then linked."""
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -86,7 +91,20 @@ def build(verbose: bool = False) -> str:
             sys.stderr.write(res.stdout + res.stderr)
             raise RuntimeError(f"hipcc link failed with exit code {res.returncode}")
         os.replace(tmp, lib)
+    build_tensors(verbose)
+    return LIB
+
+
+def build_tensors(verbose: bool = False) -> None:
+    """Compile the extension module. Where it cannot be built, one of earlier sources
+    is removed, so that the tensor layer says that it is missing."""
     cmd = tensors_command(TENSORS_LIB + ".tmp")
+    if not cmd:
+        print("fp8bq: _tensors.so not built (needs torch for ROCm and g++); the MXFP4 and routing calls on torch tensors are "
+              "not available", file=sys.stderr, flush=True)
+        if os.path.exists(TENSORS_LIB):
+            os.remove(TENSORS_LIB)
+        return
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -94,7 +112,6 @@ def build(verbose: bool = False) -> str:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"g++ failed on torch_tensors.cpp with exit code {res.returncode}")
     os.replace(TENSORS_LIB + ".tmp", TENSORS_LIB)
-    return LIB
 
 
 if __name__ == "__main__":
