@@ -304,12 +304,16 @@ __device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, [](fl
 __device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
 
 // e^x for x <= 0: 2^t of t = x log2(e), times 1 + what t's rounding left over
-// (which is up to |x| 2^-24 of the result).
+// (which is up to |x| 2^-24 of the result), log2(e) and ln 2 being the
+// mathematical constants to double precision and the low part of log2(e) what
+// its rounding to float leaves.
+constexpr double kLog2E = 1.44269504088896340736, kLn2 = 0.69314718055994530942;
+constexpr float kLog2EHigh = (float)kLog2E, kLog2ELow = (float)(kLog2E - (double)kLog2EHigh);
 __device__ __forceinline__ float exp_neg(float x) {
-  const float t = x * 0x1.715476p+0f;
-  const float rest = __builtin_fmaf(x, 0x1.715476p+0f, -t) + x * 0x1.4ae0bep-26f;
+  const float t = x * kLog2EHigh;
+  const float rest = __builtin_fmaf(x, kLog2EHigh, -t) + x * kLog2ELow;
   const float r = __builtin_amdgcn_exp2f(t);
-  return t < -126.f ? 0.f : __builtin_fmaf(r, rest * 0x1.62e430p-1f, r);
+  return t < -126.f ? 0.f : __builtin_fmaf(r, rest * (float)kLn2, r);
 }
 
 // Tokens of sequence s, clamped into the batch; s == sequences: nothing here.
