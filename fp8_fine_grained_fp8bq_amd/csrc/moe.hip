@@ -544,62 +544,80 @@ __global__ __launch_bounds__(64 * kFinalWaves) void balance_final_kernel(MoeBala
   if (tid == 0) *loss = (float)(red[0] * (double)a.coef / a.sequences);
 }
 
-// Gradient. Block (piece, sequence), a wave per token; the lane's coefficients
-// dloss * coef / S * experts * c / (topk * n^2) stay in registers. Block row
-// `sequences` clears the tokens outside every sequence.
+// The sequence of token t (0 <= t < tokens): the last one that begins at or before
+// it; -1 before the first, `sequences` behind the last. end: the first token
+// that is not t's neighbour there, above t. The wave looks at 64 offsets at a
+// time, the last ones of 64 equal stretches of the table.
+__device__ __forceinline__ int sequence_of(const MoeBalanceArgs& a, int64_t t, int64_t& end) {
+  end = a.tokens;
+  if (!a.seq_off) return 0;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.sequences + 1;                     // offsets before lo are <= t, those from lo + n on are above
+  while (n > 0) {
+    const int step = (n + 63) / 64, i = lane * step + step - 1;
+    const int c = __popcll(__ballot(i < n && (int64_t)a.seq_off[lo + (i < n ? i : 0)] <= t)) * step;
+    lo += c;
+    n = min(step - 1, n - c);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  if (lo <= a.sequences) end = min(max((int64_t)a.seq_off[lo], t + 1), a.tokens);
+  return lo - 1;
+}
+
+// Gradient. Each wave takes a contiguous run of the batch's tokens, whatever
+// sequences they are of (65536 tokens of 64 experts in 1000 sequences: 20 us
+// where blocks of their own for each sequence took 912; in one long and 1000
+// short ones 35 against 8139); of each that it meets, the lane's coefficients
+// dloss * coef / S * experts * c / (topk * n^2) stay in registers. Tokens outside
+// every sequence are cleared.
 template <int T, bool SIG, int VPL, bool PACK>
-__global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanceArgs a, int pieces, const float* dloss,
+__global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanceArgs a, int64_t run, const float* dloss,
                                                                       const int32_t* counts, const int32_t* real,
                                                                       void* dlogits, int64_t lddl) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int s = blockIdx.y;
-  if (s == a.sequences) {
-    int64_t lo, hi, end;
-    seq_range(a, 0, lo, end);
-    seq_range(a, a.sequences - 1, end, hi);
-    for (int64_t t = (int64_t)blockIdx.x * kGradWaves + wave; t < a.tokens; t += (int64_t)pieces * kGradWaves) {
-      if (t >= lo && t < hi) continue;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t first = ((int64_t)blockIdx.x * kGradWaves + wave) * run, last = min(first + run, a.tokens);
+  for (int64_t t = first; t < last;) {
+    int64_t end;
+    const int s = sequence_of(a, t, end);
+    end = min(end, last);
+    if (s < 0 || s >= a.sequences) {
       const float zero[VPL] = {};
-      store_logits<T, VPL, PACK>(dlogits, t * lddl, a.experts, zero);
+      for (; t < end; ++t) store_logits<T, VPL, PACK>(dlogits, t * lddl, a.experts, zero);
+      continue;
     }
-    return;
-  }
-  int64_t lo, hi;
-  seq_range(a, s, lo, hi);
-  const int64_t per = (hi - lo + pieces - 1) / pieces;
-  const int64_t t0 = lo + (int64_t)blockIdx.x * per, t1 = min(t0 + per, hi);
-  if (t0 >= t1) return;
-  const float n = (float)max(real[s], 1);
-  const float scale = dloss[0] * (a.coef / a.sequences) * ((float)a.experts / ((float)a.topk * n)) / n;
-  float f[VPL];
+    const float n = (float)max(real[s], 1);
+    const float scale = dloss[0] * (a.coef / a.sequences) * ((float)a.experts / ((float)a.topk * n)) / n;
+    float f[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    f[i] = expert_of<VPL, PACK>(lane, i) < a.experts
-               ? scale * counts[(int64_t)s * a.experts + expert_of<VPL, PACK>(lane, i)] : 0.f;
-  auto take = [&](TokenRow<T, VPL, PACK>& row, int64_t t) {
-    const bool ok = real_token(a, t, row.first, [](int) {});
-    float (&v)[VPL] = row.v;
-    float open[VPL];
-    probabilities<SIG, VPL, PACK>(v, open, a.experts);
-    float dot = 0.f;
+    for (int i = 0; i < VPL; ++i)
+      f[i] = expert_of<VPL, PACK>(lane, i) < a.experts
+                 ? scale * counts[(int64_t)s * a.experts + expert_of<VPL, PACK>(lane, i)] : 0.f;
+    auto take = [&](TokenRow<T, VPL, PACK>& row, int64_t at) {
+      const bool ok = real_token(a, at, row.first, [](int) {});
+      float (&v)[VPL] = row.v;
+      float open[VPL];
+      probabilities<SIG, VPL, PACK>(v, open, a.experts);
+      float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) dot += v[i] * f[i];
-    dot = wave_sum(dot);
+      for (int i = 0; i < VPL; ++i) dot += v[i] * f[i];
+      dot = wave_sum(dot);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      float d = v[i] * (f[i] - dot);
-      if constexpr (SIG) d *= open[i];
-      v[i] = ok ? d : 0.f;
+      for (int i = 0; i < VPL; ++i) {
+        float d = v[i] * (f[i] - dot);
+        if constexpr (SIG) d *= open[i];
+        v[i] = ok ? d : 0.f;
+      }
+      store_logits<T, VPL, PACK>(dlogits, at * lddl, a.experts, v);
+    };
+    for (; t < end; t += 2) {
+      TokenRow<T, VPL, PACK> x, y;
+      x.load(a, t);
+      const bool two = t + 1 < end;                     // uniform in the wave
+      if (two) y.load(a, t + 1);
+      take(x, t);
+      if (two) take(y, t + 1);
     }
-    store_logits<T, VPL, PACK>(dlogits, t * lddl, a.experts, v);
-  };
-  for (int64_t t = t0 + wave; t < t1; t += 2 * kGradWaves) {
-    TokenRow<T, VPL, PACK> x, y;
-    x.load(a, t);
-    const bool two = t + kGradWaves < t1;             // uniform in the wave
-    if (two) y.load(a, t + kGradWaves);
-    take(x, t);
-    if (two) take(y, t + kGradWaves);
+    t = end;
   }
 }
 
@@ -614,9 +632,10 @@ hipError_t run_balance(const MoeBalanceArgs& a, float* loss, int32_t* counts, in
 template <int T, bool SIG, int VPL, bool PACK>
 hipError_t run_grad(const MoeBalanceArgs& a, const float* dloss, const int32_t* counts, const int32_t* real,
                     void* dlogits, int64_t lddl, hipStream_t st) {
-  const int pieces = balance_pieces(a.tokens, a.sequences, kGradWaves);
-  balance_grad_kernel<T, SIG, VPL, PACK><<<dim3(pieces, a.sequences + 1), 64 * kGradWaves, 0, st>>>(a, pieces, dloss, counts,
-                                                                                             real, dlogits, lddl);
+  // about 4096 waves, of at least two tokens each
+  const int64_t run = a.tokens > 2 * 4096 ? (a.tokens + 4095) / 4096 : 2;
+  const unsigned blocks = (unsigned)((a.tokens + run * kGradWaves - 1) / (run * kGradWaves));
+  balance_grad_kernel<T, SIG, VPL, PACK><<<blocks, 64 * kGradWaves, 0, st>>>(a, run, dloss, counts, real, dlogits, lddl);
   return hipGetLastError();
 }
 
