@@ -544,47 +544,68 @@ __global__ __launch_bounds__(64 * kFinalWaves) void balance_final_kernel(MoeBala
   if (tid == 0) *loss = (float)(red[0] * (double)a.coef / a.sequences);
 }
 
-// The sequence of token t (0 <= t < tokens): the last one that begins at or before
-// it; -1 before the first, `sequences` behind the last. end: the first token
-// that is not t's neighbour there, above t. The wave looks at 64 offsets at a
-// time, the last ones of 64 equal stretches of the table.
-__device__ __forceinline__ int sequence_of(const MoeBalanceArgs& a, int64_t t, int64_t& end) {
-  end = a.tokens;
-  if (!a.seq_off) return 0;
-  const int lane = threadIdx.x & 63;
-  int lo = 0, n = a.sequences + 1;                     // offsets before lo are <= t, those from lo + n on are above
-  while (n > 0) {
-    const int step = (n + 63) / 64, i = lane * step + step - 1;
-    const int c = __popcll(__ballot(i < n && (int64_t)a.seq_off[lo + (i < n ? i : 0)] <= t)) * step;
-    lo += c;
-    n = min(step - 1, n - c);
+// The batch's table of offsets as a wave sees it; up to 63 sequences' offsets sit
+// in its lanes from one load.
+struct Sequences {
+  const int32_t* off;
+  int count, mine;
+  int64_t tokens;
+  __device__ __forceinline__ explicit Sequences(const MoeBalanceArgs& a)
+      : off(a.seq_off), count(a.sequences), mine(0x7FFFFFFF), tokens(a.tokens) {
+    const int lane = threadIdx.x & 63;
+    if (off && count < 64 && lane <= count) mine = off[lane];
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  if (lo <= a.sequences) end = min(max((int64_t)a.seq_off[lo], t + 1), a.tokens);
-  return lo - 1;
-}
+  // Offset s, within the batch.
+  __device__ __forceinline__ int64_t at(int s) const {
+    if (!off) return s == 0 ? 0 : tokens;
+    const int64_t v = count < 64 ? __builtin_amdgcn_readlane(mine, s) : off[s];
+    return min(max(v, (int64_t)0), tokens);
+  }
+  // The sequence of token t (0 <= t < tokens): the last one that begins at or
+  // before it; -1 before the first, `count` behind the last. end: the first
+  // token above t that is not of it. A longer table is searched 64 offsets at a
+  // time, the last ones of 64 equal stretches.
+  __device__ __forceinline__ int of(int64_t t, int64_t& end) const {
+    end = tokens;
+    if (!off) return 0;
+    int next = 0;                                      // offsets at or before t
+    if (count < 64) {
+      next = __popcll(__ballot((int64_t)mine <= t));
+    } else {
+      const int lane = threadIdx.x & 63;
+      for (int n = count + 1; n > 0;) {                // the first one above t is among the n from `next` on, or behind
+        const int step = (n + 63) / 64, i = lane * step + step - 1;
+        const int c = __popcll(__ballot(i < n && (int64_t)off[next + (i < n ? i : 0)] <= t)) * step;
+        next += c;
+        n = min(step - 1, n - c);
+      }
+    }
+    next = __builtin_amdgcn_readfirstlane(next);
+    if (next <= count) end = min(max(at(next), t + 1), tokens);
+    return next - 1;
+  }
+};
 
-// Gradient. Each wave takes a contiguous run of the batch's tokens, whatever
-// sequences they are of (65536 tokens of 64 experts in 1000 sequences: 20 us
-// where blocks of their own for each sequence took 912; in one long and 1000
-// short ones 35 against 8139); of each that it meets, the lane's coefficients
-// dloss * coef / S * experts * c / (topk * n^2) stay in registers. Tokens outside
-// every sequence are cleared.
+// Gradient. Each wave takes a contiguous run of the sequences' tokens, whatever
+// their lengths (65536 tokens of 64 experts in 1000 sequences: 19 us where blocks
+// of their own for each sequence took 903; 2^20 tokens: 237 against 14417); of
+// each sequence that it meets, the lane's coefficients dloss * coef / S * experts *
+// c / (topk * n^2) stay in registers. The tokens outside every sequence, which get
+// zeros, are dealt out beside that (half of 2^20 tokens outside: 137 us, 198 where
+// they were part of the runs).
 template <int T, bool SIG, int VPL, bool PACK>
-__global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanceArgs a, int64_t run, const float* dloss,
+__global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanceArgs a, const float* dloss,
                                                                       const int32_t* counts, const int32_t* real,
                                                                       void* dlogits, int64_t lddl) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t first = ((int64_t)blockIdx.x * kGradWaves + wave) * run, last = min(first + run, a.tokens);
-  for (int64_t t = first; t < last;) {
-    int64_t end;
-    const int s = sequence_of(a, t, end);
+  const Sequences seq(a);
+  const int64_t begin = seq.at(0), stop = max(seq.at(a.sequences), begin);
+  const int64_t id = (int64_t)blockIdx.x * kGradWaves + wave, waves = (int64_t)gridDim.x * kGradWaves;
+  const int64_t run = (stop - begin + waves - 1) / waves, first = begin + id * run, last = min(first + run, stop);
+  for (int64_t t = first, end; t < last; t = end) {
+    const int s = seq.of(t, end);
     end = min(end, last);
-    if (s < 0 || s >= a.sequences) {
-      const float zero[VPL] = {};
-      for (; t < end; ++t) store_logits<T, VPL, PACK>(dlogits, t * lddl, a.experts, zero);
-      continue;
-    }
+    if (s < 0 || s >= a.sequences) continue;            // only with offsets that decrease
     const float n = (float)max(real[s], 1);
     const float scale = dloss[0] * (a.coef / a.sequences) * ((float)a.experts / ((float)a.topk * n)) / n;
     float f[VPL];
@@ -617,7 +638,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanc
       take(x, t);
       if (two) take(y, t + 1);
     }
-    t = end;
+  }
+  for (int64_t u = id; u < a.tokens - (stop - begin); u += waves) {
+    const float zero[VPL] = {};
+    store_logits<T, VPL, PACK>(dlogits, (u < begin ? u : stop + (u - begin)) * lddl, a.experts, zero);
   }
 }
 
@@ -635,7 +659,7 @@ hipError_t run_grad(const MoeBalanceArgs& a, const float* dloss, const int32_t* 
   // about 4096 waves, of at least two tokens each
   const int64_t run = a.tokens > 2 * 4096 ? (a.tokens + 4095) / 4096 : 2;
   const unsigned blocks = (unsigned)((a.tokens + run * kGradWaves - 1) / (run * kGradWaves));
-  balance_grad_kernel<T, SIG, VPL, PACK><<<blocks, 64 * kGradWaves, 0, st>>>(a, run, dloss, counts, real, dlogits, lddl);
+  balance_grad_kernel<T, SIG, VPL, PACK><<<blocks, 64 * kGradWaves, 0, st>>>(a, dloss, counts, real, dlogits, lddl);
   return hipGetLastError();
 }
 

@@ -582,7 +582,11 @@ int fp8bq_moe_plan(const int32_t* idx, int64_t tokens, int64_t topk, int64_t ldi
  *          int32 [sequences]: n_s.
  * workspace  fp8bq_moe_balance_workspace_size bytes, 4-byte aligned, contents
  *          irrelevant; calls that run at the same time need one each.
- * Sums are float32 in a fixed order: the same result at every call.
+ * Sums are float32 in a fixed order: the same result at every call. The work is
+ * dealt to blocks by the sequences' average length (256 / sequences blocks each,
+ * one at least), so one long sequence among hundreds of short ones is slow: a
+ * million tokens of 64 experts in 1000 equal sequences take 0.18 ms, in one long
+ * and 1000 short ones 45 (the gradient 0.24 and 0.6).
  * Errors: E_INVAL (null, sizes, score, type), E_SHAPE (experts above 1024,
  *         more than 65534 sequences, tokens or tokens * topk at or above
  *         2^31), E_ALIGN, E_DEVICE, E_HIP.
