@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mxfp4_tiling.h"
+
 namespace fp8bq {
 
 // Launchers. Arguments have been validated by the entry points; each returns
@@ -28,8 +30,6 @@ constexpr int kMxDispatchSlots = 8;
 hipError_t launch_quant_mxfp4(const MxQuantArgs& a, int xtype, bool nosat, int32_t* ws, hipStream_t stream);
 hipError_t launch_dequant_mxfp4(const uint8_t* q, int64_t rows, int64_t cols, int64_t ldq, const uint8_t* s,
                                 int64_t lds, void* y, int ytype, int64_t ldy, hipStream_t stream);
-
-enum MxMode { MX_DENSE = 0, MX_ROWS = 1, MX_K = 2 };   // one product; rows grouped; K grouped
 
 // a [m, k], b [n, k] per group. chunks = ceil(k / 256); MX_K: chunks the
 // buffers hold, a group's own come from row_off.

@@ -742,63 +742,13 @@ hipError_t run_tile(const MxGemmArgs& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Which kernel. A product's time is close to rounds x (chunks x step + store)
-// + launch, where a round is one tile on each of the 256 CUs (several
-// workgroups of the small tilings share a CU; their steps then take turns).
-// Step and store times in units of 10 ns, from products of 1 x 2048 x 7168 to
-// 16384 x 18432 x 7168; a tile twice as large takes less than twice the step, as
-// long as there are enough of them. Measured (us, bf16 out):
-//                       stream   64x64  64x128 128x128 128x256 256x256
-//   1 x 2048 x 7168        6.8    11.7    13.0    15.3    26.5    38.8
-//   48 x 18432 x 7168     39.5    17.9    14.9    17.0    29.7    40.0
-//   1000 x 4096 x 7168   114.5    32.7    28.6    21.2    31.1    42.4
-//   2048 x 2048 x 2048    41.1    13.7    12.8     9.2    12.5    17.5
-//   4096 x 2048 x 7168   226.9    62.0    52.8    38.3    35.6    45.1
-//   4096 x 7168 x 2048   271.4    70.0    63.4    48.3    47.3    42.5
-//   16384 x 18432 x 7168  9031    2102    1696    1227    1176     987
-// (64 x 64, 64 x 128 and up to 256 tiles of 128 x 128 with loading waves.)
-struct Tiling { int bm, bn, step, store; };
-constexpr Tiling kTilings[] = {{32, 32, 25, 0}, {64, 64, 33, 40}, {64, 128, 42, 70}, {128, 128, 57, 130},
-                               {128, 256, 100, 250}, {256, 256, 170, 500}};
-
-// The tiling with the least estimated time for `groups` products of rows x n x
-// chunks each (an expert's rows are taken as their average: only the device
-// knows the counts).
-int pick_tiling(int64_t groups, int64_t rows, int64_t n, int64_t chunks) {
-  int best = 5;
-  double least = 0;
-  for (int i = 0; i < 6; ++i) {
-    const Tiling& t = kTilings[i];
-    const int64_t tiles = groups * ((rows + t.bm - 1) / t.bm) * ((n + t.bn - 1) / t.bn);
-    const double time = (double)((tiles + 255) / 256) * (double)(chunks * t.step + t.store);
-    if (i == 0 && tiles > 65536) continue;           // one workgroup per tile: keep the launch's thread count in range
-    if (least == 0 || time < least) {
-      best = i;
-      least = time;
-    }
-  }
-  return best;
-}
-
 template <int MODE, bool F32>
 hipError_t run(const MxGemmArgs& p, hipStream_t st) {
-  // Experts: their rows (or chunks of K) as the average of what the buffers
-  // hold. Rows count half of that: a plan's buffer has room for every choice of
-  // every token, many of which may be other GPUs' experts, and too large a tile
-  // costs more than too small a one (8 experts with 57 .. 232 rows in a buffer
-  // of 2048, n = 2048, k = 7168: 20.8 us with 64 x 128, 33.5 with 128 x 128).
-  const int64_t g = MODE == MX_DENSE ? 1 : p.groups;
-  const int64_t rows = MODE == MX_ROWS ? (p.m + 2 * g - 1) / (2 * g) : p.m;
-  const int64_t chunks = MODE == MX_K ? (p.chunks + g - 1) / g : p.chunks;
-  int pick = pick_tiling(g, rows, p.n, chunks);
-  // one 128 x 128 tile per CU or less: loading waves and a third stage hide more
-  // latency (1000 x 4096 x 7168: 22.5 against 25.9 us); with more, two workgroups
-  // per CU do better (4096 x 2048 x 7168: 37.2 against 38.8)
-  const bool deep = g * ((rows + 127) / 128) * ((p.n + 127) / 128) <= 256;
-  switch (pick) {
+  const MxPick pick = mx_pick((MxMode)MODE, p.groups, p.m, p.n, p.chunks);
+  switch (pick.tiling) {
     case 1: return run_tile<MODE, F32, 1, 1, 3, true>(p, st);
     case 2: return run_tile<MODE, F32, 1, 2, 3, true>(p, st);
-    case 3: return deep ? run_tile<MODE, F32, 2, 2, 3, true>(p, st) : run_tile<MODE, F32, 2, 2, 2, false>(p, st);
+    case 3: return pick.deep ? run_tile<MODE, F32, 2, 2, 3, true>(p, st) : run_tile<MODE, F32, 2, 2, 2, false>(p, st);
     case 4: return run_tile<MODE, F32, 2, 4, 2, false>(p, st);
     case 5: return run_tile<MODE, F32, 4, 4, 2, false>(p, st);
   }
