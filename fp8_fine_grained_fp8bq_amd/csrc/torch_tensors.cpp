@@ -211,10 +211,12 @@ PyObject* quant(PyObject* const* arg) {
   auto p = [](const std::optional<Tensor>& t) { return t ? t->data_ptr() : nullptr; };
   auto l = [](const std::optional<Tensor>& t) { return t ? t->size(1) : 0; };
   if (src) {
-    // Rows that several experts get are read once where that is worth two more launches: 16384 tokens of 7168, 131072
-    // choices of which 54066 are here: 83 us against 203.
+    // Rows that several experts get are read once where that is worth two more launches, which only the sizes tell here.
+    // Gathered / by slots, us, top-8 of 8 experts here, of 20 and of 256: 4096 x 1024 9.6 / 13.3, 5.5 / 9.9, 3.4 / 7.9; 4096 x
+    // 2048 15.7 / 17.9, 9.2 / 12.1, 4.3 / 8.5; 2048 x 7168 31.4 / 22.5, 17.2 / 16.0, 5.8 / 9.1; 16384 x 1024 35.7 / 27.0,
+    // 20.0 / 17.6, 6.4 / 9.4; 16384 x 7168 246 / 163, 131 / 91, 39 / 23.
     std::optional<Tensor> ws;
-    if (!colwise && rows >= 2 * xrows && xrows * cols >= (1 << 22))
+    if (!colwise && rows >= 2 * xrows && xrows * cols >= (12 << 20))
       ws = on.empty({xrows * (FP8BQ_DISPATCH_WORKSPACE_ROW_BYTES / 4)}, at::kInt);
     check("fp8bq_dispatch_mxfp4_1x32",
           fp8bq_dispatch_mxfp4_1x32(x.data_ptr(), xtype, xrows, cols, ld(x), src->data_ptr<int32_t>(), rows, p(q), l(q),
