@@ -466,7 +466,9 @@ int fp8bq_dispatch_mxfp4_1x32(const void* x, int xtype, int64_t xrows, int64_t c
 /*
  * Reads MXFP4 codes back: y [rows, cols] (ytype, ldy >= cols) = code * 2^e,
  * rounded once where ytype cannot hold it (bf16 and fp32 hold every value
- * that the quantiser writes for normal numbers). q, s as above. Errors as
+ * that the quantiser writes, but for 2^128, to which FP8BQ_MX_NOSAT rounds
+ * magnitudes from 1.75 * 2^127 on: it reads back as infinity, and is one in a
+ * product). q, s as above. Errors as
  * fp8bq_quant_mxfp4_1x32.
  */
 int fp8bq_dequant_mxfp4_1x32(const void* q, int64_t rows, int64_t cols, int64_t ldq, const void* s, int64_t lds,
