@@ -17,7 +17,8 @@ namespace {
 // time (four loads in flight) and ranks equal experts by eight ballots over
 // the expert's bits, so that the order is that of the tokens whatever runs
 // when. Bound by latency: 2048 choices are a handful of dependent loads and
-// barriers, 4.8 us; 131072 take 4.2 and 6.9 (their 0.5 MB would be read in 0.1).
+// barriers, 4.8 us; 131072 take 10.2 in two launches (their 0.5 MB would be read
+// in 0.1), 5.6 and 9.6 behind a prompt's other kernels.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
@@ -205,10 +206,10 @@ hipError_t launch_moe_plan(const int32_t* idx, int tokens, int topk, int64_t ldi
 // ---------------------------------------------------------------------------
 // Balance loss. A wave takes a token (its experts over the lanes, so that a
 // softmax is two reductions in registers), two tokens' loads in flight. 16384
-// tokens of 256 experts (fp32, 4 sequences): 7.3 us the sums, 5.8 the joining of
-// the pieces, 10.0 the gradient, where the bytes would take 3.3, 0.1 and 6.5: an
+// tokens of 256 experts (fp32, 4 sequences): 7.9 us the sums, 5.8 the joining of
+// the pieces, 10.7 the gradient, where the bytes would take 3.3, 0.1 and 6.5: an
 // empty kernel takes 2.5, and a wave has but four tokens, one after the other.
-// Two tokens' arithmetic side by side without branches: 8.1 and 10.7.
+// Two tokens' arithmetic side by side without branches was slower by 10%.
 // ---------------------------------------------------------------------------
 namespace {
 

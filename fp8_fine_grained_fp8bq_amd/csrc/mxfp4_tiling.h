@@ -16,6 +16,7 @@ enum MxMode { MX_DENSE = 0, MX_ROWS = 1, MX_K = 2 };   // one product; rows grou
 // long as there are enough of them. Measured (us, bf16 out):
 //                       stream   64x64  64x128 128x128 128x256 256x256
 //   1 x 2048 x 7168        6.8    11.7    13.0    15.3    26.5    38.8
+//   1 x 18432 x 7168      18.2    17.1    14.4    16.9    29.8    40.0
 //   48 x 18432 x 7168     39.5    17.9    14.9    17.0    29.7    40.0
 //   1000 x 4096 x 7168   114.5    32.7    28.6    21.2    31.1    42.4
 //   2048 x 2048 x 2048    41.1    13.7    12.8     9.2    12.5    17.5
@@ -54,7 +55,16 @@ inline MxPick mx_pick(MxMode mode, int groups, int64_t m, int64_t n, int64_t chu
   // hold. Rows count half of that: a plan's buffer has room for every choice of
   // every token, many of which may be other GPUs' experts, and too large a tile
   // costs more than too small a one (8 experts with 57 .. 232 rows in a buffer
-  // of 2048, n = 2048, k = 7168: 20.8 us with 64 x 128, 33.5 with 128 x 128).
+  // of 2048, n = 2048, k = 7168: 20.8 us with 64 x 128, 33.5 with 128 x 128
+  // without loading waves). What the guess costs, n = 2048, k = 7168 (us, this
+  // rule / the best tiling):
+  //   8 of 256 experts, even:  512 of 16384 rows    44.7 / 20.3 (64 x 128)
+  //                            2048 of 65536        50.4 / 25.9 (128 x 128, deep)
+  //                            16384 of 524288       118 / 118
+  //   8 of 8, even:            2048 of 2048         29.9 / 27.5 (128 x 128, deep)
+  //                            16384 of 16384        118 / 118
+  // and of 32 experts, n = 1024, k = 2048, 8192 of 65536 rows 25.5 / 17.7 (128 x
+  // 256), 16384 of 16384 28.5 / 26.3 (256 x 256), 2048 of 2048 12.3 / 12.3.
   const int64_t g = mode == MX_DENSE ? 1 : groups;
   const int64_t rows = mode == MX_ROWS ? (m + 2 * g - 1) / (2 * g) : m;
   // one 128 x 128 tile per CU or less: loading waves and a third stage hide more
