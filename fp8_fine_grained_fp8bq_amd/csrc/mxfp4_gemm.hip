@@ -418,10 +418,10 @@ struct MxLoader {
 // eight by a rotation within 16-lane rows.
 
 // 16 bytes per lane. Whole lines are stored past the caches (LINE), measured
-// against plain stores in turn on one box: 54066 rows of 8 experts, n = 2048, k =
+// against plain stores in turn on one card: 54066 rows of 8 experts, n = 2048, k =
 // 7168: 367 against 383 us; 32 fp32 gradients of 1024 x 2048: 59 against 91 (with
 // half lines 84); 4096 x 7168 x 2048: 40.5 against 41.7 (with half lines 45.9). On
-// other boxes, and behind a step's other kernels, the first are 370 .. 485, 64 ..
+// other cards, and behind a step's other kernels, the first are 370 .. 485, 64 ..
 // 68 and 42.
 typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
 template <bool LINE>
