@@ -590,8 +590,11 @@ struct Sequences {
 // Gradient. Each wave takes a contiguous run of the sequences' tokens, whatever
 // their lengths (65536 tokens of 64 experts in 1000 sequences: 19 us where blocks
 // of their own for each sequence took 903; 2^20 tokens: 237 against 14417); of
-// each sequence that it meets, the lane's coefficients dloss * coef / S * experts *
-// c / (topk * n^2) stay in registers. The tokens outside every sequence, which get
+// each sequence that it meets, the lane's coefficients f = dloss * coef / S * experts *
+// c / (topk * n^2) stay in registers. p (f - sum p f) is the same for f less any
+// constant, the p of a token adding up to 1 (or all 0): the mean count comes off
+// as a whole number first, or nearly even loads would leave little but the
+// rounding of f. The tokens outside every sequence, which get
 // zeros, are dealt out beside that (half of 2^20 tokens outside: 137 us, 198 where
 // they were part of the runs).
 template <int T, bool SIG, int VPL, bool PACK>
@@ -609,11 +612,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void balance_grad_kernel(MoeBalanc
     if (s < 0 || s >= a.sequences) continue;            // only with offsets that decrease
     const float n = (float)max(real[s], 1);
     const float scale = dloss[0] * (a.coef / a.sequences) * ((float)a.experts / ((float)a.topk * n)) / n;
+    const int mean = (int)((int64_t)a.topk * real[s] / a.experts);
     float f[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       f[i] = expert_of<VPL, PACK>(lane, i) < a.experts
-                 ? scale * counts[(int64_t)s * a.experts + expert_of<VPL, PACK>(lane, i)] : 0.f;
+                 ? scale * (float)(counts[(int64_t)s * a.experts + expert_of<VPL, PACK>(lane, i)] - mean) : 0.f;
     auto take = [&](TokenRow<T, VPL, PACK>& row, int64_t at) {
       const bool ok = real_token(a, at, row.first, [](int) {});
       float (&v)[VPL] = row.v;

@@ -120,3 +120,30 @@ def test_a_long_sequence_among_many_short_ones_takes_no_longer(direction, score)
         log(f"{direction} {score}: {many:.3f} ms in 1001 sequences, {few:.3f} in 8")
         # 20 times leaves room for other load; dealt out by sequences it was 50 to 500 times
         assert many <= 20 * few
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts", [8, 60, 256])
+def test_gradient_of_nearly_even_loads(experts, score):
+    """Counts that differ by a few in thousands: the gradient keeps its accuracy, since p (f - sum p f) does not depend
+    on what f has in common; of even loads it is zero."""
+    import torch
+    tokens, topk = 4096 * experts // 8, 4
+    rng = np.random.default_rng(experts)
+    x = dev(rng.normal(size=(tokens, experts)).astype(np.float32))
+    idx = (np.arange(tokens * topk) % experts).astype(np.int32).reshape(tokens, topk)
+    dl = torch.ones((), device="cuda")
+    _, counts, real = fb.moe_balance(x, dev(idx), 0.3, score)
+    assert int(counts.min()) == int(counts.max())
+    assert (fb.moe_balance_grad(dl, x, dev(idx), counts, real, 0.3, score) == 0).all()
+    idx[:5, 0], idx[7, 1] = 0, 3
+    _, counts, real = fb.moe_balance(x, dev(idx), 0.3, score)
+    g = f64(fb.moe_balance_grad(dl, x, dev(idx), counts, real, 0.3, score))
+    wg = moe.balance_grad(1.0, f64(x), idx, 0.3, score, [0, tokens])
+    p, opened = moe.scores(f64(x), score)
+    c = counts.cpu().numpy()[0].astype(np.float64)
+    top = 0.3 * np.abs(c - c.mean()).max() * experts / (topk * tokens ** 2)
+    # p (g - sum p g) with g = f - mean: every p and the sum of experts terms off by the roundings of an exponential, a
+    # quotient and the additions, none of |g| above top
+    tol = (64 + experts / 16) * 2.0 ** -24 * p * 2 * (top + 0.3 * experts / (topk * tokens ** 2)) * (1.0 if opened is None else opened)
+    assert (np.abs(g - wg) <= tol + 2.0 ** -149).all()
