@@ -15,13 +15,17 @@ Two layers with the C names:
   `fp8bq_uncache_e5m6_1x128`, `fp8bq_requant_e5m6_t_128x1`, `fp8bq_quant_mxfp4_1x32`,
   `fp8bq_dispatch_mxfp4_1x32`, `fp8bq_dequant_mxfp4_1x32`, `fp8bq_gemm_mxfp4`,
   `fp8bq_grouped_gemm_mxfp4`, `fp8bq_grouped_wgrad_mxfp4`, `fp8bq_moe_plan`, `fp8bq_moe_balance`,
-  `fp8bq_moe_balance_workspace_size`, `fp8bq_moe_balance_grad`: pointer-level, exactly the C signatures (ints
+  `fp8bq_moe_balance_workspace_size`, `fp8bq_moe_balance_grad`, `fp8bq_rmsnorm`, `fp8bq_rmsnorm_grad_workspace_size`,
+  `fp8bq_rmsnorm_grad`, `fp8bq_moe_dispatch`, `fp8bq_moe_combine`, `fp8bq_moe_combine_grad`, `fp8bq_gemv_mxfp4`,
+  `fp8bq_grouped_gemv_mxfp4`: pointer-level, exactly the C signatures (ints
   for pointers and the stream); a non-zero status raises `Fp8bqError`.
 * `quant_act_1x128`, `quant_w_128x128`, `requant_t_128x1`, `gemm`,
   `gemm_quant`, `grouped_gemm`, `grouped_gemm_decode`, `cache_e5m6_1x128`,
   `uncache_e5m6_1x128`, `requant_e5m6_t_128x1`, and the MXFP4 and routing operators
   (`quant_mxfp4_1x32`, `dispatch_mxfp4_1x32`, `dequant_mxfp4_1x32`, `gemm_mxfp4`,
-  `grouped_gemm_mxfp4`, `grouped_wgrad_mxfp4`, `moe_plan`, `moe_balance`, `moe_balance_grad`): take torch tensors on
+  `grouped_gemm_mxfp4`, `grouped_wgrad_mxfp4`, `moe_plan`, `moe_balance`, `moe_balance_grad`) and those around a layer's
+  Linears (`rmsnorm`, `rmsnorm_grad`, `moe_dispatch`, `moe_combine`, `moe_combine_grad`, `gemv_mxfp4`,
+  `grouped_gemv_mxfp4`): take torch tensors on
   the GPU, allocate the outputs with torch (memory and streams are the only
   things torch provides) and call the same entry points on the current stream.
 """
@@ -53,7 +57,9 @@ EXPORTS = ("fp8bq_quant_act_1x128", "fp8bq_quant_w_128x128", "fp8bq_requant_t_12
            "fp8bq_uncache_e5m6_1x128", "fp8bq_requant_e5m6_t_128x1", "fp8bq_quant_mxfp4_1x32",
            "fp8bq_dispatch_mxfp4_1x32", "fp8bq_dequant_mxfp4_1x32", "fp8bq_gemm_mxfp4", "fp8bq_grouped_gemm_mxfp4",
            "fp8bq_grouped_wgrad_mxfp4", "fp8bq_moe_plan", "fp8bq_moe_balance_workspace_size", "fp8bq_moe_balance",
-           "fp8bq_moe_balance_grad", "fp8bq_last_error", "fp8bq_version")
+           "fp8bq_moe_balance_grad", "fp8bq_rmsnorm", "fp8bq_rmsnorm_grad_workspace_size", "fp8bq_rmsnorm_grad",
+           "fp8bq_moe_dispatch", "fp8bq_moe_combine", "fp8bq_moe_combine_grad", "fp8bq_gemv_mxfp4",
+           "fp8bq_grouped_gemv_mxfp4", "fp8bq_last_error", "fp8bq_version")
 
 
 class Fp8bqError(RuntimeError):
@@ -111,8 +117,17 @@ def lib() -> ctypes.CDLL:
         routing = [vp, i32, i64, i64, i64, vp, i64, i64, vp, i64, i32, ctypes.c_float]   # logits .. coef
         L.fp8bq_moe_balance.argtypes = [*routing, vp, vp, vp, vp, vp]
         L.fp8bq_moe_balance_grad.argtypes = [vp, *routing, vp, vp, vp, i64, vp]
+        mat = [vp, i64]                         # rows, ld
+        L.fp8bq_rmsnorm.argtypes = [vp, i32, i64, i64, i64, *mat, vp, i32, ctypes.c_float, *mat, *mat, *mat, *mat, vp, i32, vp]
+        L.fp8bq_rmsnorm_grad_workspace_size.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_int64)]
+        L.fp8bq_rmsnorm_grad.argtypes = [vp, i32, i64, i64, i64, *mat, vp, i32, vp, *mat, *mat, vp, vp, vp]
+        L.fp8bq_moe_dispatch.argtypes = [vp, i32, i64, i64, i64, *mat, vp, i64, vp, i64, *mat, *mat, vp]
+        L.fp8bq_moe_combine.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, *mat, *mat, *mat, vp]
+        L.fp8bq_moe_combine_grad.argtypes = [vp, i32, i64, i64, i64, vp, i64, i64, vp, i64, *mat, vp, *mat, vp, vp]
+        L.fp8bq_gemv_mxfp4.argtypes = [i64, i64, i64, vp, i32, i64, *mx, vp, i32, i64, vp]
+        L.fp8bq_grouped_gemv_mxfp4.argtypes = [ctypes.c_int32, vp, i64, i64, i64, vp, i32, i64, i64, vp, *mx, vp, i32, i64, vp]
         for f in EXPORTS:
-            if "mxfp4" in f or "moe" in f:
+            if "mxfp4" in f or "moe" in f or "norm" in f:
                 getattr(L, f).restype = ctypes.c_int
         L.fp8bq_last_error.argtypes = []
         L.fp8bq_version.restype = ctypes.c_char_p
@@ -490,9 +505,64 @@ def fp8bq_moe_balance_grad(dloss, logits, ltype, tokens, experts, ldl, idx, topk
                                                sequences, score, coef, counts, real, dlogits, lddl, stream))
 
 
+# ---------------------------------------------------------------------------
+# around a layer's Linears: pointer level
+# ---------------------------------------------------------------------------
+
+def fp8bq_rmsnorm(x, xtype, rows, cols, ldx, residual, ldr, weight, wtype, eps, h, ldh, y, ldy, q, ldq, s, lds, rstd,
+                  flags=0, stream=0):
+    return _check("fp8bq_rmsnorm", lib().fp8bq_rmsnorm(x, xtype, rows, cols, ldx, residual, ldr, weight, wtype, eps, h,
+                                                       ldh, y, ldy, q, ldq, s, lds, rstd, flags, stream))
+
+
+def fp8bq_rmsnorm_grad_workspace_size(rows, cols):
+    """Bytes of workspace fp8bq_rmsnorm_grad needs."""
+    out = ctypes.c_int64(-1)
+    _check("fp8bq_rmsnorm_grad_workspace_size",
+           lib().fp8bq_rmsnorm_grad_workspace_size(rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def fp8bq_rmsnorm_grad(dy, type, rows, cols, lddy, h, ldh, weight, wtype, rstd, dh, lddh, dx, lddx, dweight, workspace,
+                       stream=0):
+    return _check("fp8bq_rmsnorm_grad", lib().fp8bq_rmsnorm_grad(dy, type, rows, cols, lddy, h, ldh, weight, wtype, rstd,
+                                                                 dh, lddh, dx, lddx, dweight, workspace, stream))
+
+
+def fp8bq_moe_dispatch(x, elem, tokens, cols, ldx, s, lds, pos, topk, src, rows, out, ldo, so, ldso, stream=0):
+    return _check("fp8bq_moe_dispatch", lib().fp8bq_moe_dispatch(x, elem, tokens, cols, ldx, s, lds, pos, topk, src, rows,
+                                                                 out, ldo, so, ldso, stream))
+
+
+def fp8bq_moe_combine(y, type, rows, cols, ldy, pos, tokens, topk, weight, ldw, base, ldb, out, ldo, stream=0):
+    return _check("fp8bq_moe_combine", lib().fp8bq_moe_combine(y, type, rows, cols, ldy, pos, tokens, topk, weight, ldw,
+                                                               base, ldb, out, ldo, stream))
+
+
+def fp8bq_moe_combine_grad(dout, type, tokens, cols, lddout, y, rows, ldy, pos, topk, weight, ldw, src, dy, lddy, dweight,
+                           stream=0):
+    return _check("fp8bq_moe_combine_grad",
+                  lib().fp8bq_moe_combine_grad(dout, type, tokens, cols, lddout, y, rows, ldy, pos, topk, weight, ldw, src,
+                                               dy, lddy, dweight, stream))
+
+
+def fp8bq_gemv_mxfp4(m, n, k, x, xtype, ldx, b, ldb, sb, ldsb, out, otype, ldo, stream=0):
+    return _check("fp8bq_gemv_mxfp4", lib().fp8bq_gemv_mxfp4(m, n, k, x, xtype, ldx, b, ldb, sb, ldsb, out, otype, ldo,
+                                                             stream))
+
+
+def fp8bq_grouped_gemv_mxfp4(groups, row_off, rows, n, k, x, xtype, xrows, ldx, src, b, ldb, sb, ldsb, out, otype, ldo,
+                             stream=0):
+    """`row_off` and `src` are device pointers (int32)."""
+    return _check("fp8bq_grouped_gemv_mxfp4",
+                  lib().fp8bq_grouped_gemv_mxfp4(groups, row_off, rows, n, k, x, xtype, xrows, ldx, src, b, ldb, sb, ldsb,
+                                                 out, otype, ldo, stream))
+
+
 # The tensor layer of these operators is in tensors.py, imported on first use.
 _TENSOR_CALLS = ("quant_mxfp4_1x32", "dispatch_mxfp4_1x32", "dequant_mxfp4_1x32", "gemm_mxfp4", "grouped_gemm_mxfp4",
-                 "grouped_wgrad_mxfp4", "moe_plan", "moe_balance", "moe_balance_grad")
+                 "grouped_wgrad_mxfp4", "moe_plan", "moe_balance", "moe_balance_grad", "rmsnorm", "rmsnorm_grad",
+                 "moe_dispatch", "moe_combine", "moe_combine_grad", "gemv_mxfp4", "grouped_gemv_mxfp4")
 
 
 def __getattr__(name):

@@ -22,7 +22,8 @@ PROBE_LIB = os.path.join(PKG, "libfp8bq_probe.so")
 TENSORS_LIB = os.path.join(PKG, "_tensors.so")
 
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "gemm_quant.hip", "gemm_grouped.hip", "gemm_decode.hip",
-           "api_mxfp4.cpp", "mxfp4_quant.hip", "mxfp4_gemm.hip", "moe.hip"]
+           "api_mxfp4.cpp", "mxfp4_quant.hip", "mxfp4_gemm.hip", "moe.hip",
+           "api_layer.cpp", "norm.hip", "moe_rows.hip", "mxfp4_gemv.hip"]
 # measurement probes of the matrix instruction (a library of their own, not the GEMM path)
 PROBE_SOURCES = ["probe.hip"]
 

@@ -6,7 +6,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include "entry.h"
+#include "entry_checks.h"
 #include "mxfp4.h"
 
 static_assert(FP8BQ_DISPATCH_WORKSPACE_ROW_BYTES == 4 * (fp8bq::kMxDispatchSlots + 1), "workspace size in the header");
@@ -14,21 +14,7 @@ static_assert(FP8BQ_MOE_PLAN_WORKSPACE_BYTES == fp8bq::kMoePlanMaxBlocks * 256 *
 
 namespace {
 
-using fp8bq::entry_fail;
-
-constexpr int64_t kMaxSide = (int64_t)1 << 31;    // rows, columns: indices fit 32 bits
-constexpr int64_t kMaxLd = (int64_t)1 << 23;      // bytes of a code row: 256 rows within 2 GiB
-constexpr int64_t kMaxRouted = (int64_t)1 << 30;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int64_t chunks_of(int64_t k) { return (k - 1) / 256 + 1; }
-int elem_bytes(int dtype) { return dtype == FP8BQ_FP32 ? 4 : 2; }
-bool bad_dtype(int t) { return t != FP8BQ_BF16 && t != FP8BQ_FP16 && t != FP8BQ_FP32; }
-
-int launched(hipError_t e, const char* what) {
-  if (e != hipSuccess) return entry_fail(FP8BQ_E_HIP, "%s: launch failed: %s", what, hipGetErrorString(e));
-  return FP8BQ_OK;
-}
+using namespace fp8bq;
 
 // Grids have fewer than 2^32 threads, that is 2^24 blocks of 256. Row form and
 // read-back: at most one block for 16 rows of a chunk.
@@ -39,20 +25,6 @@ bool too_large(int64_t rows, int64_t cols) {
 // (rows and cols as too_large leaves them).
 bool too_large_by_columns(int64_t rows, int64_t cols, int xtype) {
   return ((rows - 1) / 256 + 1) * chunks_of(cols) * (4 * elem_bytes(xtype)) >= ((int64_t)1 << 24);
-}
-
-// One code matrix [rows, k] with its scales.
-int check_codes(const char* who, const char* name, const void* q, int64_t ldq, const void* s, int64_t lds,
-                int64_t rows, int64_t k) {
-  if (!q || !s) return entry_fail(FP8BQ_E_INVAL, "%s: null codes or scales of %s", who, name);
-  if (ldq < 128 * chunks_of(k))
-    return entry_fail(FP8BQ_E_INVAL, "%s: ld of %s (%lld bytes) < 128 * ceil(k / 256)", who, name, (long long)ldq);
-  if (lds < rows) return entry_fail(FP8BQ_E_INVAL, "%s: scale ld of %s must be >= its rows", who, name);
-  if (ldq >= kMaxLd || lds >= kMaxSide / 8) return entry_fail(FP8BQ_E_SHAPE, "%s: ld of %s too large", who, name);
-  if (!aligned(q, 16) || ldq % 16 || !aligned(s, 8))
-    return entry_fail(FP8BQ_E_ALIGN, "%s: codes of %s must be 16-byte aligned with ld a multiple of 16, scales 8-byte "
-                      "aligned", who, name);
-  return FP8BQ_OK;
 }
 
 int quant(const char* who, const void* x, int xtype, int64_t xrows, int64_t cols, int64_t ldx, const int32_t* src,

@@ -1,0 +1,41 @@
+// Reductions over the lanes of a wave.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8bq {
+
+// Sum and maximum over the wave, on every lane: DPP within 16-lane rows (lane
+// ^ 1, ^ 2, mirrored halves, mirrored rows), then swaps of whole rows; one or
+// two instructions a step and no LDS.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, F&& f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  v = f(v, dpp<0x140>(v));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, [](float a, float b) { return a + b; }); }
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
+
+// The same over each aligned group of 16 lanes, and over LANES of them.
+template <class F>
+__device__ __forceinline__ float row16_reduce(float v, F&& f) {
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  return f(v, dpp<0x140>(v));
+}
+__device__ __forceinline__ float row16_sum(float v) { return row16_reduce(v, [](float a, float b) { return a + b; }); }
+__device__ __forceinline__ float row16_max(float v) { return row16_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
+
+}  // namespace fp8bq

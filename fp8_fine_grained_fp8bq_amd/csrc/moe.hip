@@ -2,6 +2,7 @@
 // order) and the router's balance loss with its gradient. Definitions:
 // include/fp8bq.h. No floating-point atomics: every sum has a fixed order.
 #include "../../include/fp8bq.h"
+#include "lanes.h"
 #include "mxfp4.h"
 
 namespace fp8bq {
@@ -282,27 +283,6 @@ __device__ __forceinline__ void store_logits(void* base, int64_t row, int expert
       if (lane + 64 * i < experts) p[lane + 64 * i] = raw[i];
   }
 }
-
-// Sum and maximum over the wave, on every lane: DPP within 16-lane rows (lane
-// ^ 1, ^ 2, mirrored halves, mirrored rows), then swaps of whole rows; one or
-// two instructions a step and no LDS.
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
-}
-template <class F>
-__device__ __forceinline__ float wave_reduce(float v, F&& f) {
-  v = f(v, dpp<0xB1>(v));
-  v = f(v, dpp<0x4E>(v));
-  v = f(v, dpp<0x141>(v));
-  v = f(v, dpp<0x140>(v));
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
-}
-__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, [](float a, float b) { return a + b; }); }
-__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
 
 // e^x for x <= 0: 2^t of t = x log2(e), times 1 + what t's rounding left over
 // (which is up to |x| 2^-24 of the result), log2(e) and ln 2 being the

@@ -3,45 +3,12 @@
 // layouts: include/fp8bq.h; the codec: mxfp4_codec.h. All of it is bound by
 // memory: 2 (4) bytes read and 17/32 bytes written per element and form.
 #include "../../include/fp8bq.h"
+#include "elem.h"
 #include "mxfp4.h"
 #include "mxfp4_codec.h"
 
 namespace fp8bq {
 namespace {
-
-template <int T> struct Elem;
-template <> struct Elem<FP8BQ_BF16> {
-  using type = uint16_t;
-  static constexpr int kBytes = 2;
-  static __device__ __forceinline__ float value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-  static __device__ __forceinline__ uint16_t round(float v) {
-    const __bf16 b = (__bf16)v;
-    uint16_t r;
-    __builtin_memcpy(&r, &b, 2);
-    return r;
-  }
-};
-template <> struct Elem<FP8BQ_FP16> {
-  using type = uint16_t;
-  static constexpr int kBytes = 2;
-  static __device__ __forceinline__ float value(uint16_t b) {
-    _Float16 h;
-    __builtin_memcpy(&h, &b, 2);
-    return (float)h;
-  }
-  static __device__ __forceinline__ uint16_t round(float v) {
-    const _Float16 h = (_Float16)v;
-    uint16_t r;
-    __builtin_memcpy(&r, &h, 2);
-    return r;
-  }
-};
-template <> struct Elem<FP8BQ_FP32> {
-  using type = float;
-  static constexpr int kBytes = 4;
-  static __device__ __forceinline__ float value(float b) { return b; }
-  static __device__ __forceinline__ float round(float v) { return v; }
-};
 
 // fp32 magnitude bits of the largest magnitude in the dwords w (two 16-bit
 // elements each, or one fp32).

@@ -1,4 +1,5 @@
-// The MXFP4 operators and the routing on torch tensors: checks of what the C
+// The MXFP4 operators, the routing and the operators around a layer's Linears
+// on torch tensors: checks of what the C
 // entry points (include/fp8bq.h) cannot see, allocation of the outputs, and
 // the call, on the tensors' device and its current stream. A Python extension
 // module (_tensors.so) because these calls are short: an operator's kernels
@@ -395,6 +396,222 @@ PyObject* moe_balance_grad(PyObject* const* arg) {
   return wrap(grad);
 }
 
+// ---- around a layer's Linears --------------------------------------------------
+
+double number(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(name, " must be a number");
+  }
+  return v;
+}
+// A matrix of given shape and type, row-major.
+const Tensor& like(const Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+  if (t.scalar_type() != type) refuse(name, " must be ", type, " (got ", t.scalar_type(), ")");
+  if (t.sizes() != shape || (shape.size() > 1 && t.size(-1) > 1 && t.stride(-1) != 1) || (shape.size() == 1 && !t.is_contiguous()))
+    refuse(name, " must be row-major, of shape ", shape, " (got ", t.sizes(), ", strides ", t.strides(), ")");
+  return t;
+}
+std::optional<Tensor> maybe_like(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type) {
+  std::optional<Tensor> t = maybe(o, name);
+  if (t) like(*t, name, shape, type);
+  return t;
+}
+void* pointer(const std::optional<Tensor>& t) { return t ? t->data_ptr() : nullptr; }
+int64_t ld(const std::optional<Tensor>& t) { return t ? ld(*t) : 0; }
+
+const Tensor& norm_weight(PyObject* o, int64_t cols, int& wtype) {
+  const Tensor& w = tensor(o, "weight");
+  wtype = dtype_code(w.scalar_type(), "weight");
+  return like(w, "weight", {cols}, w.scalar_type());
+}
+
+// (x, weight, eps, residual or None, quant, norm, pow2)
+PyObject* rmsnorm(PyObject* const* arg) {
+  const Tensor& x = matrix(tensor(arg[0], "x"), "x");
+  const at::ScalarType type = x.scalar_type();
+  const int xtype = dtype_code(type, "x");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  int wtype;
+  const Tensor& w = norm_weight(arg[1], cols, wtype);
+  const float eps = (float)number(arg[2], "eps");
+  const std::optional<Tensor> r = maybe_like(arg[3], "residual", {rows, cols}, type);
+  const bool quant = truth(arg[4]), norm = truth(arg[5]);
+  const int flags = truth(arg[6]) ? FP8BQ_SCALE_POW2 : 0;
+  if (!quant && !norm) refuse("neither the codes nor the normalised rows are asked for");
+  if (quant && cols % 128) refuse("cols must be a multiple of 128 for the codes, got ", cols);
+  const On on(x, w, r);
+  std::optional<Tensor> q, s, y, h;
+  if (quant) {
+    q = on.empty({rows, cols}, at::kByte);
+    s = on.empty({cols / 128, rows}, at::kFloat);
+  }
+  if (norm) y = on.empty({rows, cols}, type);
+  if (r) h = on.empty({rows, cols}, type);
+  Tensor rstd = on.empty({rows}, at::kFloat);
+  check("fp8bq_rmsnorm",
+        fp8bq_rmsnorm(x.data_ptr(), xtype, rows, cols, ld(x), pointer(r), ld(r), w.data_ptr(), wtype, eps, pointer(h), cols,
+                      pointer(y), cols, pointer(q), cols, static_cast<float*>(pointer(s)), rows, rstd.data_ptr<float>(), flags,
+                      on.stream));
+  return tuple(q, s, y, h, rstd);
+}
+
+// (dy, h, weight, rstd, dh or None)
+PyObject* rmsnorm_grad(PyObject* const* arg) {
+  const Tensor& h = matrix(tensor(arg[1], "h"), "h");
+  const at::ScalarType type = h.scalar_type();
+  const int xtype = dtype_code(type, "h");
+  const int64_t rows = h.size(0), cols = h.size(1);
+  const Tensor& dy = like(tensor(arg[0], "dy"), "dy", {rows, cols}, type);
+  int wtype;
+  const Tensor& w = norm_weight(arg[2], cols, wtype);
+  const Tensor& rstd = like(tensor(arg[3], "rstd"), "rstd", {rows}, at::kFloat);
+  const std::optional<Tensor> dh = maybe_like(arg[4], "dh", {rows, cols}, type);
+  const On on(h, dy, w, rstd, dh);
+  int64_t bytes = 0;
+  check("fp8bq_rmsnorm_grad_workspace_size", fp8bq_rmsnorm_grad_workspace_size(rows, cols, &bytes));
+  Tensor dx = on.empty({rows, cols}, type), dw = on.empty({cols}, at::kFloat), ws = on.empty({bytes / 4}, at::kFloat);
+  check("fp8bq_rmsnorm_grad",
+        fp8bq_rmsnorm_grad(dy.data_ptr(), xtype, rows, cols, ld(dy), h.data_ptr(), ld(h), w.data_ptr(), wtype,
+                           rstd.data_ptr<float>(), pointer(dh), ld(dh), dx.data_ptr(), cols, dw.data_ptr<float>(),
+                           ws.data_ptr(), on.stream));
+  return tuple(dx, dw);
+}
+
+// The choices' rows of one plan.
+const Tensor& choices(PyObject* o) {
+  const Tensor& pos = int32(matrix(tensor(o, "pos"), "pos"), "pos");
+  if (!pos.is_contiguous()) refuse("pos must be contiguous (got strides ", pos.strides(), ")");
+  return pos;
+}
+
+// (x, src, pos, s or None, out or None, s_out or None)
+PyObject* moe_dispatch(PyObject* const* arg) {
+  const Tensor& x = matrix(tensor(arg[0], "x"), "x");
+  const at::ScalarType type = x.scalar_type();
+  if (type != at::kByte) dtype_code(type, "x that does not hold 8-bit codes (uint8)");
+  const Tensor& src = int32_list(tensor(arg[1], "src"), "src", 1);
+  const Tensor& pos = choices(arg[2]);
+  const int64_t tokens = x.size(0), cols = x.size(1), rows = src.numel();
+  if (pos.size(0) != tokens) refuse("pos has ", pos.size(0), " tokens, x ", tokens);
+  std::optional<Tensor> s = maybe(arg[3], "s"), out = maybe_like(arg[4], "out", {rows, cols}, type), so;
+  if (s) {
+    if (type != at::kByte || cols % 128) refuse("scales go with uint8 codes of a multiple of 128 columns (got ", type, ", ", cols, " columns)");
+    like(*s, "s", {cols / 128, tokens}, at::kFloat);
+    so = maybe_like(arg[5], "s_out", {cols / 128, rows}, at::kFloat);
+  } else if (arg[5] != Py_None) {
+    refuse("s_out without s");
+  }
+  const On on(x, src, pos, s, out, so);
+  if (!out) out = on.empty({rows, cols}, type);
+  if (s && !so) so = on.empty({cols / 128, rows}, at::kFloat);
+  check("fp8bq_moe_dispatch",
+        fp8bq_moe_dispatch(x.data_ptr(), (int)x.element_size(), tokens, cols, ld(x), static_cast<const float*>(pointer(s)), ld(s),
+                           pos.data_ptr<int32_t>(), pos.size(1), src.data_ptr<int32_t>(), rows, out->data_ptr(), ld(out),
+                           static_cast<float*>(pointer(so)), ld(so), on.stream));
+  return tuple(out, so);
+}
+
+// (y, pos, weight or None, base or None, out or None)
+PyObject* moe_combine(PyObject* const* arg) {
+  const Tensor& y = matrix(tensor(arg[0], "y"), "y");
+  const at::ScalarType type = y.scalar_type();
+  const int code = dtype_code(type, "y");
+  const Tensor& pos = choices(arg[1]);
+  const int64_t tokens = pos.size(0), topk = pos.size(1), rows = y.size(0), cols = y.size(1);
+  const std::optional<Tensor> w = maybe_like(arg[2], "weight", {tokens, topk}, at::kFloat);
+  const std::optional<Tensor> base = maybe_like(arg[3], "base", {tokens, cols}, type);
+  std::optional<Tensor> out = maybe_like(arg[4], "out", {tokens, cols}, type);
+  const On on(y, pos, w, base, out);
+  if (!out) out = on.empty({tokens, cols}, type);
+  check("fp8bq_moe_combine",
+        fp8bq_moe_combine(y.data_ptr(), code, rows, cols, ld(y), pos.data_ptr<int32_t>(), tokens, topk,
+                          static_cast<const float*>(pointer(w)), ld(w), pointer(base), ld(base), out->data_ptr(), ld(out),
+                          on.stream));
+  return wrap(out);
+}
+
+// (dout, y, pos, weight, src, out or None)
+PyObject* moe_combine_grad(PyObject* const* arg) {
+  const Tensor& y = matrix(tensor(arg[1], "y"), "y");
+  const at::ScalarType type = y.scalar_type();
+  const int code = dtype_code(type, "y");
+  const Tensor& pos = choices(arg[2]);
+  const int64_t tokens = pos.size(0), topk = pos.size(1), rows = y.size(0), cols = y.size(1);
+  const Tensor& dout = like(tensor(arg[0], "dout"), "dout", {tokens, cols}, type);
+  const Tensor& w = like(tensor(arg[3], "weight"), "weight", {tokens, topk}, at::kFloat);
+  const Tensor& src = int32_shaped(tensor(arg[4], "src"), "src", {rows});
+  std::optional<Tensor> dy = maybe_like(arg[5], "out", {rows, cols}, type);
+  const On on(y, dout, pos, w, src, dy);
+  if (!dy) dy = on.empty({rows, cols}, type);
+  Tensor dw = on.empty({tokens, topk}, at::kFloat);
+  check("fp8bq_moe_combine_grad",
+        fp8bq_moe_combine_grad(dout.data_ptr(), code, tokens, cols, ld(dout), y.data_ptr(), rows, ld(y), pos.data_ptr<int32_t>(),
+                               topk, w.data_ptr<float>(), ld(w), src.data_ptr<int32_t>(), dy->data_ptr(), ld(dy),
+                               dw.data_ptr<float>(), on.stream));
+  return tuple(dy, dw);
+}
+
+// x [rows, k] against codes of k elements, padded to a multiple of 256.
+int64_t inner(const Tensor& x, const Mx& w) {
+  const int64_t k = x.size(1);
+  if (k > w.k || k <= w.k - 256) refuse("x has ", k, " columns, the codes of w stand for ", w.k - 255, " to ", w.k);
+  return k;
+}
+// The type of a product's output, and `out` checked against it.
+at::ScalarType gemv_type(const std::optional<Tensor>& out, int64_t rows, int64_t n, std::optional<at::ScalarType> dtype,
+                         at::ScalarType usual, int& otype) {
+  const at::ScalarType t = out ? out->scalar_type() : dtype.value_or(usual);
+  if (out && dtype && *dtype != t) refuse("out is ", t, ", dtype says ", *dtype);
+  otype = dtype_code(t, "the output");
+  if (out) like(*out, "out", {rows, n}, t);
+  return t;
+}
+
+// (x, w, ws, out or None, dtype or None)
+PyObject* gemv(PyObject* const* arg) {
+  const Tensor& x = matrix(tensor(arg[0], "x"), "x");
+  const Tensor &w = tensor(arg[1], "w"), &ws = tensor(arg[2], "ws");
+  const int xtype = dtype_code(x.scalar_type(), "x");
+  const Mx b(w, ws, "w");
+  const int64_t m = x.size(0), k = inner(x, b);
+  const std::optional<Tensor> given = maybe(arg[3], "out");
+  int otype;
+  const at::ScalarType t = gemv_type(given, m, b.rows, dtype_arg(arg[4]), x.scalar_type(), otype);
+  const On on(x, w, ws, given);
+  const Tensor out = given ? *given : on.empty({m, b.rows}, t);
+  check("fp8bq_gemv_mxfp4", fp8bq_gemv_mxfp4(m, b.rows, k, x.data_ptr(), xtype, ld(x), b.q, b.ldq, b.s, b.lds, out.data_ptr(),
+                                             otype, ld(out), on.stream));
+  return wrap(out);
+}
+
+// (row_off, x, w, ws, src or None, out or None, dtype or None)
+PyObject* grouped_gemv(PyObject* const* arg) {
+  const Tensor& off = tensor(arg[0], "row_off");
+  const Tensor& x = matrix(tensor(arg[1], "x"), "x");
+  const Tensor &w = tensor(arg[2], "w"), &ws = tensor(arg[3], "ws");
+  const int xtype = dtype_code(x.scalar_type(), "x");
+  if (w.dim() != 3 || w.size(0) < 1) refuse("w must be codes [groups, n, bytes], got ", w.sizes());
+  const int64_t groups = w.size(0);
+  const Mx b(w, ws, "w", groups);
+  const int64_t k = inner(x, b);
+  int32_shaped(off, "row_off", {groups + 1});
+  const std::optional<Tensor> src = maybe(arg[4], "src"), given = maybe(arg[5], "out");
+  if (src) int32_list(*src, "src", 1);
+  const int64_t rows = src ? src->numel() : x.size(0);
+  if (groups > 256) refuse("at most 256 groups, got ", groups);
+  int otype;
+  const at::ScalarType t = gemv_type(given, rows, b.rows, dtype_arg(arg[6]), x.scalar_type(), otype);
+  const On on(x, w, ws, off, src, given);
+  const Tensor out = given ? *given : on.empty({rows, b.rows}, t);
+  check("fp8bq_grouped_gemv_mxfp4",
+        fp8bq_grouped_gemv_mxfp4((int32_t)groups, off.data_ptr<int32_t>(), rows, b.rows, k, x.data_ptr(), xtype, x.size(0), ld(x),
+                                 static_cast<const int32_t*>(pointer(src)), b.q, b.ldq, b.s, b.lds, out.data_ptr(), otype, ld(out),
+                                 on.stream));
+  return wrap(out);
+}
+
 // ---- the module ----------------------------------------------------------------
 
 // No C++ exception leaves a function: refusals become ValueError, statuses the
@@ -437,7 +654,10 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {
     method<quant, 5>("quant"), method<dequant, 4>("dequant"), method<gemm, 6>("gemm"),
     method<grouped_gemm, 7>("grouped_gemm"), method<grouped_wgrad, 7>("grouped_wgrad"), method<moe_plan, 3>("moe_plan"),
-    method<moe_balance, 5>("moe_balance"), method<moe_balance_grad, 8>("moe_balance_grad"), {nullptr, nullptr, 0, nullptr}};
+    method<moe_balance, 5>("moe_balance"), method<moe_balance_grad, 8>("moe_balance_grad"),
+    method<rmsnorm, 7>("rmsnorm"), method<rmsnorm_grad, 5>("rmsnorm_grad"), method<moe_dispatch, 6>("moe_dispatch"),
+    method<moe_combine, 5>("moe_combine"), method<moe_combine_grad, 6>("moe_combine_grad"), method<gemv, 5>("gemv"),
+    method<grouped_gemv, 7>("grouped_gemv"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,4 +1,4 @@
-"""The MXFP4 operators and the routing of tokens to experts on torch tensors. Reached as attributes of the package,
+"""The MXFP4 operators, the routing of tokens to experts and the operators around a layer's Linears on torch tensors. Reached as attributes of the package,
 which imports this module on their first use (the package itself does not need torch).
 
 The calls check their arguments (ValueError), allocate the outputs and call the C entry points (Fp8bqError for their
@@ -77,3 +77,51 @@ def moe_balance_grad(dloss, logits, idx, counts, real, coef: float, score: str =
     """Gradient of moe_balance with respect to the logits, in their type; counts and real are moe_balance's, dloss
     float32 [] on the GPU."""
     return _tensors.moe_balance_grad(dloss, logits, idx, counts, real, coef, score, seq_off)
+
+
+def rmsnorm(x, weight, eps: float = 1e-6, residual=None, quant: bool = True, norm: bool = False, pow2: bool = False):
+    """RMS norm of the rows of x (bf16 / fp16 / fp32 [rows, cols]) after adding `residual` -> (q, s, y, h, rstd): codes
+    uint8 [rows, cols] and scales float32 [cols / 128, rows] for the next FP8 Linear (quant; pow2: power-of-two scales),
+    the normalised rows in x's type (norm), x + residual in x's type, and float32 [rows]; None for what is not asked
+    for. weight [cols] of any of the three types."""
+    return _tensors.rmsnorm(x, weight, eps, residual, quant, norm, pow2)
+
+
+def rmsnorm_grad(dy, h, weight, rstd, dh=None):
+    """Gradient of rmsnorm: dy of the normalised rows, h (x itself where there was no residual) and rstd as rmsnorm
+    returned them, dh what reaches h besides -> (dx in h's type, the gradient of x and of the residual; dweight float32
+    [cols])."""
+    return _tensors.rmsnorm_grad(dy, h, weight, rstd, dh)
+
+
+def moe_dispatch(x, src, pos, s=None, out=None, s_out=None):
+    """Tokens to the rows of a plan (src and pos are moe_plan's): x bf16 / fp16 / fp32 [tokens, cols], or uint8 codes with
+    their scales s float32 [cols / 128, tokens] -> (rows [len(src), cols], their scales [cols / 128, len(src)] or None).
+    Padding rows are zeros, rows behind the last expert are left as they are in `out` and `s_out`. Its gradient is
+    moe_combine(drows, pos)."""
+    return _tensors.moe_dispatch(x, src, pos, s, out, s_out)
+
+
+def moe_combine(y, pos, weight=None, base=None, out=None):
+    """Rows y [rows, cols] back to their tokens: base[t] + the sum of weight[t, j] * y[pos[t, j]] over the choices that
+    have a row, in y's type [tokens, cols]. weight float32 [tokens, topk] (None: ones); base in y's type (None: zeros)."""
+    return _tensors.moe_combine(y, pos, weight, base, out)
+
+
+def moe_combine_grad(dout, y, pos, weight, src, out=None):
+    """Gradient of moe_combine -> (dy [rows, cols] in y's type, dweight float32 [tokens, topk]); padding rows of dy are
+    zeros, rows behind the last expert are left as they are in `out`. base's gradient is dout."""
+    return _tensors.moe_combine_grad(dout, y, pos, weight, src, out)
+
+
+def gemv_mxfp4(x, w, ws, out=None, dtype=None):
+    """Product of a few rows x (bf16 / fp16 / fp32 [m, k], kept as they are) with an MXFP4 weight: codes w [n, 128 ceil(k /
+    256)] with scales ws -> [m, n] in x's type (or `dtype`)."""
+    return _tensors.gemv(x, w, ws, out, dtype)
+
+
+def grouped_gemv_mxfp4(row_off, x, w, ws, src=None, out=None, dtype=None):
+    """The same over experts: rows row_off[e] .. row_off[e + 1] of the result are those of x[src] (x without src) times
+    expert e's weight w[e]^T; row_off int32 [G + 1] and src int32 [rows] on the GPU (moe_plan's). Rows of no expert are
+    left as they are in `out`."""
+    return _tensors.grouped_gemv(row_off, x, w, ws, src, out, dtype)

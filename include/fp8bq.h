@@ -1,7 +1,8 @@
 /*
  * fp8bq -- fine-grained FP8 (E4M3) quantisation and block-scaled FP8 GEMM for
  * AMD Instinct MI355X (gfx950); further down, the same Linear in 4-bit
- * microscaled form (MXFP4) and the routing of tokens to its experts.
+ * microscaled form (MXFP4), the routing of tokens to its experts, and what
+ * stands around the Linears of a layer.
  *
  * The operation is the FP8 mixed-precision Linear of the DeepSeek-V3 report
  * (Chinese translation, chapter 3 "Infrastructure"):
@@ -610,6 +611,146 @@ int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, in
                            int64_t ldl, const int32_t* idx, int64_t topk, int64_t ldidx, const int32_t* seq_off,
                            int64_t sequences, int score, float coef, const int32_t* counts, const int32_t* real,
                            void* dlogits, int64_t lddl, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the Linears of a layer (report section 3.3.1: norms, gating and the
+ * sums of the experts' outputs stay in BF16 or FP32): the RMS norm whose output
+ * is the FP8 Linear's operand, tokens to their experts' rows and back, and the
+ * products of generated tokens with 4-bit weights. Types are fp8bq_dtype values;
+ * 16- and 32-bit matrices need no alignment beyond their element's, and sums are
+ * float32 in a fixed order: the same result at every call.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * RMS norm of rows, after the residual's addition, quantised for the next FP8
+ * Linear:
+ *   h = x + residual (x without one);  rstd = 1 / sqrt(mean_c h^2 + eps);
+ *   y = h * rstd * weight,
+ * all in float32, the norm of the sum before it is rounded.
+ * x         [rows, cols] of xtype, ldx >= cols; cols 1 .. 32768.
+ * residual  NULL, or [rows, cols] of xtype, ldr >= cols; then h (required)
+ *           receives the sum rounded to xtype, ldh >= cols. h may be residual
+ *           or x itself (with the same ld).
+ * weight    [cols] of wtype.
+ * y         NULL, or [rows, cols] of xtype: y rounded once.
+ * q, s      both NULL, or E4M3 [rows, cols] and scales in the layout and by the
+ *           rule of fp8bq_quant_act_1x128 (ROWWISE) for the float32 values of y
+ *           (not y's rounded ones); cols a multiple of 128. One of y and q is
+ *           required. NaN gives the code 0x7F or 0xFF (NaN), an infinity makes its
+ *           tile NaN (with power-of-two scales only itself); other tiles of the
+ *           row follow from rstd, which such a row makes NaN or 0.
+ * rstd      NULL, or float [rows].
+ * eps       finite, >= 0 (a row of zeros with eps = 0 is NaN). Sums of squares
+ *           are float32: rows whose mean square passes 3e38 become 0.
+ * flags     0 or FP8BQ_SCALE_POW2.
+ * Errors: E_INVAL (null, sizes <= 0, ld too small, bad type, flags or eps, h
+ *         without residual), E_SHAPE (cols % 128 with q, cols above 32768, too
+ *         large), E_ALIGN (elements; q 16-byte aligned, ldq a multiple of 16; s,
+ *         rstd 4-byte aligned), E_DEVICE, E_HIP.
+ */
+int fp8bq_rmsnorm(const void* x, int xtype, int64_t rows, int64_t cols, int64_t ldx,
+                  const void* residual, int64_t ldr, const void* weight, int wtype, float eps,
+                  void* h, int64_t ldh, void* y, int64_t ldy, void* q, int64_t ldq, float* s, int64_t lds,
+                  float* rstd, int flags, void* stream);
+
+/*
+ * Its gradient, from dy (of y; the quantisation passes gradients through), the
+ * h and rstd of the forward pass (x where there was no residual) and dh, the
+ * gradient that reaches h besides (NULL: none):
+ *   dx = rstd * (dy * weight - h * rstd * mean_c(dy * weight * h * rstd)) + dh,
+ * which is the gradient of x and of the residual, and
+ *   dweight = sum over rows of dy * h * rstd   (float [cols]).
+ * dy, h, dh, dx  [rows, cols] of type. dx may be dh or dy (with the same ld).
+ * workspace      fp8bq_rmsnorm_grad_workspace_size bytes, 4-byte aligned,
+ *                contents irrelevant; calls that run at the same time need one
+ *                each.
+ * Errors as fp8bq_rmsnorm.
+ */
+int fp8bq_rmsnorm_grad_workspace_size(int64_t rows, int64_t cols, int64_t* bytes);
+int fp8bq_rmsnorm_grad(const void* dy, int type, int64_t rows, int64_t cols, int64_t lddy, const void* h, int64_t ldh,
+                       const void* weight, int wtype, const float* rstd, const void* dh, int64_t lddh,
+                       void* dx, int64_t lddx, float* dweight, void* workspace, void* stream);
+
+/*
+ * Tokens to the rows of a dispatch plan (fp8bq_moe_plan): row pos[t][j] of out
+ * is row t of x, bit for bit; rows without a token (src[r] outside [0, tokens))
+ * are zeros, and those marked FP8BQ_ROW_UNUSED are left as they were. Rows of
+ * 16 or 32 bits, or the 8-bit codes of tokens quantised before the dispatch
+ * (report section 3.3.3, "low-precision communication") with their scales. Its
+ * gradient is fp8bq_moe_combine of the rows' gradients with weight and base NULL.
+ * x        [tokens, cols] of `elem` (1, 2 or 4) bytes an element, ldx >= cols.
+ * s, so    both NULL, or (elem 1, cols a multiple of 128) scales of 1x128 tiles:
+ *          tile (t, c) at s[c * lds + t], lds >= tokens, and of the dispatched
+ *          rows at so[c * ldso + r], ldso >= rows; 0 for rows without a token.
+ * pos, src of one plan: int32 [tokens, topk] (contiguous; entries outside
+ *          [0, rows) are skipped) and int32 [rows]. No two entries of pos may
+ *          name the same row.
+ * out      [rows, cols], ldo >= cols.
+ * Errors: E_INVAL, E_SHAPE, E_ALIGN (elements), E_DEVICE, E_HIP.
+ */
+int fp8bq_moe_dispatch(const void* x, int elem, int64_t tokens, int64_t cols, int64_t ldx, const float* s, int64_t lds,
+                       const int32_t* pos, int64_t topk, const int32_t* src, int64_t rows,
+                       void* out, int64_t ldo, float* so, int64_t ldso, void* stream);
+
+/*
+ * Rows back to their tokens:
+ *   out[t] = base[t] + sum_j weight[t][j] * y[pos[t][j]],
+ * choices in their order, those whose pos lies outside [0, rows) left out (their
+ * weight is not looked at; a token without any gets base[t], or zeros).
+ * y        [rows, cols] of type, ldy >= cols: the experts' outputs.
+ * weight   float [tokens, topk], ldw >= topk, or NULL (ones).
+ * base     [tokens, cols] of type (a residual, a shared expert's output), ldb >=
+ *          cols, or NULL. Its gradient is the output's.
+ * out      [tokens, cols] of type, rounded once; may be base (with the same ld).
+ * Errors as fp8bq_moe_dispatch.
+ */
+int fp8bq_moe_combine(const void* y, int type, int64_t rows, int64_t cols, int64_t ldy, const int32_t* pos,
+                      int64_t tokens, int64_t topk, const float* weight, int64_t ldw, const void* base, int64_t ldb,
+                      void* out, int64_t ldo, void* stream);
+
+/*
+ * Its gradient: dy[pos[t][j]] = weight[t][j] * dout[t] (zeros in rows without a
+ * token, rows marked FP8BQ_ROW_UNUSED left as they were) and
+ * dweight[t][j] = dout[t] . y[pos[t][j]] (0 for a choice that was left out).
+ * dout [tokens, cols], y and dy [rows, cols] of type; dweight float
+ * [tokens, topk], contiguous; src, pos of one plan. dy must not be y.
+ * Errors as fp8bq_moe_dispatch.
+ */
+int fp8bq_moe_combine_grad(const void* dout, int type, int64_t tokens, int64_t cols, int64_t lddout, const void* y,
+                           int64_t rows, int64_t ldy, const int32_t* pos, int64_t topk, const float* weight, int64_t ldw,
+                           const int32_t* src, void* dy, int64_t lddy, float* dweight, void* stream);
+
+/*
+ * Product of a few rows with an MXFP4 weight, the rows kept as they are
+ * (fp8bq_gemm_mxfp4 takes rows quantised to 4 bits):
+ *   out[i][j] = sum_k x[i][k] * b_hat[j][k],
+ * the weight's values exact, x exact in any of the three types, sums in float32,
+ * rounded once to otype. For generated tokens: the weight's bytes are the cost,
+ * and each is read once for up to 64 rows. Any m is computed, but from about a
+ * hundred rows on the quantised product is faster.
+ * x        [m, k] of xtype, ldx >= k. b, sb: as fp8bq_gemm_mxfp4's (codes and
+ *          scales past k, up to the next multiple of 256, zero).
+ * out      [m, n] of otype (any of the three), ldo >= n.
+ * The gradient of x is this product of the output's gradient with the weight
+ * quantised along its columns (qt, st).
+ * Errors: as fp8bq_gemm_mxfp4.
+ */
+int fp8bq_gemv_mxfp4(int64_t m, int64_t n, int64_t k, const void* x, int xtype, int64_t ldx, const void* b, int64_t ldb,
+                     const void* sb, int64_t ldsb, void* out, int otype, int64_t ldo, void* stream);
+
+/*
+ * The same over experts: rows [row_off[e], row_off[e + 1]) meet weight e (row_off
+ * DEVICE int32 [groups + 1], b, sb and the clamping as fp8bq_grouped_gemm_mxfp4;
+ * rows of no expert are left as they were in out).
+ * rows     rows that out (and src) hold.
+ * src      device int32 [rows], or NULL: row r is x[src[r]], of zeros where src[r]
+ *          lies outside [0, xrows), so that tokens need not be brought to their
+ *          rows first; without it row r is x[r], and xrows >= rows.
+ * Each expert's weight is read once for up to 64 of its rows.
+ */
+int fp8bq_grouped_gemv_mxfp4(int32_t groups, const int32_t* row_off, int64_t rows, int64_t n, int64_t k, const void* x,
+                             int xtype, int64_t xrows, int64_t ldx, const int32_t* src, const void* b, int64_t ldb,
+                             const void* sb, int64_t ldsb, void* out, int otype, int64_t ldo, void* stream);
 
 /* Thread-local description of the last non-OK status on this thread. */
 const char* fp8bq_last_error(void);
