@@ -63,7 +63,7 @@ int gemv(const char* who, bool grouped, int32_t groups, const int32_t* row_off, 
     if (!aligned(row_off, 4) || !aligned(src, 4))
       return entry_fail(FP8BQ_E_ALIGN, "%s: row_off and src must be 4-byte aligned", who);
   }
-  // 16 rows of the weight and of x a workgroup, of up to 512 threads; 65535 row tiles
+  // workgroups of up to 256 threads for 16 rows of the weight and up to 16 of x; 65535 row tiles (of two rows where m is 2 at most)
   if (m > 65535 * (int64_t)16 || xrows >= kMaxSide || n >= ((int64_t)1 << 26) || k >= ((int64_t)1 << 28) ||
       (n / 16 + 1) * (grouped ? groups : m / 16 + 1) >= ((int64_t)1 << 22))
     return entry_fail(FP8BQ_E_SHAPE, "%s: too large", who);

@@ -1,17 +1,27 @@
 // Products of a few unquantised rows with MXFP4 weights (weight-only 4 bit):
 // out[i][j] = sum_k x[i][k] 2^e[j][k / 32] c[j][k]. Definitions: include/fp8bq.h.
 //
-// The weight's bytes are the cost (17/32 an element, each read once), so it
-// goes from memory straight to registers: lane l of a wave takes 16 bytes, one
-// scale group of 32 codes, of weight row l % 16, so that four lanes read 64
-// neighbouring bytes of a row. v_cvt_scalef32_pk_bf16_fp4 turns two codes into
-// two bf16 with the scale applied, exactly (a code has two significant bits,
+// The weight's bytes are the cost (17/32 an element, each read once for up to 16
+// rows), so it goes from memory straight to registers: lane l of a wave takes 16
+// bytes, one scale group of 32 codes, of weight row l % 16, so that four lanes
+// read 64 neighbouring bytes of a row. v_cvt_scalef32_pk_bf16_fp4 turns two codes
+// into two bf16 with the scale applied, exactly (a code has two significant bits,
 // and bf16 the exponents of E8M0 with subnormals), and the products go through
-// the bf16 MFMA of 16 x 16 x 32: weights are its 16 rows, x its 16 columns,
-// and its 32 positions of K are 8 of each of the four lanes' groups; x is
-// fetched in the same order. Sums are fp32. fp16 and fp32 activations are split
-// into two and three bf16 terms whose sum is x exactly (11 = 8 + 3 and 24 = 8 +
-// 8 + 8 significant bits), each with an MFMA of its own.
+// the bf16 MFMA of 16 x 16 x 32: weights are its 16 rows, x its 16 columns, and
+// its 32 positions of K are 8 of each of the four lanes' groups; x is fetched in
+// the same order. Sums are fp32. fp32 activations are split into three bf16 terms
+// whose sum is x exactly (24 = 8 + 8 + 8 significant bits), each with an MFMA of
+// its own. fp16 ones meet weights decoded to fp16 where the scales of all lanes
+// allow that exactly, which a model's weights always do; else they are split into
+// two bf16 terms (11 = 8 + 3 bits).
+//
+// What bounds it: the weight's bytes, once enough loads are in flight. One row of
+// 18432 x 7168 (70 MB) takes 14.4 us, 15.8 with the weight out of the caches; the
+// same loads alone take 15. What it took (us, the same product): x loaded by the
+// lanes that use it 20 (a load for every lane of the MFMA's 16 columns fills the
+// 64 bytes a cycle of the CU's vector cache), x held in registers over many
+// weight tiles 30 and x staged for a workgroup with a barrier a step 19 (both
+// wait for memory in step), branches around the loads 27 to 40.
 #include "../../include/fp8bq.h"
 #include "elem.h"
 #include "layer.h"
@@ -24,39 +34,53 @@ namespace {
 
 typedef __bf16 v8bf16 __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf16 __attribute__((ext_vector_type(2)));
+typedef _Float16 v8f16 __attribute__((ext_vector_type(8)));
+typedef _Float16 v2f16 __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+// bf16 terms of an element of x.
 template <int T> constexpr int kTerms = T == FP8BQ_BF16 ? 1 : T == FP8BQ_FP16 ? 2 : 3;
 
-// Eight values of x as bf16 terms. Each term is the value's top 8 significant
-// bits (cut off, not rounded, so that no finite value becomes infinite); an
-// infinity or NaN stays in the first.
+// Eight values of x as bf16 terms. Each term is the top 8 significant bits of
+// what the ones before it leave (cut off, not rounded, so that no finite value
+// becomes infinite); an infinity or NaN stays in the first, the others are then
+// zero. SPECIAL: there may be one.
+template <int T, bool SPECIAL>
+__device__ __forceinline__ void split(const float (&x)[8], v8bf16 (&t)[kTerms<T>]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = x[i];
+#pragma unroll
+  for (int n = 0; n < kTerms<T>; ++n) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t b[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float& f = v[2 * i + h];
+        b[h] = __float_as_uint(f);
+        const float rest = f - __uint_as_float(b[h] & 0xFFFF0000u);
+        f = SPECIAL && (b[h] & 0x7F800000u) == 0x7F800000u ? 0.f : rest;
+        if (SPECIAL && (b[h] & 0x7FFFFFFFu) > 0x7F800000u) b[h] |= 0x400000u;      // a NaN whose bits are all low
+      }
+      w[i] = (b[0] >> 16) | (b[1] & 0xFFFF0000u);
+    }
+    __builtin_memcpy(&t[n], w, 16);
+  }
+}
 template <int T>
-__device__ __forceinline__ void split(const Raw8<T>& x, v8bf16 (&t)[kTerms<T>]) {
+__device__ __forceinline__ void terms_of(const Raw8<T>& x, v8bf16 (&t)[kTerms<T>]) {
   if constexpr (T == FP8BQ_BF16) {
     __builtin_memcpy(&t[0], &x, 16);
   } else {
     float v[8];
     values8<T>(x, v);
+    uint32_t top = 0;
 #pragma unroll
-    for (int n = 0; n < kTerms<T>; ++n) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t top[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& f = v[2 * i + h];
-          const uint32_t b = __float_as_uint(f);
-          top[h] = b >> 16;
-          if ((b & 0x7FFFFFFFu) > 0x7F800000u) top[h] |= 0x40;      // a NaN whose bits are all low
-          const float rest = f - __uint_as_float(b & 0xFFFF0000u);
-          f = (b & 0x7F800000u) == 0x7F800000u ? 0.f : rest;
-        }
-        w[i] = top[0] | (top[1] << 16);
-      }
-      __builtin_memcpy(&t[n], w, 16);
-    }
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    if (__any(top >= 0x7F800000u)) split<T, true>(v, t);
+    else split<T, false>(v, t);
   }
 }
 
@@ -65,127 +89,269 @@ __device__ __forceinline__ v8bf16 decode8(uint32_t codes, float scale) {
                c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
   return v8bf16{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
+__device__ __forceinline__ v8f16 decode8_f16(uint32_t codes, float scale) {
+  const v2f16 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1),
+              c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3);
+  return v8f16{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// fp16 holds a code times 2^e exactly for e from -23 (half of it is the
+// smallest subnormal) to 13 (6 * 2^13 = 49152): scale bytes 104 to 140.
+__device__ __forceinline__ bool fits_f16(uint32_t byte) { return byte - 104u <= 36u; }
 
-// A workgroup makes 16 * NT weight rows' results for 16 * MT rows of x at a
-// time; its waves take the chunks of 256 along K in turn and add up their sums
-// in LDS, in their order.
-template <int T, int MT, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void gemv_kernel(GemvArgs p) {
+template <int T>
+__device__ __forceinline__ void store4(void* out, int64_t at, int n, v4f v) {
   using E = typename Elem<T>::type;
-  __shared__ v4f part[WAVES][MT * NT][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lo = lane & 15, hi = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
-  const int chunks = (int)((p.k + 255) / 256);
-  const uint8_t *b = p.b, *sb = p.sb;
-  int64_t m0 = (int64_t)blockIdx.y * (16 * MT), m1 = min(m0 + 16 * MT, p.m);
-  if (p.groups) {
-    const int e = blockIdx.y;
-    m0 = min(max((int64_t)p.row_off[e], (int64_t)0), p.m);
-    m1 = min(max((int64_t)p.row_off[e + 1], m0), p.m);
-    b += (int64_t)e * p.n * p.ldb;
-    sb += (int64_t)e * chunks * p.ldsb * 8;
-  }
-  const uint8_t *pb[NT], *ps[NT];
+  E e[4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t row = min(n0 + 16 * t + lo, p.n - 1);       // rows past the end repeat the last one
-    pb[t] = b + row * p.ldb + 16 * hi;
-    ps[t] = sb + row * 8;
-  }
-  for (; m0 < m1; m0 += 16 * MT) {
-    const E* px[MT];
+  for (int r = 0; r < 4; ++r) e[r] = Elem<T>::round(v[r]);
+  E* p = static_cast<E*>(out) + at;
+  if (n >= 4) {
+    __builtin_memcpy(p, e, sizeof(e));
+  } else {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      int64_t row = m0 + 16 * t + lo;
-      px[t] = nullptr;
-      if (row < m1) {
-        if (p.src) row = p.src[row];
-        if (row >= 0 && row < p.xrows) px[t] = static_cast<const E*>(p.x) + row * p.ldx + 32 * hi;
-      }
-    }
-    v4f acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int c = wave; c < chunks; c += WAVES) {
-      uint4 q[NT][2];
-      uint2 s[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        q[t][0] = *reinterpret_cast<const uint4*>(pb[t] + (int64_t)c * 128);
-        q[t][1] = *reinterpret_cast<const uint4*>(pb[t] + (int64_t)c * 128 + 64);
-        s[t] = *reinterpret_cast<const uint2*>(ps[t] + (int64_t)c * p.ldsb * 8);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float scale[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) scale[t] = mx_scale(((h ? s[t].y : s[t].x) >> (8 * hi)) & 0xFFu);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t col = (int64_t)c * 256 + 128 * h + 8 * j, left = p.k - col - 32 * hi;
-          v8bf16 w[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint4 v = q[t][h];
-            w[t] = decode8(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w, scale[t]);
-          }
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            Raw8<T> x{};
-            if (px[i]) {
-              if (left >= 8) {
-                x = load8<T>(px[i] + col);
-              } else if (left > 0) {
-                E e[8] = {};
-#pragma unroll
-                for (int z = 0; z < 7; ++z)
-                  if (z < left) e[z] = px[i][col + z];
-                __builtin_memcpy(&x, e, sizeof(x));
-              }
-            }
-            v8bf16 terms[kTerms<T>];
-            split<T>(x, terms);
-#pragma unroll
-            for (int z = 0; z < kTerms<T>; ++z)
-#pragma unroll
-              for (int t = 0; t < NT; ++t) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[t], terms[z], acc[i][t], 0, 0, 0);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
-    __syncthreads();
-    // lane's 4 results: rows n0 + 16 j + 4 (lane / 16) .. + 3 of the weight, row m0 + 16 i + lane % 16 of x
-    for (int z = wave; z < MT * NT; z += WAVES) {
-      v4f v = part[0][z][lane];
-#pragma unroll
-      for (int u = 1; u < WAVES; ++u) v += part[u][z][lane];
-      const int64_t m = m0 + 16 * (z / NT) + lo, n = n0 + 16 * (z % NT) + 4 * hi;
-      if (m < m1) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (n + r >= p.n) break;
-          const int64_t at = m * p.ldo + n + r;
-          if (p.otype == FP8BQ_FP32) static_cast<float*>(p.out)[at] = v[r];
-          else if (p.otype == FP8BQ_BF16) static_cast<uint16_t*>(p.out)[at] = Elem<FP8BQ_BF16>::round(v[r]);
-          else static_cast<uint16_t*>(p.out)[at] = Elem<FP8BQ_FP16>::round(v[r]);
-        }
-      }
-    }
-    __syncthreads();                             // the next rows' sums go to the same place
+    for (int r = 0; r < 3; ++r)
+      if (r < n) p[r] = e[r];
   }
 }
 
+// ---------------------------------------------------------------------------
+// Up to 2 P rows of x (P = 1 .. 8): no barrier until the end. The waves of a
+// workgroup have the same 16 * NT weight rows and take the chunks of 256 along K
+// in turn; each passes its chunk of x through LDS of its own, where the lanes of
+// rows that are not there share those of the last one (a load for every lane
+// would cost the CU's 64 bytes a cycle of the vector cache 16 times for one row).
+// ---------------------------------------------------------------------------
+template <int T, int P, int NT>
+struct Few {
+  using E = typename Elem<T>::type;
+  static constexpr int kPlanes = T == FP8BQ_FP32 ? 3 : 1;
+  static constexpr int kRows = 2 * P;
+  struct Shared { uint4 x[kPlanes][kRows * 32]; };             // of one wave: [step][lane / 16][row]
+  struct Stage {
+    Raw8<T> x[P];
+    uint4 q[NT][2];
+    uint2 s[NT];
+  };
+  const GemvArgs& p;
+  Shared& sh;
+  int lane, lo, hi;
+  const uint8_t *b, *sb;                 // of the workgroup's first weight row
+  uint32_t ob[NT], os[NT];
+  const E* px[P];                        // what this lane loads of a chunk
+
+  // Unit u (8 elements) of row r: step z of the MFMAs takes it to lane 16 h + r.
+  static __device__ __forceinline__ int slot(int r, int z, int h) {
+    const int at = (z * 4 + h) * kRows + r;
+    return kRows >= 8 ? at ^ ((z & 3) + 4 * (h & 1)) : at;     // neighbouring units of a row to different banks
+  }
+  __device__ __forceinline__ void load_codes(Stage& t, int c) const {
+    const uint8_t *bc = b + (int64_t)c * 128, *sc = sb + (int64_t)c * p.ldsb * 8;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      t.q[i][0] = *reinterpret_cast<const uint4*>(bc + ob[i]);
+      t.q[i][1] = *reinterpret_cast<const uint4*>(bc + ob[i] + 64);
+      t.s[i] = *reinterpret_cast<const uint2*>(sc + os[i]);
+    }
+  }
+  // Chunk c, which px stands `ahead` chunks before. Nothing here or in the loop
+  // around it branches: behind a branch the compiler waits for every load in
+  // flight.
+  __device__ __forceinline__ void load(Stage& t, int c, int ahead = 0) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) t.x[i] = load8<T>(px[i] + ahead * 256);
+    load_codes(t, c);
+  }
+  __device__ __forceinline__ void advance(int chunks) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) px[i] += chunks * 256;
+  }
+  __device__ __forceinline__ void load_last(Stage& t, int c) const {
+    const int left = (int)(p.k - (int64_t)c * 256) - 8 * (lane & 31);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      E e[8] = {};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) e[j] = px[i][j];
+      __builtin_memcpy(&t.x[i], e, sizeof(e));
+    }
+    load_codes(t, c);
+  }
+  __device__ __forceinline__ void use(const Stage& t, v4f (&acc)[NT]) const {
+    const int u = lane & 31;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int at = slot(2 * i + (lane >> 5), (u >> 4) * 4 + (u & 3), (u >> 2) & 3);
+      if constexpr (kPlanes == 1) {
+        __builtin_memcpy(&sh.x[0][at], &t.x[i], 16);
+      } else {
+        v8bf16 terms[kTerms<T>];
+        terms_of<T>(t.x[i], terms);
+#pragma unroll
+        for (int n = 0; n < kPlanes; ++n) __builtin_memcpy(&sh.x[n][at], &terms[n], 16);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");     // the wave's LDS accesses stay in this order
+    bool fits = true;
+    uint32_t byte[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      byte[i][0] = (t.s[i].x >> (8 * hi)) & 0xFFu;
+      byte[i][1] = (t.s[i].y >> (8 * hi)) & 0xFFu;
+      fits = fits && fits_f16(byte[i][0]) && fits_f16(byte[i][1]);
+    }
+    const bool f16 = T == FP8BQ_FP16 && __all(fits);
+    const int r = min(lo, kRows - 1);
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      uint4 x[kPlanes];
+#pragma unroll
+      for (int n = 0; n < kPlanes; ++n) x[n] = sh.x[n][slot(r, z, hi)];
+      auto code = [&](int i) {
+        const uint4 v = t.q[i][z >> 2];
+        return (z & 3) == 0 ? v.x : (z & 3) == 1 ? v.y : (z & 3) == 2 ? v.z : v.w;
+      };
+      if (f16) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode8_f16(code(i), mx_scale(byte[i][z >> 2])), __builtin_bit_cast(v8f16, x[0]), acc[i], 0, 0, 0);
+        continue;
+      }
+      v8bf16 terms[kTerms<T>];
+      if constexpr (T == FP8BQ_FP16) {
+        terms_of<T>(__builtin_bit_cast(Raw8<T>, x[0]), terms);
+      } else {
+#pragma unroll
+        for (int n = 0; n < kPlanes; ++n) terms[n] = __builtin_bit_cast(v8bf16, x[n]);
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const v8bf16 w = decode8(code(i), mx_scale(byte[i][z >> 2]));
+#pragma unroll
+        for (int n = 0; n < kTerms<T>; ++n) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, terms[n], acc[i], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+};
+
+__device__ __forceinline__ void store_result(const GemvArgs& p, int64_t m, int64_t n, v4f v) {
+  if (n >= p.n) return;
+  if (p.src && !(p.src[m] >= 0 && p.src[m] < p.xrows)) v = v4f{0.f, 0.f, 0.f, 0.f};
+  const int left = (int)min((int64_t)4, p.n - n);
+  if (p.otype == FP8BQ_FP32) store4<FP8BQ_FP32>(p.out, m * p.ldo + n, left, v);
+  else if (p.otype == FP8BQ_BF16) store4<FP8BQ_BF16>(p.out, m * p.ldo + n, left, v);
+  else store4<FP8BQ_FP16>(p.out, m * p.ldo + n, left, v);
+}
+
+// Rows m0 .. m1 of the result, 2 P at a time, for weight rows n0 .. n0 + 16 NT.
+// lds: of WAVES * (sizeof(Few::Shared) + NT KB).
+template <int T, int P, int NT, int WAVES>
+__device__ __forceinline__ void few_rows(const GemvArgs& p, const uint8_t* b, const uint8_t* sb, int64_t n0, int64_t m0, int64_t m1, char* lds) {
+  using F = Few<T, P, NT>;
+  using E = typename Elem<T>::type;
+  const int whole = (int)(p.k / 256);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  v4f* part = reinterpret_cast<v4f*>(lds);       // [wave][tile][lane]
+  F f{p, reinterpret_cast<typename F::Shared*>(lds + WAVES * NT * 1024)[wave], lane, lane & 15, lane >> 4, b + n0 * p.ldb, sb + n0 * 8};
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const uint32_t r = (uint32_t)min((int64_t)(16 * i + f.lo), p.n - 1 - n0);       // rows past the end repeat the last one
+    f.ob[i] = r * (uint32_t)p.ldb + 16 * f.hi;
+    f.os[i] = r * 8;
+  }
+  for (; m0 < m1; m0 += F::kRows) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {        // rows past the end repeat the last one, rows of zeros take any
+      const int64_t r = min(m0 + 2 * i + (lane >> 5), m1 - 1), x = p.src ? p.src[r] : r;
+      f.px[i] = static_cast<const E*>(p.x) + (x >= 0 && x < p.xrows ? x : 0) * p.ldx + 8 * (lane & 31) + wave * 256;
+    }
+    v4f acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    typename F::Stage st[2];
+    int c = wave;
+    if (c < whole) {
+      f.load(st[0], c);
+      for (; c + WAVES < whole; c += 2 * WAVES) {
+        f.load(st[1], c + WAVES, WAVES);
+        f.use(st[0], acc);
+        const int next = min(c + 2 * WAVES, whole - 1);        // the last load may be one that nobody uses
+        f.advance(next - c);
+        f.load(st[0], next);
+        f.use(st[1], acc);
+      }
+      if (c < whole) {
+        f.use(st[0], acc);
+        f.advance(WAVES);
+        c += WAVES;
+      } else {
+        f.advance(c - (whole - 1));
+      }
+    }
+    if (c == whole && p.k % 256) {       // the chunk that k ends in
+      f.load_last(st[0], c);
+      f.use(st[0], acc);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) part[(wave * NT + i) * 64 + lane] = acc[i];
+    __syncthreads();
+    for (int i = wave; i < NT; i += WAVES) {
+      v4f v = part[i * 64 + lane];
+#pragma unroll
+      for (int u = 1; u < WAVES; ++u) v += part[(u * NT + i) * 64 + lane];
+      if (f.lo < F::kRows && m0 + f.lo < m1) store_result(p, m0 + f.lo, n0 + 16 * i + 4 * f.hi, v);
+    }
+    __syncthreads();                     // the next rows' sums go to the same place
+  }
+}
+
+// One product: P by the number of rows.
+template <int T, int P, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void gemv_kernel(GemvArgs p) {
+  __shared__ __align__(16) char lds[WAVES * (sizeof(typename Few<T, P, NT>::Shared) + NT * 1024)];
+  const int64_t m0 = (int64_t)blockIdx.y * (2 * P);
+  few_rows<T, P, NT, WAVES>(p, p.b, p.sb, (int64_t)blockIdx.x * (16 * NT), m0, min(m0 + 2 * P, p.m), lds);
+}
+
+// Experts: only here are the numbers of their rows known.
+template <int T, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void grouped_gemv_kernel(GemvArgs p) {
+  __shared__ __align__(16) char lds[WAVES * (sizeof(typename Few<T, 8, NT>::Shared) + NT * 1024)];
+  const int e = blockIdx.y;
+  const int64_t m0 = min(max((int64_t)p.row_off[e], (int64_t)0), p.m), m1 = min(max((int64_t)p.row_off[e + 1], m0), p.m);
+  const uint8_t *b = p.b + (int64_t)e * p.n * p.ldb, *sb = p.sb + (int64_t)e * ((p.k + 255) / 256) * p.ldsb * 8;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
+  if (m1 - m0 <= 2) few_rows<T, 1, NT, WAVES>(p, b, sb, n0, m0, m1, lds);
+  else if (m1 - m0 <= 4) few_rows<T, 2, NT, WAVES>(p, b, sb, n0, m0, m1, lds);
+  else few_rows<T, 8, NT, WAVES>(p, b, sb, n0, m0, m1, lds);
+}
+
+template <int T, int P, int NT, int WAVES>
+void launch_dense(const GemvArgs& p, hipStream_t st) {
+  const dim3 grid((unsigned)((p.n + 16 * NT - 1) / (16 * NT)), (unsigned)((p.m + 2 * P - 1) / (2 * P)));
+  gemv_kernel<T, P, NT, WAVES><<<grid, 64 * WAVES, 0, st>>>(p);
+}
+template <int T, int NT, int WAVES>
+void launch_grouped(const GemvArgs& p, hipStream_t st) {
+  const dim3 grid((unsigned)((p.n + 16 * NT - 1) / (16 * NT)), (unsigned)p.groups);
+  grouped_gemv_kernel<T, NT, WAVES><<<grid, 64 * WAVES, 0, st>>>(p);
+}
+// Rows in passes of 2 P, the fewest that hold them all up to 16. One weight tile
+// a wave; two for more than 8 rows, so that x is loaded half as often, unless n is
+// too small to fill the chip with pairs (us with one / two tiles, 16 rows of bf16:
+// 18432 x 7168 21.7 / 19.9, 7168 x 2048 5.9 / 5.1, 2048 x 7168 6.2 / 7.9; 8 rows
+// of 18432 x 7168 16.3 / 16.7). Four waves share K; two for 16 rows of fp32, whose
+// x takes 24 KB of LDS a wave (57.8 / 47.4 us with four / two).
 template <int T>
 hipError_t run(const GemvArgs& p, hipStream_t st) {
-  const dim3 grid((unsigned)((p.n + 15) / 16), (unsigned)(p.groups ? p.groups : (p.m + 15) / 16));
-  gemv_kernel<T, 1, 1, 8><<<grid, 512, 0, st>>>(p);
+  constexpr int kWide = T == FP8BQ_FP32 ? 2 : 4;
+  if (p.groups) launch_grouped<T, 2, 2>(p, st);    // 32 tokens to 32 of 256 experts, 2048 x 7168: 60 us; pairs of tiles with four
+  else if (p.m <= 2) launch_dense<T, 1, 1, 4>(p, st);          // waves 58, but 30 against 25 where every expert has 8 rows
+  else if (p.m <= 4) launch_dense<T, 2, 1, 4>(p, st);
+  else if (p.m <= 8) launch_dense<T, 4, 1, 4>(p, st);
+  else if (p.n >= 4096) launch_dense<T, 8, 2, kWide>(p, st);
+  else launch_dense<T, 8, 1, kWide>(p, st);
   return hipGetLastError();
 }
 

@@ -725,9 +725,9 @@ int fp8bq_moe_combine_grad(const void* dout, int type, int64_t tokens, int64_t c
  * (fp8bq_gemm_mxfp4 takes rows quantised to 4 bits):
  *   out[i][j] = sum_k x[i][k] * b_hat[j][k],
  * the weight's values exact, x exact in any of the three types, sums in float32,
- * rounded once to otype. For generated tokens: the weight's bytes are the cost,
- * and each is read once for up to 64 rows. Any m is computed, but from about a
- * hundred rows on the quantised product is faster.
+ * rounded once to otype. For generated tokens: the weight's bytes are the cost.
+ * Any m is computed, in passes of 16 rows that read the weight again (from 17 rows
+ * on the quantised product is faster, where its accuracy serves).
  * x        [m, k] of xtype, ldx >= k. b, sb: as fp8bq_gemm_mxfp4's (codes and
  *          scales past k, up to the next multiple of 256, zero).
  * out      [m, n] of otype (any of the three), ldo >= n.
@@ -746,7 +746,7 @@ int fp8bq_gemv_mxfp4(int64_t m, int64_t n, int64_t k, const void* x, int xtype, 
  * src      device int32 [rows], or NULL: row r is x[src[r]], of zeros where src[r]
  *          lies outside [0, xrows), so that tokens need not be brought to their
  *          rows first; without it row r is x[r], and xrows >= rows.
- * Each expert's weight is read once for up to 64 of its rows.
+ * Each expert's weight is read once for up to 16 of its rows.
  */
 int fp8bq_grouped_gemv_mxfp4(int32_t groups, const int32_t* row_off, int64_t rows, int64_t n, int64_t k, const void* x,
                              int xtype, int64_t xrows, int64_t ldx, const int32_t* src, const void* b, int64_t ldb,

@@ -121,14 +121,19 @@ def test_padded_codes_and_outputs():
 
 
 def test_a_row_does_not_depend_on_the_others():
+    """The same at every call, and rows of a pass of 16 are those of a call of their own."""
     import torch
     w, ws, _ = operand(9, 200, 1500)
     x = matrix(10, 80, 1500)
     whole = fb.gemv_mxfp4(x, w, ws)
     assert torch.equal(whole, fb.gemv_mxfp4(x, w, ws))
+    for lo in (0, 16, 64):
+        assert torch.equal(fb.gemv_mxfp4(x[lo:lo + 16], w, ws), whole[lo:lo + 16])
     off = torch.tensor([0, 80], dtype=torch.int32, device="cuda")
-    assert torch.equal(fb.gemv_mxfp4(x[:16], w, ws), fb.gemv_mxfp4(x[:16].contiguous(), w, ws))
-    assert torch.equal(whole, fb.grouped_gemv_mxfp4(off, x, w[None], ws[None]))
+    grouped = fb.grouped_gemv_mxfp4(off, x, w[None], ws[None])
+    for lo in (0, 16, 64):
+        part = torch.tensor([0, 16], dtype=torch.int32, device="cuda")
+        assert torch.equal(fb.grouped_gemv_mxfp4(part, x[lo:lo + 16], w[None], ws[None]), grouped[lo:lo + 16])
 
 
 def experts(seed, groups, n, k):
