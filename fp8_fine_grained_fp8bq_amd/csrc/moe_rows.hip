@@ -11,7 +11,8 @@
 namespace fp8bq {
 namespace {
 
-constexpr int kChoices = 8;              // choices whose loads are in flight together
+constexpr int kUnit = 8;                 // elements of a lane
+constexpr int kChoices = 4;              // choices whose loads are in flight together
 
 // Work is numbered in blocks of four waves; workgroups beyond a launch's limit
 // take several.
@@ -50,24 +51,19 @@ __device__ __forceinline__ void zero_row(uint8_t* p, int64_t bytes, int elem) {
   const int64_t items = items_of(bytes, elem);
   for (int64_t i = threadIdx.x & 63; i < items; i += 64) {
     const Item it(i, bytes, elem);
-    if (it.whole) __builtin_memcpy(p + it.at, &z, 16);
+    if (it.whole) stream_store(p + it.at, z);
     else store_element(p + it.at, 0, elem);
   }
 }
 
 // The rows of a plan that no token has (src outside the tokens, but not
-// FP8BQ_ROW_UNUSED): 64 rows a wave.
+// FP8BQ_ROW_UNUSED): four rows a wave.
+constexpr int kPadRows = 16;             // of a block
 __device__ __forceinline__ void zero_padding(const int32_t* src, int64_t rows, int64_t tokens, uint8_t* out, int64_t row_stride,
                                              int64_t bytes, int elem, int64_t w) {
-  const int64_t r0 = w * 64;
-  const int lane = threadIdx.x & 63;
-  int s = FP8BQ_ROW_UNUSED;
-  if (r0 + lane < rows) s = src[r0 + lane];
-  uint64_t m = __ballot(s != FP8BQ_ROW_UNUSED && (s < 0 || s >= tokens));
-  while (m) {
-    const int i = __builtin_ctzll(m);
-    m &= m - 1;
-    zero_row(out + (r0 + i) * row_stride, bytes, elem);
+  for (int64_t r = w * (kPadRows / 4); r < min((w + 1) * (kPadRows / 4), rows); ++r) {
+    const int s = src[r];
+    if (s != FP8BQ_ROW_UNUSED && (s < 0 || s >= tokens)) zero_row(out + r * row_stride, bytes, elem);
   }
 }
 
@@ -87,13 +83,13 @@ __device__ __forceinline__ void dispatch_block(const MoeDispatchArgs& a, int64_t
     const uint8_t* p = a.x + t * a.ldx * a.elem + it.at;
     const int32_t* pos = a.pos + t * a.topk;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (it.whole) __builtin_memcpy(&v, p, 16);
+    if (it.whole) v = load_any<uint4>(p);
     else v.x = load_element(p, a.elem);
     for (int j = 0; j < a.topk; ++j) {
       const int64_t r = pos[j];
       if (r < 0 || r >= a.rows) continue;
       uint8_t* o = a.out + r * a.ldo * a.elem + it.at;
-      if (it.whole) __builtin_memcpy(o, &v, 16);
+      if (it.whole) stream_store(o, v);
       else store_element(o, v.x, a.elem);
     }
     return;
@@ -121,22 +117,17 @@ __global__ __launch_bounds__(256) void moe_dispatch_kernel(MoeDispatchArgs a, in
 template <int T, int N>
 __device__ __forceinline__ void combine(const MoeCombineArgs& a, int64_t t, int64_t col) {
   using E = typename Elem<T>::type;
-  struct Some { E e[N]; };
+  using V = Some<T, N>;
   const E* y = static_cast<const E*>(a.y) + col;
   const int32_t* pos = a.pos + t * a.topk;
   const float* gate = a.w ? a.w + t * a.ldw : nullptr;
-  auto load = [](const E* p) {
-    Some v;
-    __builtin_memcpy(&v, p, sizeof(v));
-    return v;
-  };
   float sum[N];
-  Some base{};
-  if (a.base) base = load(static_cast<const E*>(a.base) + t * a.ldb + col);
+  V base{};
+  if (a.base) base = load_any<V>(static_cast<const E*>(a.base) + t * a.ldb + col);
 #pragma unroll
   for (int i = 0; i < N; ++i) sum[i] = Elem<T>::value(base.e[i]);
   for (int j0 = 0; j0 < a.topk; j0 += kChoices) {
-    Some v[kChoices];
+    V v[kChoices];
     float g[kChoices];
     bool on[kChoices];
 #pragma unroll
@@ -144,9 +135,9 @@ __device__ __forceinline__ void combine(const MoeCombineArgs& a, int64_t t, int6
       const int64_t r = j0 + j < a.topk ? pos[j0 + j] : -1;
       on[j] = r >= 0 && r < a.rows;
       g[j] = 1.f;
-      v[j] = Some{};
+      v[j] = V{};
       if (on[j]) {
-        v[j] = load(y + r * a.ldy);
+        v[j] = load_any<V>(y + r * a.ldy);
         if (gate) g[j] = gate[j0 + j];
       }
     }
@@ -158,20 +149,21 @@ __device__ __forceinline__ void combine(const MoeCombineArgs& a, int64_t t, int6
       }
     }
   }
-  Some o;
+  V o;
 #pragma unroll
   for (int i = 0; i < N; ++i) o.e[i] = Elem<T>::round(sum[i]);
-  __builtin_memcpy(static_cast<E*>(a.out) + t * a.ldo + col, &o, sizeof(o));
+  stream_store(static_cast<E*>(a.out) + t * a.ldo + col, o);
 }
 
 template <int T>
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeCombineArgs a, int64_t blocks) {
-  const int64_t units = a.cols >> 3, pieces = (units + (a.cols & 7) + 63) / 64;
+  constexpr int N = kUnit;
+  const int64_t units = a.cols / N, left = a.cols % N, pieces = (units + left + 63) / 64;
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t w = wave_of(b), t = w / pieces, i = (w - t * pieces) * 64 + (threadIdx.x & 63);
     if (t >= a.tokens) return;
-    if (i < units) combine<T, 8>(a, t, i * 8);
-    else if (i - units < (a.cols & 7)) combine<T, 1>(a, t, units * 8 + i - units);
+    if (i < units) combine<T, N>(a, t, i * N);
+    else if (i - units < left) combine<T, 1>(a, t, units * N + i - units);
   }
 }
 
@@ -209,11 +201,11 @@ __device__ __forceinline__ void combine_grad(const MoeCombineGradArgs& a, int64_
     for (int64_t col = threadIdx.x * 8; col < whole; col += 2048) {
       float f[8];
       Raw8<T> v[kChoices];
-      values8<T>(load8<T>(d + col), f);
+      values8<T>(load_any<Raw8<T>>(d + col), f);
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) {
         v[j] = Raw8<T>{};
-        if (row[j] >= 0) v[j] = load8<T>(y + row[j] * a.ldy + col);
+        if (row[j] >= 0) v[j] = load_any<Raw8<T>>(y + row[j] * a.ldy + col);
       }
 #pragma unroll
       for (int j = 0; j < kChoices; ++j) {
@@ -225,7 +217,7 @@ __device__ __forceinline__ void combine_grad(const MoeCombineGradArgs& a, int64_
             dot[j] = __builtin_fmaf(f[i], e[i], dot[j]);
             o[i] = g[j] * f[i];
           }
-          store8<T>(dy + row[j] * a.lddy + col, o);
+          stream_store(dy + row[j] * a.lddy + col, round8<T>(o));
         }
       }
     }
@@ -261,14 +253,14 @@ unsigned grid_of(int64_t blocks) { return (unsigned)(blocks < kMaxGrid ? blocks 
 }  // namespace
 
 hipError_t launch_moe_dispatch(const MoeDispatchArgs& a, hipStream_t st) {
-  const int64_t copy = (a.tokens * ((items_of(a.cols * a.elem, a.elem) + 63) / 64) + 3) / 4, pad = (a.rows + 255) / 256;
-  const int64_t scales = a.s ? pad * ((a.cols / 128 + 7) / 8) : 0;
+  const int64_t copy = (a.tokens * ((items_of(a.cols * a.elem, a.elem) + 63) / 64) + 3) / 4, pad = (a.rows + kPadRows - 1) / kPadRows;
+  const int64_t scales = a.s ? (a.rows + 255) / 256 * ((a.cols / 128 + 7) / 8) : 0;
   moe_dispatch_kernel<<<grid_of(copy + pad + scales), 256, 0, st>>>(a, copy, pad, copy + pad + scales);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const MoeCombineArgs& a, int type, hipStream_t st) {
-  const int64_t blocks = (a.tokens * ((a.cols / 8 + a.cols % 8 + 63) / 64) + 3) / 4;
+  const int64_t blocks = (a.tokens * ((a.cols / kUnit + a.cols % kUnit + 63) / 64) + 3) / 4;
   switch (type) {
     case FP8BQ_BF16: moe_combine_kernel<FP8BQ_BF16><<<grid_of(blocks), 256, 0, st>>>(a, blocks); break;
     case FP8BQ_FP16: moe_combine_kernel<FP8BQ_FP16><<<grid_of(blocks), 256, 0, st>>>(a, blocks); break;
@@ -278,7 +270,7 @@ hipError_t launch_moe_combine(const MoeCombineArgs& a, int type, hipStream_t st)
 }
 
 hipError_t launch_moe_combine_grad(const MoeCombineGradArgs& a, int type, hipStream_t st) {
-  const int64_t blocks = a.tokens + (a.rows + 255) / 256;
+  const int64_t blocks = a.tokens + (a.rows + kPadRows - 1) / kPadRows;
   switch (type) {
     case FP8BQ_BF16: moe_combine_grad_kernel<FP8BQ_BF16><<<grid_of(blocks), 256, 0, st>>>(a, blocks); break;
     case FP8BQ_FP16: moe_combine_grad_kernel<FP8BQ_FP16><<<grid_of(blocks), 256, 0, st>>>(a, blocks); break;

@@ -49,31 +49,30 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-// A lane's columns: U units and, of the up to 7 columns behind the last whole
-// unit, one.
+// A lane's columns: U units (0: rows of fewer than 8 columns) and, of the up to
+// 7 columns behind the last whole unit, one.
 template <int LANES, int U>
 struct Columns {
-  int l, step, full;
+  int l, step, full, odd;
   int64_t last;                          // the odd column, or -1
-  __device__ Columns(int lane, int cols) : l(lane), step(lanes_of_row<LANES>()), full(cols >> 3) {
-    last = l < (cols & 7) ? (cols & ~7) + l : -1;
+  __device__ Columns(int lane, int cols) : l(lane), step(lanes_of_row<LANES>()), full(cols >> 3), odd(cols & 7) {
+    last = l < odd ? (cols & ~7) + l : -1;
   }
   __device__ __forceinline__ bool has(int u) const { return l + u * step < full; }
   __device__ __forceinline__ int64_t col(int u) const { return 8 * (int64_t)(l + u * step); }
+  // Where a lane loads from: lanes without the unit share the row's last one.
+  __device__ __forceinline__ int64_t source(int u) const { return 8 * (int64_t)min(l + u * step, full - 1); }
 };
+template <int U> constexpr int kSome = U ? U : 1;
 
-// A lane's weights, of any of the three types (one of `base` elements in).
+// A lane's weights, of any of the three types.
 template <int LANES, int U>
-__device__ __forceinline__ void load_weights(const void* w, int wtype, const Columns<LANES, U>& c, float (&v)[U][8], float& last) {
+__device__ __forceinline__ void load_weights(const void* w, int wtype, const Columns<LANES, U>& c, float (&v)[kSome<U>][8], float& last) {
   auto get = [&](auto t) {
     constexpr int T = decltype(t)::value;
     const auto* p = static_cast<const typename Elem<T>::type*>(w);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-      if (c.has(u)) values8<T>(load8<T>(p + c.col(u)), v[u]);
-    }
+    for (int u = 0; u < U; ++u) values8<T>(load8<T>(p + c.source(u)), v[u]);
     last = c.last >= 0 ? Elem<T>::value(p[c.last]) : 0.f;
   };
   if (wtype == FP8BQ_FP32) get(std::integral_constant<int, FP8BQ_FP32>{});
@@ -81,21 +80,27 @@ __device__ __forceinline__ void load_weights(const void* w, int wtype, const Col
   else get(std::integral_constant<int, FP8BQ_FP16>{});
 }
 
-// A lane's elements of the row at p, zeros where it has none.
+// A lane's elements of the row at p. Every lane loads, and what it has no column
+// for is set to zero after: loads under a lane's branch are waited for where the
+// branch ends, one after the other (4096 x 7168 back: 58 us, 70 to 84 then).
 template <int T, int U>
 struct Row {
-  Raw8<T> unit[U];
+  Raw8<T> unit[kSome<U>];
   typename Elem<T>::type last;
   template <int LANES>
-  __device__ __forceinline__ void load(const void* base, int64_t at, const Columns<LANES, U>& c, bool here) {
+  __device__ __forceinline__ void load(const void* base, int64_t at, const Columns<LANES, U>& c) {
     const auto* p = static_cast<const typename Elem<T>::type*>(base) + at;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      unit[u] = Raw8<T>{};
-      if (here && c.has(u)) unit[u] = load8<T>(p + c.col(u));
-    }
     last = {};
-    if (here && c.last >= 0) last = p[c.last];
+    if (c.odd) last = p[max(c.last, (int64_t)0)];              // uniform
+#pragma unroll
+    for (int u = 0; u < U; ++u) unit[u] = load8<T>(p + c.source(u));
+  }
+  template <int LANES>
+  __device__ __forceinline__ void clear(const Columns<LANES, U>& c, bool here = true) {
+    if (!here || c.last < 0) last = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (!here || !c.has(u)) unit[u] = Raw8<T>{};
   }
 };
 
@@ -127,17 +132,20 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
   const int per_block = LANES == kBlockRow ? 1 : 256 / LANES;
   const int sub = LANES == kBlockRow ? 0 : threadIdx.x / LANES;
   const Columns<LANES, U> c(LANES == kBlockRow ? threadIdx.x : threadIdx.x % LANES, a.cols);
-  float w[U][8], wlast;
+  float w[kSome<U>][8], wlast;
   load_weights(a.w, a.wtype, c, w, wlast);
 
   int turn = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * per_block; row0 < a.rows; row0 += (int64_t)gridDim.x * per_block, turn ^= 1) {
     const int64_t row = row0 + sub;
     const bool here = row < a.rows;              // (a whole workgroup's row always is)
+    const int64_t from = here ? row : a.rows - 1;
     Row<T, U> x, r;
-    x.load(a.x, row * a.ldx, c, here);
-    if constexpr (RES) r.load(a.r, row * a.ldr, c, here);
-    float v[U][8], vlast = Elem<T>::value(x.last);
+    x.load(a.x, from * a.ldx, c);
+    if constexpr (RES) r.load(a.r, from * a.ldr, c);
+    x.clear(c);
+    if constexpr (RES) r.clear(c);
+    float v[kSome<U>][8], vlast = Elem<T>::value(x.last);
     if constexpr (RES) {
       vlast += Elem<T>::value(r.last);
       if (here && c.last >= 0) static_cast<E*>(a.h)[row * a.ldh + c.last] = Elem<T>::round(vlast);
@@ -151,7 +159,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
         values8<T>(r.unit[u], o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[u][i] += o[i];
-        if (here && c.has(u)) store8<T>(static_cast<E*>(a.h) + row * a.ldh + c.col(u), v[u]);
+        if (here && c.has(u)) stream_store(static_cast<E*>(a.h) + row * a.ldh + c.col(u), round8<T>(v[u]));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[u][i], v[u][i], ss);
@@ -161,27 +169,46 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
     if (a.y && here && c.last >= 0) static_cast<E*>(a.y)[row * a.ldy + c.last] = Elem<T>::round(vlast * rstd * wlast);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * rstd * w[u][i];
       const bool mine = here && c.has(u);
-      if (a.y && mine) store8<T>(static_cast<E*>(a.y) + row * a.ldy + c.col(u), v[u]);
-      if (a.q) {                                 // cols is a multiple of 128: a tile's 16 lanes have the unit or not together
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = v[u][i] * rstd * w[u][i];
+      TileScale t;
+      uint2 e;
+      auto encode = [&](const float (&f)[8], auto p2) {
+        e.x = encode4<decltype(p2)::value>(f[0], f[1], f[2], f[3], t);
+        e.y = encode4<decltype(p2)::value>(f[4], f[5], f[6], f[7], t);
+      };
+      auto amax = [](const float (&f)[8]) {
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[u][i]));
-        const TileScale t = tile_scale(row16_max(m), pow2);
-        uint2 e;
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+        return row16_max(m);
+      };
+      if (a.q) {                                 // cols is a multiple of 128: a tile's 16 lanes have the unit or not together
         if (pow2) {
-          e.x = encode4<true>(v[u][0], v[u][1], v[u][2], v[u][3], t);
-          e.y = encode4<true>(v[u][4], v[u][5], v[u][6], v[u][7], t);
+          t = tile_scale(amax(y), true);
+          encode(y, std::true_type{});
         } else {
-          e.x = encode4<false>(v[u][0], v[u][1], v[u][2], v[u][3], t);
-          e.y = encode4<false>(v[u][4], v[u][5], v[u][6], v[u][7], t);
+          // rstd is a factor of the whole tile: it goes into the scale, and the codes come from h w, off by the roundings
+          // of that product, of the tile's amax / 448 and of the quotient only. Where h w may have underflowed, from y.
+          float hw[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) hw[i] = v[u][i] * w[u][i];
+          t = tile_scale(amax(hw), false);
+          if (t.s >= kFastScaleMin) {
+            encode(hw, std::false_type{});
+            t.s *= rstd;
+          } else {
+            t = tile_scale(amax(y), false);
+            encode(y, std::false_type{});
+          }
         }
-        if (mine) {
-          *reinterpret_cast<uint2*>(a.q + row * a.ldq + c.col(u)) = e;
-          if ((c.l & 15) == 0) a.s[(c.col(u) >> 7) * a.lds + row] = t.s;
-        }
+      }
+      if (a.y && mine) stream_store(static_cast<E*>(a.y) + row * a.ldy + c.col(u), round8<T>(y));
+      if (a.q && mine) {
+        *reinterpret_cast<uint2*>(a.q + row * a.ldq + c.col(u)) = e;
+        if ((c.l & 15) == 0) a.s[(c.col(u) >> 7) * a.lds + row] = t.s;
       }
     }
   }
@@ -189,18 +216,20 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
 
 // ---------------------------------------------------------------------------
 // Gradient. With xh = h rstd and g = dy w: dx = rstd (g - xh mean(g xh)) + dh,
-// dw = sum over the rows of dy xh. A group of lanes walks over rows, keeps its
-// columns' share of dw in registers and writes it out at its end; a second
-// kernel adds the groups' shares in their order.
+// dw = sum over the rows of dy xh. The lanes of a row walk over rows, keep their
+// columns' share of dw in registers, and a workgroup writes its share out at its
+// end; a second kernel adds the workgroups' shares in their order. Bound by
+// memory: 6 bytes (8 with dh) a 16-bit element.
 // ---------------------------------------------------------------------------
 template <int T, int LANES, int U, int THREADS, bool DH>
-__global__ __launch_bounds__(THREADS) void rmsnorm_grad_kernel(NormGradArgs a, int groups) {
+__global__ __launch_bounds__(THREADS) void rmsnorm_grad_kernel(NormGradArgs a) {
   using E = typename Elem<T>::type;
   __shared__ float part[2][16];
   const Columns<LANES, U> c(LANES == kBlockRow ? threadIdx.x : threadIdx.x % LANES, a.cols);
   const int group = LANES == kBlockRow ? blockIdx.x : blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t groups = LANES == kBlockRow ? gridDim.x : (int64_t)gridDim.x * (256 / LANES);
   const int64_t turns = (a.rows + groups - 1) / groups;      // the same for every group: barriers and lane sums in step
-  float w[U][8], dw[U][8], wlast, dwlast = 0.f;
+  float w[kSome<U>][8], dw[kSome<U>][8], wlast, dwlast = 0.f;
   load_weights(a.w, a.wtype, c, w, wlast);
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -208,12 +237,15 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_grad_kernel(NormGradArgs a, i
     for (int i = 0; i < 8; ++i) dw[u][i] = 0.f;
   for (int64_t k = 0; k < turns; ++k) {
     const int64_t row = k * groups + group;
-    const bool here = row < a.rows && group < groups;
+    const bool here = row < a.rows;
+    const int64_t from = here ? row : a.rows - 1;
     Row<T, U> y, x, r;
-    y.load(a.dy, row * a.lddy, c, here);
-    x.load(a.h, row * a.ldh, c, here);
-    if constexpr (DH) r.load(a.dh, row * a.lddh, c, here);
-    const float rstd = here ? a.rstd[row] : 0.f;
+    y.load(a.dy, from * a.lddy, c);
+    x.load(a.h, from * a.ldh, c);
+    if constexpr (DH) r.load(a.dh, from * a.lddh, c);
+    const float rstd = a.rstd[from];
+    y.clear(c, here);
+    x.clear(c, here);
     const float dylast = Elem<T>::value(y.last), xhlast = Elem<T>::value(x.last) * rstd;
     float dot = dylast * wlast * xhlast;
     dwlast = __builtin_fmaf(dylast, xhlast, dwlast);
@@ -248,28 +280,44 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_grad_kernel(NormGradArgs a, i
           const float dx = rstd * __builtin_fmaf(-(h[i] * rstd), mean, dy[i] * w[u][i]);
           d[i] = DH ? dx + d[i] : dx;
         }
-        store8<T>(out + c.col(u), d);
+        stream_store(out + c.col(u), round8<T>(d));
       }
     }
   }
-  if (group < groups) {
-    float* parts = a.parts + (int64_t)group * a.cols;
+  // the workgroup's share: of the groups in it, in their order
+  float* out = gridDim.x == 1 ? a.dw : a.parts + (int64_t)blockIdx.x * a.cols;
+  if constexpr (LANES == kBlockRow) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (c.has(u)) store8<FP8BQ_FP32>(parts + c.col(u), dw[u]);
-    if (c.last >= 0) parts[c.last] = dwlast;
+      if (c.has(u)) __builtin_memcpy(out + c.col(u), dw[u], sizeof(dw[u]));
+    if (c.last >= 0) out[c.last] = dwlast;
+  } else {
+    constexpr int kCols = LANES * 8;               // at most this many
+    __shared__ float share[256 / LANES][kCols];
+    float* mine = share[threadIdx.x / LANES];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c.has(u)) __builtin_memcpy(mine + c.col(u), dw[u], sizeof(dw[u]));
+    if (c.last >= 0) mine[c.last] = dwlast;
+    __syncthreads();
+    for (int col = threadIdx.x; col < a.cols; col += 256) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < 256 / LANES; ++g) v += share[g][col];
+      out[col] = v;
+    }
   }
 }
 
-// dw: 64 columns a workgroup, its 16 waves each adding every 16th group.
-__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* parts, int groups, int cols, float* dw) {
+// dw: 64 columns a workgroup, its 16 waves each adding every 16th row of sums.
+__global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* parts, int rows, int cols, float* dw) {
   __shared__ float sum[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = blockIdx.x * 64 + lane;
   float v = 0.f;
   if (col < cols) {
 #pragma unroll 8
-    for (int g = wave; g < groups; g += 16) v += parts[(int64_t)g * cols + col];
+    for (int r = wave; r < rows; r += 16) v += parts[(int64_t)r * cols + col];
   }
   sum[wave][lane] = v;
   __syncthreads();
@@ -288,9 +336,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* parts, in
 template <class F>
 void with_shape(int64_t cols, F&& f) {
   using std::integral_constant;
-  const int64_t units = cols < 8 ? 1 : cols / 8;
+  const int64_t units = cols / 8;
   auto threads = [&](int u) { return (int)((units + 64 * u - 1) / (64 * u) * 64); };
-  if (cols <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 1>{}, integral_constant<int, 256>{}, 256);
+  if (cols < 8) f(integral_constant<int, 16>{}, integral_constant<int, 0>{}, integral_constant<int, 256>{}, 256);
+  else if (cols <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 1>{}, integral_constant<int, 256>{}, 256);
   else if (cols <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{}, integral_constant<int, 256>{}, 256);
   else if (units <= 512) f(integral_constant<int, kBlockRow>{}, integral_constant<int, 1>{}, integral_constant<int, 512>{}, threads(1));
   else if (units <= 1024) f(integral_constant<int, kBlockRow>{}, integral_constant<int, 2>{}, integral_constant<int, 512>{}, threads(2));
@@ -304,26 +353,32 @@ hipError_t forward(const NormArgs& a, bool pow2, hipStream_t st) {
     const int64_t per_block = lanes == kBlockRow ? 1 : 256 / (lanes == kBlockRow ? 1 : lanes);
     const int64_t blocks = (a.rows + per_block - 1) / per_block;
     rmsnorm_kernel<T, decltype(lanes)::value, decltype(units)::value, decltype(bound)::value, RES>
-        <<<(unsigned)(blocks < 4096 ? blocks : 4096), threads, 0, st>>>(a, pow2);
+        <<<(unsigned)(blocks < (1 << 22) ? blocks : 1 << 22), threads, 0, st>>>(a, pow2);
   });
   return hipGetLastError();
 }
 
-int groups_of(int64_t rows, int64_t cols) {
-  const int most = cols <= 128 ? 4096 : cols <= 512 ? 1024 : 512;
-  return (int)(rows < most ? rows : most);
+// Workgroups of the gradient, of which each leaves a row of sums: enough to fill
+// the chip, few enough that their sums are a small part of the traffic. Us with
+// 256 / 512 / 1024 where a row takes a workgroup: 2048 x 16384 54.8 / 62.4 / 75.5,
+// 4096 x 7168 49.0 / 49.5 to 52.8 / 57.1, 16384 x 2048 83 / 55.5 / 49.7. At least
+// two rows each (333 x 2048 fp32: 7.4 us, 8.7 with one).
+int grad_blocks(int64_t rows, int64_t cols) {
+  int64_t most = cols > 8192 ? 256 : cols > 2048 ? 512 : 1024;
+  if (cols <= 128) rows = (rows + 15) / 16;
+  else if (cols <= 512) rows = (rows + 3) / 4;
+  most = most < (rows + 1) / 2 ? most : (rows + 1) / 2;
+  return (int)most;
 }
 
 template <int T, bool DH>
 hipError_t gradient(const NormGradArgs& a, hipStream_t st) {
-  const int groups = groups_of(a.rows, a.cols);
+  const int blocks = grad_blocks(a.rows, a.cols);
   with_shape(a.cols, [&](auto lanes, auto units, auto bound, int threads) {
-    const int per_block = lanes == kBlockRow ? 1 : 256 / (lanes == kBlockRow ? 1 : lanes);
-    rmsnorm_grad_kernel<T, decltype(lanes)::value, decltype(units)::value, decltype(bound)::value, DH>
-        <<<(groups + per_block - 1) / per_block, threads, 0, st>>>(a, groups);
+    rmsnorm_grad_kernel<T, decltype(lanes)::value, decltype(units)::value, decltype(bound)::value, DH><<<blocks, threads, 0, st>>>(a);
   });
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  rmsnorm_dw_kernel<<<(a.cols + 63) / 64, 1024, 0, st>>>(a.parts, groups, a.cols, a.dw);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || blocks == 1) return e;
+  rmsnorm_dw_kernel<<<(a.cols + 63) / 64, 1024, 0, st>>>(a.parts, blocks, a.cols, a.dw);
   return hipGetLastError();
 }
 
@@ -337,7 +392,7 @@ hipError_t launch_rmsnorm(const NormArgs& a, int xtype, bool pow2, hipStream_t s
   }
 }
 
-int64_t norm_grad_parts(int64_t rows, int64_t cols) { return groups_of(rows, cols); }
+int64_t norm_grad_parts(int64_t rows, int64_t cols) { return grad_blocks(rows, cols); }
 
 hipError_t launch_rmsnorm_grad(const NormGradArgs& a, int xtype, hipStream_t st) {
   switch (xtype) {

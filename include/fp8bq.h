@@ -636,9 +636,9 @@ int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, in
  * q, s      both NULL, or E4M3 [rows, cols] and scales in the layout and by the
  *           rule of fp8bq_quant_act_1x128 (ROWWISE) for the float32 values of y
  *           (not y's rounded ones); cols a multiple of 128. One of y and q is
- *           required. NaN gives the code 0x7F or 0xFF (NaN), an infinity makes its
- *           tile NaN (with power-of-two scales only itself); other tiles of the
- *           row follow from rstd, which such a row makes NaN or 0.
+ *           required. A row that holds a NaN reads back as NaN (its codes or its
+ *           scales are NaN); one that holds an infinity reads back as NaN there or
+ *           in that tile, and as 0 elsewhere (its rstd is 0).
  * rstd      NULL, or float [rows].
  * eps       finite, >= 0 (a row of zeros with eps = 0 is NaN). Sums of squares
  *           are float32: rows whose mean square passes 3e38 become 0.

@@ -41,6 +41,12 @@ def check_codes(q, s, y, pow2):
     assert (np.signbit(got) == np.signbit(y)).all()
 
 
+def read_back(q, s):
+    """Values of E4M3 codes with 1x128 scales."""
+    with np.errstate(invalid="ignore"):
+        return e4m3.decode(q.cpu().numpy()) * np.repeat(f64(s).T, 128, 1)
+
+
 def check_forward(x, r, w, eps, out, dtype, pow2=False):
     q, s, y, h, rstd = out
     vx, vr = f64(x), None if r is None else f64(r)
@@ -129,25 +135,26 @@ def test_rows_of_zeros_and_tiny_and_large_values():
         assert (q[1][f64(w) > 0] == 0x80).all()
         assert s[1, 4] == zero and (q[4, 128:256] & 0x7F == 0).all()
     out = fb.rmsnorm(x, w, 0.0, norm=True)
-    assert np.isnan(f64(out[2])[0]).all() and (out[0][0].cpu().numpy() & 0x7F == 0x7F).all()      # 0 / 0, as the formula says
+    assert np.isnan(f64(out[2])[0]).all() and np.isnan(read_back(out[0], out[1])[0]).all()         # 0 / 0, as the formula says
 
 
 @pytest.mark.parametrize("cols", [128, 512, 1152, 16384])
-def test_nan_and_infinity_stay_in_their_row(cols):
+@pytest.mark.parametrize("pow2", [False, True])
+def test_nan_and_infinity_stay_in_their_row(cols, pow2):
     x, w = matrix(8, 20, cols), weight(6, cols, "bfloat16")
-    clean = fb.rmsnorm(x, w, norm=True)
+    clean = fb.rmsnorm(x, w, norm=True, pow2=pow2)
     x = x.clone()
     x[3, 5] = float("nan")
     x[11, cols - 1] = float("inf")
-    q, s, y, _, rstd = fb.rmsnorm(x, w, norm=True)
+    q, s, y, _, rstd = fb.rmsnorm(x, w, norm=True, pow2=pow2)
     keep = [i for i in range(20) if i not in (3, 11)]
     assert np.array_equal(f64(y)[keep], f64(clean[2])[keep])
     assert np.array_equal(q.cpu().numpy()[keep], clean[0].cpu().numpy()[keep])
     assert np.array_equal(f64(s)[:, keep], f64(clean[1])[:, keep])
-    vy, vr = f64(y), f64(rstd)
-    assert np.isnan(vy[3]).all() and np.isnan(vr[3]) and (q[3].cpu().numpy() & 0x7F == 0x7F).all()
+    vy, vr, back = f64(y), f64(rstd), read_back(q, s)
+    assert np.isnan(vy[3]).all() and np.isnan(vr[3]) and np.isnan(back[3]).all()
     assert vr[11] == 0 and np.isnan(vy[11, -1]) and (vy[11, :-1] == 0).all()
-    assert q[11, -1].item() & 0x7F == 0x7F
+    assert np.isnan(back[11, -1]) and (back[11, :-128] == 0).all()
 
 
 def test_pointer_level_in_place_and_padded():
