@@ -212,3 +212,26 @@ def test_rows_past_32_bits(what):
         assert torch.equal(out[lo:lo + 4000].float(), (rows * part).sum(1))
         assert torch.equal(dw[lo:lo + 4000], (rows * dout[lo:lo + 4000, None].float()).sum(2))
         assert torch.equal(dy[pos[lo:lo + 4000].long()].float(), part * dout[lo:lo + 4000, None].float())
+
+
+def test_more_tokens_than_workgroups():
+    """More pieces of rows than one launch has workgroups for: dispatch, combine and its gradient of 17 million tokens,
+    whose whole numbers come through exactly."""
+    import torch
+    tokens, cols = 17_000_000, 16
+    log(f"rows of {tokens} tokens")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    idx = torch.randint(-1, 5, (tokens, 1), generator=gen, device="cuda", dtype=torch.int32)
+    _, off, src, pos = fb.moe_plan(idx, 5, 16)
+    x = torch.randint(-8, 9, (tokens, cols), generator=gen, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    rows, _ = fb.moe_dispatch(x, src, pos)
+    last = int(off[-1])
+    used = src[:last]
+    assert torch.equal(rows[:last], torch.where((used >= 0)[:, None], x[used.clamp(min=0).long()], torch.zeros((), dtype=x.dtype, device="cuda")))
+    w = torch.randint(1, 4, (tokens, 1), generator=gen, device="cuda").float()
+    mine = pos >= 0
+    assert torch.equal(fb.moe_combine(rows, pos, w), torch.where(mine, x * w, 0.0).to(x.dtype))
+    dy, dw = fb.moe_combine_grad(x, rows, pos, w, src)
+    assert torch.equal(dw, torch.where(mine, (x.float() ** 2).sum(1, keepdim=True), 0.0))
+    assert torch.equal(fb.moe_combine(dy, pos), torch.where(mine, x * w, 0.0).to(x.dtype))
+    assert (dy[:last][used < 0] == 0).all()

@@ -190,6 +190,24 @@ def test_rows_past_32_bits():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("rows,cols", [(68_000_000, 9), (17_500_000, 130), (4_300_000, 520)])
+def test_more_rows_than_workgroups(rows, cols):
+    """Rows by 16 lanes, by a wave and by a workgroup, more than one launch has workgroups for: the same as of a slice."""
+    import torch
+    log(f"norm of {rows} x {cols}")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    w = weight(14, cols, "float32")
+    _, _, y, _, rstd = fb.rmsnorm(x, w, quant=False, norm=True)
+    for lo in (0, rows // 2 - 77, rows - 300):
+        a = fb.rmsnorm(x[lo:lo + 300], w, quant=False, norm=True)
+        assert torch.equal(y[lo:lo + 300], a[2]) and torch.equal(rstd[lo:lo + 300], a[4])
+    dx, dw = fb.rmsnorm_grad(y, x, w, rstd)
+    for lo in (0, rows - 300):
+        assert torch.equal(dx[lo:lo + 300], fb.rmsnorm_grad(y[lo:lo + 300], x[lo:lo + 300], w, rstd[lo:lo + 300])[0])
+    assert torch.isfinite(dw).all()
+
+
 def check_grad(dy, h, w, rstd, dh, got, dtype):
     vy, vh, vw, vr = f64(dy), f64(h), f64(w), f64(rstd)[:, None]
     wx, ww = layer.rmsnorm_grad(vy, vh, vw, f64(rstd), None if dh is None else f64(dh))
