@@ -12,12 +12,13 @@
 // the same order. Sums are fp32. fp32 activations are split into three bf16 terms
 // whose sum is x exactly (24 = 8 + 8 + 8 significant bits), each with an MFMA of
 // its own. fp16 ones meet weights decoded to fp16 where the scales of all lanes
-// allow that exactly, which a model's weights always do; else they are split into
-// two bf16 terms (11 = 8 + 3 bits).
+// allow that exactly, as those of a model's weights do (all but those of tiles of
+// zeros); else they are split into two bf16 terms (11 = 8 + 3 bits).
 //
-// What bounds it: the weight's bytes, once enough loads are in flight. One row of
-// 18432 x 7168 (70 MB) takes 14.4 us, 15.8 with the weight out of the caches; the
-// same loads alone take 15. What it took (us, the same product): x loaded by the
+// What bounds it: the weight's bytes, once enough loads are in flight; for 9 to 16
+// rows also x, whose chunk takes 32 registers a lane where a weight tile's takes
+// 10, so that fewer are in flight. One row of 18432 x 7168 (70 MB) takes 14.4 us,
+// 15.8 with the weight out of the caches; the same loads alone take 15. What it took (us, the same product): x loaded by the
 // lanes that use it 20 (a load for every lane of the MFMA's 16 columns fills the
 // 64 bytes a cycle of the CU's vector cache), x held in registers over many
 // weight tiles 30 and x staged for a workgroup with a barrier a step 19 (both
@@ -142,6 +143,7 @@ struct Few {
   // Unit u (8 elements) of row r: step z of the MFMAs takes it to lane 16 h + r.
   static __device__ __forceinline__ int slot(int r, int z, int h) {
     const int at = (z * 4 + h) * kRows + r;
+    static_assert(kRows < 8 || kRows % 8 == 0, "the places of a unit's rows are whole groups of 8");
     return kRows >= 8 ? at ^ ((z & 3) + 4 * (h & 1)) : at;     // neighbouring units of a row to different banks
   }
   __device__ __forceinline__ void load_codes(Stage& t, int c) const {
@@ -338,11 +340,12 @@ void launch_grouped(const GemvArgs& p, hipStream_t st) {
   grouped_gemv_kernel<T, NT, WAVES><<<grid, 64 * WAVES, 0, st>>>(p);
 }
 // Rows in passes of 2 P, the fewest that hold them all up to 16. One weight tile
-// a wave; two for more than 8 rows, so that x is loaded half as often, unless n is
-// too small to fill the chip with pairs (us with one / two tiles, 16 rows of bf16:
-// 18432 x 7168 21.7 / 19.9, 7168 x 2048 5.9 / 5.1, 2048 x 7168 6.2 / 7.9; 8 rows
-// of 18432 x 7168 16.3 / 16.7). Four waves share K; two for 16 rows of fp32, whose
-// x takes 24 KB of LDS a wave (57.8 / 47.4 us with four / two).
+// a wave; two or three for more than 8 rows, so that x is loaded less often, as
+// long as that many fill the chip (us with one / two / three tiles, 16 rows of
+// bf16: 18432 x 7168 21.7 / 20.3 / 18.8, 7168 x 2048 5.9 / 4.9 / 5.7, 2048 x 7168
+// 6.2 / 7.9 with two; 8 rows of 18432 x 7168 16.3 / 16.7). Four waves share K; two
+// for 16 rows of fp32, whose x takes 24 KB of LDS a wave (57.8 / 47.4 us with
+// four / two).
 template <int T>
 hipError_t run(const GemvArgs& p, hipStream_t st) {
   constexpr int kWide = T == FP8BQ_FP32 ? 2 : 4;
@@ -350,6 +353,7 @@ hipError_t run(const GemvArgs& p, hipStream_t st) {
   else if (p.m <= 2) launch_dense<T, 1, 1, 4>(p, st);          // waves 58, but 30 against 25 where every expert has 8 rows
   else if (p.m <= 4) launch_dense<T, 2, 1, 4>(p, st);
   else if (p.m <= 8) launch_dense<T, 4, 1, 4>(p, st);
+  else if (p.n >= 48 * 256 && T != FP8BQ_FP32) launch_dense<T, 8, T == FP8BQ_FP32 ? 2 : 3, kWide>(p, st);
   else if (p.n >= 4096) launch_dense<T, 8, 2, kWide>(p, st);
   else launch_dense<T, 8, 1, kWide>(p, st);
   return hipGetLastError();

@@ -23,7 +23,8 @@ def check_product(out, vx, vw, k, xtype, otype):
 @pytest.mark.parametrize("xtype", DTYPES)
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 16, 32), (1, 17, 31), (1, 2048, 7168), (2, 33, 33), (3, 64, 255), (7, 100, 256),
                                    (15, 48, 257), (16, 64, 512), (17, 50, 700), (31, 129, 1057), (32, 32, 2048), (48, 16, 96),
-                                   (64, 80, 640), (65, 96, 1000), (130, 40, 300), (5, 18432, 128)])
+                                   (64, 80, 640), (65, 96, 1000), (130, 40, 300), (5, 18432, 128),
+                                   (12, 4100, 520), (20, 4097, 300), (12, 12301, 300), (16, 12288, 1030)])
 def test_product(m, n, k, xtype):
     log(f"gemv {m}x{n}x{k} {xtype}")
     w, ws, vw = operand(n + k, n, k)
@@ -35,7 +36,8 @@ def test_product(m, n, k, xtype):
 
 
 @pytest.mark.parametrize("xtype", DTYPES)
-@pytest.mark.parametrize("m,n,k", [(1, 64, 7168), (4, 40, 1057), (16, 100, 2048), (33, 70, 1024), (70, 33, 900)])
+@pytest.mark.parametrize("m,n,k", [(1, 64, 7168), (4, 40, 1057), (16, 100, 2048), (33, 70, 1024), (70, 33, 900), (10, 4099, 1057),
+                                   (11, 12290, 800)])
 def test_integers_are_exact(m, n, k, xtype):
     """Small whole numbers: every partial sum is a multiple of 1/2 below 2^23, so nothing rounds and every product counts."""
     import torch
