@@ -346,16 +346,20 @@ void launch_grouped(const GemvArgs& p, hipStream_t st) {
 // 6.2 / 7.9 with two; 8 rows of 18432 x 7168 16.3 / 16.7). Four waves share K; two
 // for 16 rows of fp32, whose x takes 24 KB of LDS a wave (57.8 / 47.4 us with
 // four / two).
+// Experts: two tiles and two waves (32 tokens to 32 of 256 experts, 2048 x 7168:
+// 56 to 60 us; four waves 58, but 30 against 25 where every expert of 2048 x 2048
+// has 8 rows).
 template <int T>
 hipError_t run(const GemvArgs& p, hipStream_t st) {
-  constexpr int kWide = T == FP8BQ_FP32 ? 2 : 4;
-  if (p.groups) launch_grouped<T, 2, 2>(p, st);    // 32 tokens to 32 of 256 experts, 2048 x 7168: 60 us; pairs of tiles with four
-  else if (p.m <= 2) launch_dense<T, 1, 1, 4>(p, st);          // waves 58, but 30 against 25 where every expert has 8 rows
+  constexpr bool kFp32 = T == FP8BQ_FP32;
+  constexpr int kWaves = kFp32 ? 2 : 4;
+  if (p.groups) launch_grouped<T, 2, 2>(p, st);
+  else if (p.m <= 2) launch_dense<T, 1, 1, 4>(p, st);
   else if (p.m <= 4) launch_dense<T, 2, 1, 4>(p, st);
   else if (p.m <= 8) launch_dense<T, 4, 1, 4>(p, st);
-  else if (p.n >= 48 * 256 && T != FP8BQ_FP32) launch_dense<T, 8, T == FP8BQ_FP32 ? 2 : 3, kWide>(p, st);
-  else if (p.n >= 4096) launch_dense<T, 8, 2, kWide>(p, st);
-  else launch_dense<T, 8, 1, kWide>(p, st);
+  else if (p.n < 4096) launch_dense<T, 8, 1, kWaves>(p, st);
+  else if (p.n < 48 * 256 || kFp32) launch_dense<T, 8, 2, kWaves>(p, st);
+  else launch_dense<T, 8, kFp32 ? 2 : 3, kWaves>(p, st);
   return hipGetLastError();
 }
 
