@@ -55,7 +55,7 @@ __device__ __forceinline__ V load_any(const void* p) {
 }
 // Results that are written whole, as they go by: marked as not worth keeping in
 // the caches (rows of 8192 tokens dispatched to 64 experts: 115 -> 102 us, 4096 x
-// 7168 normalised: 49 -> 40). Loads so marked were slower by a fifth wherever an
+// 7168 normalised: 49 -> 40). Loads so marked were slower by a fifth to a third wherever an
 // operand still was in a cache, and faster only far beyond their size.
 template <class V>
 __device__ __forceinline__ void stream_store(void* p, const V& v) {

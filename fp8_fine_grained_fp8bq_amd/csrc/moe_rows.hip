@@ -3,6 +3,8 @@
 // include/fp8bq.h. All of it is bound by memory, so each row is read and
 // written once: a wave takes a piece of a token's row and visits the token's
 // choices (`pos`) with it, instead of each dispatched row fetching its token.
+// 8192 tokens of 7168 columns, 8 of 64 experts each: codes out 102 us (5.6 TB/s),
+// 16-bit rows back 210, its gradient 412.
 #include "../../include/fp8bq.h"
 #include "elem.h"
 #include "lanes.h"
@@ -13,6 +15,7 @@ namespace {
 
 constexpr int kUnit = 8;                 // elements of a lane
 constexpr int kChoices = 4;              // choices whose loads are in flight together
+                                         // (8: fewer waves; 16384 rows of 2048: 20.7 us, 17.0 with 4)
 
 // Work is numbered in blocks of four waves; workgroups beyond a launch's limit
 // take several.

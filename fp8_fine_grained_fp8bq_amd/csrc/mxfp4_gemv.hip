@@ -18,11 +18,12 @@
 // What bounds it: the weight's bytes, once enough loads are in flight; for 9 to 16
 // rows also x, whose chunk takes 32 registers a lane where a weight tile's takes
 // 10, so that fewer are in flight. One row of 18432 x 7168 (70 MB) takes 14.4 us,
-// 15.8 with the weight out of the caches; the same loads alone take 15. What it took (us, the same product): x loaded by the
-// lanes that use it 20 (a load for every lane of the MFMA's 16 columns fills the
-// 64 bytes a cycle of the CU's vector cache), x held in registers over many
-// weight tiles 30 and x staged for a workgroup with a barrier a step 19 (both
-// wait for memory in step), branches around the loads 27 to 40.
+// 15.8 with the weight out of the caches; the same loads alone take 15. What it
+// took (us, the same product): x loaded by the lanes that use it 20 (a load for
+// every lane of the MFMA's 16 columns fills the 64 bytes a cycle of the CU's
+// vector cache), x held in registers over many weight tiles 30 and x staged for a
+// workgroup with a barrier a step 19 (both wait for memory in step), branches
+// around the loads 27 to 40.
 #include "../../include/fp8bq.h"
 #include "elem.h"
 #include "layer.h"

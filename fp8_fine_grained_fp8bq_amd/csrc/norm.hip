@@ -6,8 +6,8 @@
 // s = amax|y| / 448, q = E4M3(y / s). A row lives in the registers of its
 // lanes as fp32 from the load to the store, so the mean and the scales cost
 // no second read: 2 (4 with r) bytes read and 1 to 5 written per 16-bit element.
-// Bound by memory; the arithmetic (about 14 instructions an element) hides
-// under it.
+// Bound by memory: 16384 x 7168 with codes and rows takes 184 us (5.8 TB/s),
+// 4096 x 7168 with codes 37.5, its gradient 49.6.
 #include "../../include/fp8bq.h"
 #include "elem.h"
 #include "fp8_codec.h"
@@ -82,7 +82,7 @@ __device__ __forceinline__ void load_weights(const void* w, int wtype, const Col
 
 // A lane's elements of the row at p. Every lane loads, and what it has no column
 // for is set to zero after: loads under a lane's branch are waited for where the
-// branch ends, one after the other (4096 x 7168 back: 58 us, 70 to 84 then).
+// branch ends, one after the other (4096 x 7168 back: 49.6 us, 70 to 84 then).
 template <int T, int U>
 struct Row {
   Raw8<T> unit[kSome<U>];
