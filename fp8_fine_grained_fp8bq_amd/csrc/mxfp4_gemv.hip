@@ -330,37 +330,70 @@ __global__ __launch_bounds__(64 * WAVES, 2) void grouped_gemv_kernel(GemvArgs p)
   else few_rows<T, 8, NT, WAVES>(p, b, sb, n0, m0, m1, lds);
 }
 
-template <int T, int P, int NT, int WAVES>
+template <int T, int P, int NT>
 void launch_dense(const GemvArgs& p, hipStream_t st) {
   const dim3 grid((unsigned)((p.n + 16 * NT - 1) / (16 * NT)), (unsigned)((p.m + 2 * P - 1) / (2 * P)));
-  gemv_kernel<T, P, NT, WAVES><<<grid, 64 * WAVES, 0, st>>>(p);
+  gemv_kernel<T, P, NT, 4><<<grid, 256, 0, st>>>(p);
 }
+// Tiles a wave, from 3 rows on: x is loaded once for all tiles of a workgroup and
+// costs about as much as one of them, and workgroups run in rounds of 256, one a
+// CU; so the number with the least rounds * (tiles + 1). Us with one to five
+// tiles, weights out of the caches: 16 rows of bf16, k = 4096, n = 8192 10.5 / 8.3 /
+// 9.6 / 11.9 / 12.3, n = 20480 20.5 / 17.7 / 16.1 / 19.7 / 13.6, n = 24576 24.3 /
+// 18.6 / 16.9 / 20.3 / 21.7; 4 rows of 18432 x 7168 18.8 / 18.5 / 17.6 / 21.6 / 15.7.
+// One and two rows differ by 3% where five tiles do best (15.8 / 15.6) and take
+// one. fp32 with more than 8 rows has registers for three.
+template <int T, int P>
+void launch_tiled(const GemvArgs& p, hipStream_t st) {
+  constexpr int kMost = T == FP8BQ_FP32 && P == 8 ? 3 : 5;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int nt = 1; nt <= kMost; ++nt) {
+    const int64_t groups = (p.n + 16 * nt - 1) / (16 * nt) * ((p.m + 2 * P - 1) / (2 * P)), cost = (groups + 255) / 256 * (nt + 1);
+    if (cost < least) least = cost, best = nt;
+  }
+  if (best == 1) launch_dense<T, P, 1>(p, st);
+  else if (best == 2) launch_dense<T, P, 2>(p, st);
+  else if (best == 3) launch_dense<T, P, 3>(p, st);
+  else if constexpr (kMost == 5) {
+    if (best == 4) launch_dense<T, P, 4>(p, st);
+    else launch_dense<T, P, 5>(p, st);
+  }
+}
+
 template <int T, int NT, int WAVES>
 void launch_grouped(const GemvArgs& p, hipStream_t st) {
   const dim3 grid((unsigned)((p.n + 16 * NT - 1) / (16 * NT)), (unsigned)p.groups);
   grouped_gemv_kernel<T, NT, WAVES><<<grid, 64 * WAVES, 0, st>>>(p);
 }
-// Rows in passes of 2 P, the fewest that hold them all up to 16. One weight tile
-// a wave; two or three for more than 8 rows, so that x is loaded less often, as
-// long as that many fill the chip (us with one / two / three tiles, 16 rows of
-// bf16: 18432 x 7168 21.7 / 20.3 / 18.8, 7168 x 2048 5.9 / 4.9 / 5.7, 2048 x 7168
-// 6.2 / 7.9 with two; 8 rows of 18432 x 7168 16.3 / 16.7). Four waves share K; two
-// for 16 rows of fp32, whose x takes 24 KB of LDS a wave (57.8 / 47.4 us with
-// four / two).
-// Experts: two tiles and two waves (32 tokens to 32 of 256 experts, 2048 x 7168:
-// 56 to 60 us; four waves 58, but 30 against 25 where every expert of 2048 x 2048
-// has 8 rows).
+// Experts. Four waves share K where they all run at once (two workgroups a CU, one
+// of fp32), as few rows reach few experts: a token's 8 of 32 experts, 2048 x 7168,
+// 14.5 us, 18.9 with two waves. Else three tiles, for two waves where the weights
+// are wide (128 rows to 32 experts of 7168 x 2048 57 us, 64 with two tiles, 71 with four
+// waves) or x is fp32, for four where K gives each five chunks and there are
+// enough of them (32 tokens to 32 of 256 experts, 2048 x 7168: 54 us, 61 with two
+// waves; 16 rows to 16 experts at most 29, 23 with two tiles for two waves); and
+// two tiles for two waves (2048 x 3584: 27 us, 29 to 32 else).
+template <int T>
+void launch_experts(const GemvArgs& p, hipStream_t st) {
+  constexpr bool kFp32 = T == FP8BQ_FP32;
+  const int64_t tiles = (p.n + 15) / 16, reached = p.m < p.groups ? p.m : p.groups;
+  if ((tiles + 1) / 2 * reached <= (kFp32 ? 256 : 512)) launch_grouped<T, 2, 4>(p, st);
+  else if (kFp32 || p.n >= 4096) launch_grouped<T, 3, 2>(p, st);
+  else if constexpr (!kFp32) {
+    if (p.k >= 20 * 256 && (tiles + 2) / 3 * reached > 1024) launch_grouped<T, 3, 4>(p, st);
+    else launch_grouped<T, 2, 2>(p, st);
+  }
+}
+
+// Rows in passes of 2 P, the fewest that hold them all up to 16.
 template <int T>
 hipError_t run(const GemvArgs& p, hipStream_t st) {
-  constexpr bool kFp32 = T == FP8BQ_FP32;
-  constexpr int kWaves = kFp32 ? 2 : 4;
-  if (p.groups) launch_grouped<T, 2, 2>(p, st);
-  else if (p.m <= 2) launch_dense<T, 1, 1, 4>(p, st);
-  else if (p.m <= 4) launch_dense<T, 2, 1, 4>(p, st);
-  else if (p.m <= 8) launch_dense<T, 4, 1, 4>(p, st);
-  else if (p.n < 4096) launch_dense<T, 8, 1, kWaves>(p, st);
-  else if (p.n < 48 * 256 || kFp32) launch_dense<T, 8, 2, kWaves>(p, st);
-  else launch_dense<T, 8, kFp32 ? 2 : 3, kWaves>(p, st);
+  if (p.groups) launch_experts<T>(p, st);
+  else if (p.m <= 2) launch_dense<T, 1, 1>(p, st);
+  else if (p.m <= 4) launch_tiled<T, 2>(p, st);
+  else if (p.m <= 8) launch_tiled<T, 4>(p, st);
+  else launch_tiled<T, 8>(p, st);
   return hipGetLastError();
 }
 

@@ -618,7 +618,8 @@ int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, in
  * is the FP8 Linear's operand, tokens to their experts' rows and back, and the
  * products of generated tokens with 4-bit weights. Types are fp8bq_dtype values;
  * 16- and 32-bit matrices need no alignment beyond their element's, and sums are
- * float32 in a fixed order: the same result at every call.
+ * float32 in an order fixed by the arguments other than the data: the same
+ * result at every call.
  * ------------------------------------------------------------------------- */
 
 /*

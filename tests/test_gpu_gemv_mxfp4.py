@@ -24,7 +24,9 @@ def check_product(out, vx, vw, k, xtype, otype):
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 16, 32), (1, 17, 31), (1, 2048, 7168), (2, 33, 33), (3, 64, 255), (7, 100, 256),
                                    (15, 48, 257), (16, 64, 512), (17, 50, 700), (31, 129, 1057), (32, 32, 2048), (48, 16, 96),
                                    (64, 80, 640), (65, 96, 1000), (130, 40, 300), (5, 18432, 128),
-                                   (12, 4100, 520), (20, 4097, 300), (12, 12301, 300), (16, 12288, 1030)])
+                                   (12, 4100, 520), (20, 4097, 300), (12, 12301, 300), (16, 12288, 1030), (4, 8003, 300),
+                                   (3, 9001, 1100), (4, 13001, 300), (3, 17003, 1300), (8, 8003, 1100), (5, 9001, 300), (7, 13001, 1300),
+                                   (6, 17003, 300), (9, 8003, 300), (13, 9001, 1100), (12, 13001, 1300), (14, 17003, 1100), (33, 6001, 300)])
 def test_product(m, n, k, xtype):
     log(f"gemv {m}x{n}x{k} {xtype}")
     w, ws, vw = operand(n + k, n, k)
@@ -146,7 +148,8 @@ def experts(seed, groups, n, k):
 
 @pytest.mark.parametrize("xtype", DTYPES)
 @pytest.mark.parametrize("counts,n,k", [([1], 32, 64), ([0, 0, 1], 16, 257), ([3, 0, 17, 1], 100, 600), ([70, 1, 0, 33], 50, 1057),
-                                        ([0] * 20 + [2] * 12, 2048, 512), ([0, 0], 16, 32)])
+                                        ([0] * 20 + [2] * 12, 2048, 512), ([0, 0], 16, 32), ([17, 0, 3, 1, 40], 4100, 300),
+                                        ([5, 0, 1, 18, 0, 2, 2, 3], 2050, 5200), ([9, 0, 1, 2, 33, 0, 4, 6], 2050, 600)])
 def test_experts(counts, n, k, xtype):
     import torch
     log(f"grouped gemv {counts[:6]} {n}x{k} {xtype}")
@@ -170,6 +173,24 @@ def test_experts(counts, n, k, xtype):
             if lo < hi:
                 check_product(got[lo:hi], picked[lo:hi], vw[e], k, xtype, xtype)
         assert (got[off[-1]:] == 7).all()
+
+
+@pytest.mark.parametrize("xtype", ["bfloat16", "float16"])
+def test_many_experts_of_a_long_k(xtype):
+    """Each expert's weight is the first one's with its rows moved on."""
+    import torch
+    counts, n, k = [1, 0, 3, 18, 2, 5, 1, 0, 33, 4, 8, 9, 1, 1, 16], 4000, 5200
+    log(f"grouped gemv {n}x{k} {xtype}")
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    w, ws, vw = operand(40, n, k)
+    wide = torch.stack([w.roll(7 * e, 0) for e in range(len(counts))])
+    scales = torch.stack([ws.roll(7 * e, 1) for e in range(len(counts))])
+    x = matrix(15, int(off[-1]), k, xtype)
+    got = f64(fb.grouped_gemv_mxfp4(torch.from_numpy(off).cuda(), x, wide, scales))
+    for e in range(len(counts)):
+        lo, hi = off[e], off[e + 1]
+        if lo < hi:
+            check_product(got[lo:hi], f64(x)[lo:hi], np.roll(vw, 7 * e, 0), k, xtype, xtype)
 
 
 def test_offsets_out_of_range_are_clamped():
