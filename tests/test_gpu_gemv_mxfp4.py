@@ -25,8 +25,8 @@ def check_product(out, vx, vw, k, xtype, otype):
                                    (15, 48, 257), (16, 64, 512), (17, 50, 700), (31, 129, 1057), (32, 32, 2048), (48, 16, 96),
                                    (64, 80, 640), (65, 96, 1000), (130, 40, 300), (5, 18432, 128),
                                    (12, 4100, 520), (20, 4097, 300), (12, 12301, 300), (16, 12288, 1030), (4, 8003, 300),
-                                   (3, 9001, 1100), (4, 13001, 300), (3, 17003, 1300), (8, 8003, 1100), (5, 9001, 300), (7, 13001, 1300),
-                                   (6, 17003, 300), (9, 8003, 300), (13, 9001, 1100), (12, 13001, 1300), (14, 17003, 1100), (33, 6001, 300)])
+                                   (3, 9001, 300), (4, 13001, 300), (3, 17003, 1300), (8, 8003, 300), (5, 9001, 300), (7, 13001, 520),
+                                   (6, 17003, 300), (9, 8003, 300), (13, 9001, 520), (12, 13001, 300), (14, 17003, 300), (33, 6001, 300)])
 def test_product(m, n, k, xtype):
     log(f"gemv {m}x{n}x{k} {xtype}")
     w, ws, vw = operand(n + k, n, k)
@@ -149,7 +149,7 @@ def experts(seed, groups, n, k):
 @pytest.mark.parametrize("xtype", DTYPES)
 @pytest.mark.parametrize("counts,n,k", [([1], 32, 64), ([0, 0, 1], 16, 257), ([3, 0, 17, 1], 100, 600), ([70, 1, 0, 33], 50, 1057),
                                         ([0] * 20 + [2] * 12, 2048, 512), ([0, 0], 16, 32), ([17, 0, 3, 1, 40], 4100, 300),
-                                        ([5, 0, 1, 18, 0, 2, 2, 3], 2050, 5200), ([9, 0, 1, 2, 33, 0, 4, 6], 2050, 600)])
+                                        ([9, 0, 1, 2, 33, 0, 4, 6, 1, 2], 2050, 300)])
 def test_experts(counts, n, k, xtype):
     import torch
     log(f"grouped gemv {counts[:6]} {n}x{k} {xtype}")
