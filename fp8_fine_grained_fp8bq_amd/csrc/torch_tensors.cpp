@@ -1,8 +1,7 @@
 // The MXFP4 operators, the routing and the operators around a layer's Linears
-// on torch tensors: checks of what the C
-// entry points (include/fp8bq.h) cannot see, allocation of the outputs, and
-// the call, on the tensors' device and its current stream. A Python extension
-// module (_tensors.so) because these calls are short: an operator's kernels
+// on torch tensors: checks of what the C entry points (include/fp8bq.h) cannot
+// see, allocation of the outputs, and the call, on the tensors' device and its
+// current stream. A Python extension module (_tensors.so) because these calls are short: an operator's kernels
 // take a few microseconds for a token, and the same steps in Python took nine
 // per call, of which the launch is three. tensors.py documents the functions
 // and gives them their keyword arguments.

@@ -1,5 +1,5 @@
-"""The MXFP4 operators, the routing of tokens to experts and the operators around a layer's Linears on torch tensors. Reached as attributes of the package,
-which imports this module on their first use (the package itself does not need torch).
+"""The MXFP4 operators, the routing of tokens to experts and the operators around a layer's Linears on torch tensors.
+Reached as attributes of the package, which imports this module on their first use (the package itself does not need torch).
 
 The calls check their arguments (ValueError), allocate the outputs and call the C entry points (Fp8bqError for their
 statuses); all of that is in the extension module _tensors (csrc/torch_tensors.cpp). They run on the tensors' device,
