@@ -191,12 +191,13 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
           encode(y, std::true_type{});
         } else {
           // rstd is a factor of the whole tile: it goes into the scale, and the codes come from h w, off by the roundings
-          // of that product, of the tile's amax / 448 and of the quotient only. Where h w may have underflowed, from y.
+          // of that product, of the tile's amax / 448 and of the quotient only. Where h w may have underflowed, or has
+          // overflowed, from y.
           float hw[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) hw[i] = v[u][i] * w[u][i];
           t = tile_scale(amax(hw), false);
-          if (t.s >= kFastScaleMin) {
+          if (t.s >= kFastScaleMin && t.s < INFINITY) {
             encode(hw, std::false_type{});
             t.s *= rstd;
           } else {

@@ -296,3 +296,31 @@ def test_gradient_is_the_same_at_every_call():
     for _ in range(3):
         b = fb.rmsnorm_grad(dy, h, w, rstd)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def check_read_back(out, wy):
+    """Values within half a step of E4M3 of the float64 y, and half of its smallest step (2^-10 s), 1% being for the other
+    roundings; 2^-149 for y's own where it is subnormal, and what 448 s leaves of it where the scale is rounded off."""
+    back = read_back(out[0], out[1])
+    assert np.isfinite(back).all()
+    s = np.repeat(f64(out[1]).T, 128, 1)
+    check("values", back, wy, 1.01 * (2.0 ** -4 * np.abs(wy) + 2.0 ** -10 * s) + 2.0 ** -149 + np.maximum(np.abs(wy) - 448 * s, 0))
+
+
+@pytest.mark.parametrize("cols", [128, 512, 1152, 16512])
+@pytest.mark.parametrize("residual", [False, True])
+def test_weights_whose_product_with_a_row_overflows(cols, residual):
+    """h * weight beyond float32's range where y = h * rstd * weight is not."""
+    import torch
+    x = torch.full((3, cols), 100.0, device="cuda")
+    x[1, ::2], x[2, 5] = -37.5, 1e4
+    w = torch.ones(cols, device="cuda")
+    w[: cols // 2] = 1e37
+    w[5], w[7] = 1.0, 1e30
+    r = x * 3 if residual else None
+    for pow2 in (False, True):
+        out = fb.rmsnorm(x, w, 1e-6, residual=r, norm=True, pow2=pow2)
+        wy = layer.rmsnorm(f64(x), None if r is None else f64(r), f64(w), 1e-6)[2]
+        check("y", f64(out[2]), wy, rounded(wy, Y * np.abs(wy), "float32"))
+        check_codes(out[0], out[1], wy, pow2)
+        check_read_back(out, wy)
