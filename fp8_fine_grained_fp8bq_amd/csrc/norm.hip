@@ -202,7 +202,11 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
             t.s *= rstd;
           } else {
             t = tile_scale(amax(y), false);
-            encode(y, std::false_type{});
+            const float most = kFmax * t.s;      // a subnormal scale may be rounded off by a third: codes end at 448
+            float ends[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ends[i] = fabsf(y[i]) > most ? __builtin_copysignf(most, y[i]) : y[i];
+            encode(ends, std::false_type{});
           }
         }
       }

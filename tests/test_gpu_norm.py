@@ -324,3 +324,13 @@ def test_weights_whose_product_with_a_row_overflows(cols, residual):
         check("y", f64(out[2]), wy, rounded(wy, Y * np.abs(wy), "float32"))
         check_codes(out[0], out[1], wy, pow2)
         check_read_back(out, wy)
+
+
+@pytest.mark.parametrize("size", [1e-40, 1e-41, 3e-42, 1e-42, 3e-43, 1e-43])
+def test_scales_of_a_few_steps_of_the_smallest_number(size):
+    """amax / 448 rounds to a scale up to a third too small: codes end at 448 then."""
+    x, w = matrix(24, 40, 640, "float32"), weight(16, 640, "float32") * size
+    out = fb.rmsnorm(x, w, 0.0, norm=True)
+    wy = layer.rmsnorm(f64(x), None, f64(w), 0.0)[2]
+    check("scales", f64(out[1]).T, np.abs(wy).reshape(40, 5, 128).max(2) / 448, 2.0 ** -149)
+    check_read_back(out, wy)
