@@ -104,6 +104,8 @@ struct Row {
   }
 };
 
+constexpr float kMinNormal = 0x1p-126f;
+
 // The scale of a tile whose largest magnitude is amax (as fp8_codec.h has it
 // for bf16 magnitudes): s = fl32(amax / 448), or the power of two.
 __device__ __forceinline__ TileScale tile_scale(float amax, bool pow2) {
@@ -191,13 +193,13 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_kernel(NormArgs a, bool pow2)
           encode(y, std::true_type{});
         } else {
           // rstd is a factor of the whole tile: it goes into the scale, and the codes come from h w, off by the roundings
-          // of that product, of the tile's amax / 448 and of the quotient only. Where h w may have underflowed, or has
-          // overflowed, from y.
+          // of that product, of the tile's amax / 448 and of the quotient only. They come from y where h w may have
+          // underflowed or has overflowed, and where the scale is subnormal, with which they go as it is rounded.
           float hw[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) hw[i] = v[u][i] * w[u][i];
           t = tile_scale(amax(hw), false);
-          if (t.s >= kFastScaleMin && t.s < INFINITY) {
+          if (t.s >= kFastScaleMin && t.s < INFINITY && t.s * rstd >= kMinNormal) {
             encode(hw, std::false_type{});
             t.s *= rstd;
           } else {

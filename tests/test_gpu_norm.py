@@ -334,3 +334,11 @@ def test_scales_of_a_few_steps_of_the_smallest_number(size):
     wy = layer.rmsnorm(f64(x), None, f64(w), 0.0)[2]
     check("scales", f64(out[1]).T, np.abs(wy).reshape(40, 5, 128).max(2) / 448, 2.0 ** -149)
     check_read_back(out, wy)
+
+
+@pytest.mark.parametrize("size", [1e-35, 1e-38, 1e-41])
+def test_large_rows_with_tiny_weights(size):
+    """h * weight is normal, the scale of y is not."""
+    x, w = matrix(23, 20, 640, "float32") * 1e15, weight(15, 640, "float32") * size
+    out = fb.rmsnorm(x, w, 0.0, norm=True)
+    check_read_back(out, layer.rmsnorm(f64(x), None, f64(w), 0.0)[2])
