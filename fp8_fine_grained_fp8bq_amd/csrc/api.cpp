@@ -219,10 +219,11 @@ int fp8bq_quant_w_128x128(const void* w, int64_t n, int64_t k, int64_t ldw, void
 
 namespace {
 
+// none: a product of no rows, whose a, sa and out may be null.
 int check_gemm_common(const char* who, int64_t m, int64_t n, int64_t k, const void* a, int64_t lda,
                       const float* sa, const void* b, int64_t ldb, const float* sb, const void* out,
-                      int64_t ldo, int out_elem_bytes) {
-  if (!a || !b || !sa || !sb || !out) return fail(FP8BQ_E_INVAL, "%s: null pointer", who);
+                      int64_t ldo, int out_elem_bytes, bool none = false) {
+  if (!b || !sb || (!none && (!a || !sa || !out))) return fail(FP8BQ_E_INVAL, "%s: null pointer", who);
   if (m <= 0 || n <= 0 || k <= 0) return fail(FP8BQ_E_INVAL, "%s: m, n, k must be positive", who);
   if (lda < k || ldb < k) return fail(FP8BQ_E_INVAL, "%s: lda and ldb must be >= k", who);
   if (ldo < n) return fail(FP8BQ_E_INVAL, "%s: ldo must be >= n", who);
@@ -304,7 +305,7 @@ int fp8bq_grouped_gemm(int32_t groups, const int64_t* row_off, int64_t n, int64_
   }
   const int64_t m = row_off[groups];
   if (m / 128 >= ((int64_t)1 << 30)) return fail(FP8BQ_E_SHAPE, "grouped_gemm: too many rows");
-  if (int st = check_gemm_common("grouped_gemm", m > 0 ? m : 1, n, k, a, lda, sa, b, ldb, sb, out, ldo, 2))
+  if (int st = check_gemm_common("grouped_gemm", m > 0 ? m : 1, n, k, a, lda, sa, b, ldb, sb, out, ldo, 2, m == 0))
     return st;
   if (ldsa < m) return fail(FP8BQ_E_INVAL, "grouped_gemm: ldsa must be >= m");
   if (ldsb < k / 128) return fail(FP8BQ_E_INVAL, "grouped_gemm: ldsb must be >= k / 128");
@@ -340,7 +341,7 @@ static int check_decode(const char* who, int32_t groups, const int64_t* row_off,
   if (flags != 0) return fail(FP8BQ_E_INVAL, "%s: flags must be 0, got %d", who, flags);
   if (int st = check_decode_offsets(who, groups, row_off)) return st;
   const int64_t m = row_off[groups];
-  if (int st = check_gemm_common(who, m > 0 ? m : 1, n, k, a, lda, sa, b, ldb, sb, out, ldo, 2)) return st;
+  if (int st = check_gemm_common(who, m > 0 ? m : 1, n, k, a, lda, sa, b, ldb, sb, out, ldo, 2, m == 0)) return st;
   if (product_at_least(groups, n / 64, (int64_t)1 << 31)) return fail(FP8BQ_E_SHAPE, "%s: too many column slices", who);
   if (ldsa < m) return fail(FP8BQ_E_INVAL, "%s: ldsa must be >= m", who);
   if (ldsb < k / 128) return fail(FP8BQ_E_INVAL, "%s: ldsb must be >= k / 128", who);

@@ -33,9 +33,9 @@ int check_rows(const char* who, const char* name, const void* p, int64_t rows, i
   return FP8BQ_OK;
 }
 
-// What the three routing operators share.
-int check_plan(const char* who, int64_t tokens, int64_t rows, int64_t cols, int64_t topk, const int32_t* pos) {
-  if (tokens <= 0 || rows <= 0 || cols <= 0 || topk <= 0) return entry_fail(FP8BQ_E_INVAL, "%s: sizes must be positive", who);
+// What the three routing operators share. `none`: there may be no rows.
+int check_plan(const char* who, int64_t tokens, int64_t rows, int64_t cols, int64_t topk, const int32_t* pos, bool none = false) {
+  if (tokens <= 0 || rows < 0 || (rows == 0 && !none) || cols <= 0 || topk <= 0) return entry_fail(FP8BQ_E_INVAL, "%s: sizes must be positive", who);
   if (!pos) return entry_fail(FP8BQ_E_INVAL, "%s: null pos", who);
   if (!aligned(pos, 4)) return entry_fail(FP8BQ_E_ALIGN, "%s: pos must be 4-byte aligned", who);
   if (tokens >= kMaxRouted || topk >= kMaxRouted || tokens * topk >= kMaxRouted || rows >= kMaxRouted || cols >= kMaxSide)
@@ -169,8 +169,9 @@ int fp8bq_moe_combine(const void* y, int type, int64_t rows, int64_t cols, int64
                       void* stream) {
   const char* who = "moe_combine";
   if (bad_dtype(type)) return entry_fail(FP8BQ_E_INVAL, "%s: type must be BF16, FP16 or FP32, got %d", who, type);
-  if (int e = check_plan(who, tokens, rows, cols, topk, pos)) return e;
-  if (int e = check_rows(who, "y", y, rows, cols, ldy, elem_bytes(type))) return e;
+  if (int e = check_plan(who, tokens, rows, cols, topk, pos, !y)) return e;
+  if (rows)
+    if (int e = check_rows(who, "y", y, rows, cols, ldy, elem_bytes(type))) return e;
   if (weight)
     if (int e = check_gate(who, weight, tokens, topk, ldw)) return e;
   if (base)
@@ -186,12 +187,14 @@ int fp8bq_moe_combine_grad(const void* dout, int type, int64_t tokens, int64_t c
                            const int32_t* src, void* dy, int64_t lddy, float* dweight, void* stream) {
   const char* who = "moe_combine_grad";
   if (bad_dtype(type)) return entry_fail(FP8BQ_E_INVAL, "%s: type must be BF16, FP16 or FP32, got %d", who, type);
-  if (int e = check_plan(who, tokens, rows, cols, topk, pos)) return e;
-  if (!weight || !src || !dweight) return entry_fail(FP8BQ_E_INVAL, "%s: null pointer", who);
+  if (int e = check_plan(who, tokens, rows, cols, topk, pos, !y)) return e;
+  if (!weight || (rows && !src) || !dweight) return entry_fail(FP8BQ_E_INVAL, "%s: null pointer", who);
   if (int e = check_gate(who, weight, tokens, topk, ldw)) return e;
   if (int e = check_rows(who, "dout", dout, tokens, cols, lddout, elem_bytes(type))) return e;
-  if (int e = check_rows(who, "y", y, rows, cols, ldy, elem_bytes(type))) return e;
-  if (int e = check_rows(who, "dy", dy, rows, cols, lddy, elem_bytes(type))) return e;
+  if (rows) {
+    if (int e = check_rows(who, "y", y, rows, cols, ldy, elem_bytes(type))) return e;
+    if (int e = check_rows(who, "dy", dy, rows, cols, lddy, elem_bytes(type))) return e;
+  }
   if (!aligned(src, 4) || !aligned(dweight, 4)) return entry_fail(FP8BQ_E_ALIGN, "%s: src and dweight must be 4-byte aligned", who);
   if (int e = entry_device()) return e;
   const MoeCombineGradArgs a{dout, tokens, cols, lddout, y, rows, ldy, pos, (int)topk, weight, ldw, src, dy, lddy, dweight};

@@ -512,9 +512,16 @@ PyObject* moe_dispatch(PyObject* const* arg) {
   return tuple(out, so);
 }
 
+// The experts' rows, which may be none.
+const Tensor& rows_of_experts(PyObject* o) {
+  const Tensor& y = tensor(o, "y");
+  if (y.dim() == 2 && y.size(0) == 0 && y.size(1) > 0) return y;
+  return matrix(y, "y");
+}
+
 // (y, pos, weight or None, base or None, out or None)
 PyObject* moe_combine(PyObject* const* arg) {
-  const Tensor& y = matrix(tensor(arg[0], "y"), "y");
+  const Tensor& y = rows_of_experts(arg[0]);
   const at::ScalarType type = y.scalar_type();
   const int code = dtype_code(type, "y");
   const Tensor& pos = choices(arg[1]);
@@ -525,7 +532,7 @@ PyObject* moe_combine(PyObject* const* arg) {
   const On on(y, pos, w, base, out);
   if (!out) out = on.empty({tokens, cols}, type);
   check("fp8bq_moe_combine",
-        fp8bq_moe_combine(y.data_ptr(), code, rows, cols, ld(y), pos.data_ptr<int32_t>(), tokens, topk,
+        fp8bq_moe_combine(rows ? y.data_ptr() : nullptr, code, rows, cols, ld(y), pos.data_ptr<int32_t>(), tokens, topk,
                           static_cast<const float*>(pointer(w)), ld(w), pointer(base), ld(base), out->data_ptr(), ld(out),
                           on.stream));
   return wrap(out);
@@ -533,7 +540,7 @@ PyObject* moe_combine(PyObject* const* arg) {
 
 // (dout, y, pos, weight, src, out or None)
 PyObject* moe_combine_grad(PyObject* const* arg) {
-  const Tensor& y = matrix(tensor(arg[1], "y"), "y");
+  const Tensor& y = rows_of_experts(arg[1]);
   const at::ScalarType type = y.scalar_type();
   const int code = dtype_code(type, "y");
   const Tensor& pos = choices(arg[2]);
@@ -546,7 +553,7 @@ PyObject* moe_combine_grad(PyObject* const* arg) {
   if (!dy) dy = on.empty({rows, cols}, type);
   Tensor dw = on.empty({tokens, topk}, at::kFloat);
   check("fp8bq_moe_combine_grad",
-        fp8bq_moe_combine_grad(dout.data_ptr(), code, tokens, cols, ld(dout), y.data_ptr(), rows, ld(y), pos.data_ptr<int32_t>(),
+        fp8bq_moe_combine_grad(dout.data_ptr(), code, tokens, cols, ld(dout), rows ? y.data_ptr() : nullptr, rows, ld(y), pos.data_ptr<int32_t>(),
                                topk, w.data_ptr<float>(), ld(w), src.data_ptr<int32_t>(), dy->data_ptr(), ld(dy),
                                dw.data_ptr<float>(), on.stream));
   return tuple(dy, dw);

@@ -104,7 +104,8 @@ def moe_dispatch(x, src, pos, s=None, out=None, s_out=None):
 
 def moe_combine(y, pos, weight=None, base=None, out=None):
     """Rows y [rows, cols] back to their tokens: base[t] + the sum of weight[t, j] * y[pos[t, j]] over the choices that
-    have a row, in y's type [tokens, cols]. weight float32 [tokens, topk] (None: ones); base in y's type (None: zeros)."""
+    have a row, in y's type [tokens, cols]. weight float32 [tokens, topk] (None: ones); base in y's type (None: zeros).
+    y may have no rows, as where every choice is another GPU's."""
     return _tensors.moe_combine(y, pos, weight, base, out)
 
 

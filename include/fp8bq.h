@@ -300,7 +300,8 @@ int fp8bq_gemm_quant(int op, int64_t m, int64_t n, int64_t k,
  * row_off  HOST array of G + 1 int64: expert e owns rows [row_off[e],
  *          row_off[e+1]) of a and out; row_off[0] == 0, non-decreasing, every
  *          entry a multiple of 128 (pad each expert's rows, e.g. with zeros).
- *          m = row_off[G].
+ *          m = row_off[G]; with m = 0 nothing is done, and a, sa and out may be
+ *          NULL.
  * a, sa    E4M3 [m, k] with chunk-major row scales (as fp8bq_gemm), ldsa >= m.
  * b        G weights of [n, k] each, row stride ldb, expert e's at b + e*n*ldb.
  * sb       G block grids [n/128][k/128], row stride ldsb, expert e's at
@@ -698,7 +699,8 @@ int fp8bq_moe_dispatch(const void* x, int elem, int64_t tokens, int64_t cols, in
  *   out[t] = base[t] + sum_j weight[t][j] * y[pos[t][j]],
  * choices in their order, those whose pos lies outside [0, rows) left out (their
  * weight is not looked at; a token without any gets base[t], or zeros).
- * y        [rows, cols] of type, ldy >= cols: the experts' outputs.
+ * y        [rows, cols] of type, ldy >= cols: the experts' outputs. NULL with
+ *          rows = 0 where no expert has one.
  * weight   float [tokens, topk], ldw >= topk, or NULL (ones).
  * base     [tokens, cols] of type (a residual, a shared expert's output), ldb >=
  *          cols, or NULL. Its gradient is the output's.
@@ -714,7 +716,8 @@ int fp8bq_moe_combine(const void* y, int type, int64_t rows, int64_t cols, int64
  * token, rows marked FP8BQ_ROW_UNUSED left as they were) and
  * dweight[t][j] = dout[t] . y[pos[t][j]] (0 for a choice that was left out).
  * dout [tokens, cols], y and dy [rows, cols] of type; dweight float
- * [tokens, topk], contiguous; src, pos of one plan. dy must not be y.
+ * [tokens, topk], contiguous; src, pos of one plan. dy must not be y. With y
+ * NULL and rows = 0 src and dy may be NULL too.
  * Errors as fp8bq_moe_dispatch.
  */
 int fp8bq_moe_combine_grad(const void* dout, int type, int64_t tokens, int64_t cols, int64_t lddout, const void* y,

@@ -242,3 +242,39 @@ def test_tensor_layer_refusals():
 def test_message_of_a_refusal():
     with pytest.raises(fb.Fp8bqError, match="E_INVAL.*no output"):
         fb.fp8bq_rmsnorm(A16, 0, 4, 64, 64, None, 0, A16, 0, 1e-6, None, 0, None, 0, None, 0, None, 0, None)
+
+
+def test_no_rows_reach_the_device_check(L):
+    """No expert here got a token: rows 0 with null pointers to the rows, which torch gives empty tensors."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is visible; valid arguments would launch")
+    expect(L, fb.E_DEVICE, "fp8bq_moe_combine", COMB, a0=None, a2=0)
+    expect(L, fb.E_DEVICE, "fp8bq_moe_combine", COMB, a0=None, a2=0, a4=0, a8=None, a9=0, a10=None, a11=0)
+    expect(L, fb.E_DEVICE, "fp8bq_moe_combine_grad", COMBG, a5=None, a6=0, a12=None, a13=None)
+    expect(L, fb.E_DEVICE, "fp8bq_moe_combine_grad", COMBG, a5=None, a6=0, a7=0, a12=None, a13=None, a14=0)
+    expect(L, fb.E_INVAL, "fp8bq_moe_combine", COMB, a0=None, a2=-1)
+    expect(L, fb.E_INVAL, "fp8bq_moe_combine", COMB, a0=None, a2=0, a3=0)
+    expect(L, fb.E_INVAL, "fp8bq_moe_combine", COMB, a0=None, a2=0, a12=None)
+    each(L, fb.E_INVAL, "fp8bq_moe_combine_grad", [None], (0, 8, 10, 15))
+    off = (ctypes.c_int64 * 3)(0, 0, 0)
+    product = [2, off, 256, 384, None, 384, None, 1, A16, 384, O4, 3, None, 256]
+    for fn, rest in (("fp8bq_grouped_gemm", [0, None]), ("fp8bq_grouped_gemm_decode", [0, None]),
+                     ("fp8bq_grouped_gemm_decode_ws", [None, 0, 0, None]), ("fp8bq_grouped_gemm_decode_noalloc", [0, None])):
+        expect(L, fb.E_DEVICE, fn, product + rest)
+        each_of = lambda values, i: [expect(L, fb.E_INVAL, fn, product + rest, **{f"a{i}": v}) for v in values]  # noqa: E731
+        each_of([None], 8), each_of([None], 10), each_of([383], 5), each_of([383], 9), each_of([255], 13)
+        expect(L, fb.E_INVAL, fn, product + rest, a1=(ctypes.c_int64 * 3)(0, 0, 128))
+
+
+def test_no_rows_in_the_tensor_layer():
+    """Empty matrices of rows are no refusal of their own."""
+    import torch
+    x, pos, gate = torch.zeros((4, 256)), torch.full((4, 2), -1, dtype=torch.int32), torch.zeros((4, 2))
+    y, src = torch.zeros((0, 256)), torch.zeros(0, dtype=torch.int32)
+    for f in (lambda: fb.moe_combine(y, pos, gate, base=x), lambda: fb.moe_combine_grad(x, y, pos, gate, src)):
+        with pytest.raises(ValueError, match="on the GPU"):
+            f()
+    for f in (lambda: fb.moe_combine(y[:, :0], pos, gate), lambda: fb.moe_combine_grad(x, y, pos, gate, torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="shape|columns|must be"):
+            f()

@@ -222,3 +222,35 @@ def test_balance_of_the_same_plan():
     rows, _ = fb.moe_dispatch(ones, src, pos)
     used = moe.plan(idx.cpu().numpy(), 12, 4, src.numel())[2]
     assert np.array_equal((f64(rows)[used != -2] == 1).all(1), used[used != -2] >= 0)
+
+
+@pytest.mark.parametrize("tokens,topk", [(1, 1), (40, 3)])
+def test_layer_without_rows(tokens, topk):
+    """Every choice is another GPU's: the experts have no rows, and the layer returns its residual stream."""
+    import torch
+    cols, experts = 384, 5
+    log(f"layer of {tokens} tokens without rows")
+    x, r, dout = matrix(130, tokens, cols), matrix(131, tokens, cols), matrix(132, tokens, cols)
+    w = matrix(133, 1, cols, "float32", 0.2)[0].contiguous() + 1
+    wq, ws, _ = weights_fp8(134, experts, cols, cols)
+    idx = torch.full((tokens, topk), -1, dtype=torch.int32, device="cuda")
+    gate = torch.ones((tokens, topk), device="cuda")
+    q, s, y, h, rstd = fb.rmsnorm(x, w, residual=r, norm=True)
+    counts, off, src, pos = fb.moe_plan(idx, experts, pad=128)
+    rows = int(off[-1])
+    assert rows == 0 and (counts == 0).all()
+    qd, sd = fb.moe_dispatch(q, src, pos, s=s)
+    for product in (fb.grouped_gemm, fb.grouped_gemm_decode):
+        z = product(off.tolist(), qd[:rows], sd[:, :rows].contiguous(), wq, ws)
+        assert z.shape == (0, cols)
+    z = fb.grouped_gemm_decode(off.tolist(), qd[:rows], sd[:, :rows].contiguous(), wq, ws, split=False)
+    assert torch.equal(fb.moe_combine(z, pos, gate, base=h), h)
+    assert (fb.moe_combine(z, pos, gate) == 0).all()
+    dz, dgate = fb.moe_combine_grad(dout, z, pos, gate, src[:rows])
+    assert dz.shape == (0, cols) and dgate.shape == (tokens, topk) and (dgate == 0).all()
+    dy = fb.moe_combine(dz, pos, base=y)
+    assert torch.equal(dy, y)
+    dx, dw = fb.rmsnorm_grad(dy, h, w, rstd, dh=dout)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    out = torch.full((tokens, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(fb.moe_combine(z, pos, out=out), torch.zeros_like(out))
