@@ -635,12 +635,17 @@ int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, in
  *           or x itself (with the same ld).
  * weight    [cols] of wtype.
  * y         NULL, or [rows, cols] of xtype: y rounded once.
- * q, s      both NULL, or E4M3 [rows, cols] and scales in the layout and by the
- *           rule of fp8bq_quant_act_1x128 (ROWWISE) for the float32 values of y
- *           (not y's rounded ones); cols a multiple of 128. One of y and q is
- *           required. A row that holds a NaN reads back as NaN (its codes or its
- *           scales are NaN); one that holds an infinity reads back as NaN there or
- *           in that tile, and as 0 elsewhere (its rstd is 0).
+ * q, s      both NULL, or E4M3 [rows, cols] and scales of 1x128 tiles in the
+ *           layout of fp8bq_quant_act_1x128 (ROWWISE); cols a multiple of 128.
+ *           One of y and q is required. rstd being a factor of the whole tile,
+ *           the codes are those of g = h * weight (each step in float32):
+ *             t = amax|g| / 448;  q = E4M3(g / t);  s = t * rstd.
+ *           They are those of y's float32 values, s = amax|y| / 448 and
+ *           q = E4M3(y / s), with FP8BQ_SCALE_POW2 (s = 2^k as there), and in
+ *           tiles where t is below 2^-100 or infinite or s below 2^-126. E4M3
+ *           ends at 448. A row that holds a NaN reads back as NaN (its codes or
+ *           its scales are NaN); one that holds an infinity reads back as NaN
+ *           there or in that tile, and as 0 elsewhere (its rstd is 0).
  * rstd      NULL, or float [rows].
  * eps       finite, >= 0 (a row of zeros with eps = 0 is NaN). Sums of squares
  *           are float32: rows whose mean square passes 3e38 become 0.

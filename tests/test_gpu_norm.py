@@ -342,3 +342,33 @@ def test_large_rows_with_tiny_weights(size):
     x, w = matrix(23, 20, 640, "float32") * 1e15, weight(15, 640, "float32") * size
     out = fb.rmsnorm(x, w, 0.0, norm=True)
     check_read_back(out, layer.rmsnorm(f64(x), None, f64(w), 0.0)[2])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("cols", [128, 512, 1152, 7168])
+def test_codes_bit_for_bit(cols, residual, dtype):
+    """Given rstd, every step up to the codes and scales is one float32 operation, which numpy does alike."""
+    rows = 40
+    x, w = matrix(25, rows, cols, dtype), weight(17, cols, dtype)
+    x[5, :128] *= 2.0 ** -12                                           # tiles whose scale of h * weight is below 2^-100, from y
+    w[:128] *= 1e-28 if dtype == "float32" else 1
+    r = matrix(26, rows, cols, dtype, 2.0) if residual else None
+    f32 = lambda t: f64(t).astype(np.float32)  # noqa: E731
+    tiles = lambda a: a.reshape(rows, -1, 128)  # noqa: E731
+    v = f32(x) + f32(r) if residual else f32(x)
+    for pow2 in (False, True):
+        q, s, _, _, rstd = fb.rmsnorm(x, w, residual=r, pow2=pow2)
+        hw, y = tiles(v * f32(w)), tiles(v * f32(rstd)[:, None] * f32(w))
+        amax = lambda a: np.abs(a).max(2, keepdims=True)  # noqa: E731
+        if pow2:
+            want_s = layer.scale(amax(y).astype(np.float64), True).astype(np.float32)
+            z = y / want_s
+        else:
+            of_hw, of_y = amax(hw) / np.float32(448), amax(y) / np.float32(448)
+            from_hw = of_hw >= np.float32(2.0 ** -100)
+            want_s = np.where(from_hw, of_hw * f32(rstd)[:, None, None], of_y)
+            z = np.where(from_hw, hw / of_hw, y / of_y)
+        assert z.dtype == np.float32 and want_s.dtype == np.float32
+        assert np.array_equal(f32(s).T, want_s[:, :, 0])
+        assert np.array_equal(q.cpu().numpy(), e4m3.encode(z.astype(np.float64)).reshape(rows, cols))
