@@ -6,14 +6,15 @@
 // bytes, one scale group of 32 codes, of weight row l % 16, so that four lanes
 // read 64 neighbouring bytes of a row. v_cvt_scalef32_pk_bf16_fp4 turns two codes
 // into two bf16 with the scale applied, exactly (a code has two significant bits,
-// and bf16 the exponents of E8M0 with subnormals), and the products go through
-// the bf16 MFMA of 16 x 16 x 32: weights are its 16 rows, x its 16 columns, and
-// its 32 positions of K are 8 of each of the four lanes' groups; x is fetched in
-// the same order. Sums are fp32. fp32 activations are split into three bf16 terms
-// whose sum is x exactly (24 = 8 + 8 + 8 significant bits), each with an MFMA of
-// its own. fp16 ones meet weights decoded to fp16 where the scales of all lanes
-// allow that exactly, as those of a model's weights do (all but those of tiles of
-// zeros); else they are split into two bf16 terms (11 = 8 + 3 bits).
+// and bf16 the exponents of E8M0 with subnormals, but for products of 2^128 and
+// more, which become infinite), and the products go through the bf16 MFMA of
+// 16 x 16 x 32: weights are its 16 rows, x its 16 columns, and its 32 positions of
+// K are 8 of each of the four lanes' groups; x is fetched in the same order. Sums
+// are fp32. fp32 activations are split into three bf16 terms whose sum is x exactly
+// (24 = 8 + 8 + 8 significant bits) down to bf16's 2^-133, each with an MFMA of its
+// own. fp16 ones meet weights decoded to fp16 where the scales of all lanes allow
+// that exactly, as those of a model's weights do (all but those of tiles of zeros);
+// else they are split into two bf16 terms (11 = 8 + 3 bits).
 //
 // What bounds it: the weight's bytes, once enough loads are in flight; for 9 to 16
 // rows also x, whose chunk takes 32 registers a lane where a weight tile's takes

@@ -619,8 +619,8 @@ int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, in
  * is the FP8 Linear's operand, tokens to their experts' rows and back, and the
  * products of generated tokens with 4-bit weights. Types are fp8bq_dtype values;
  * 16- and 32-bit matrices need no alignment beyond their element's, and sums are
- * float32 in an order fixed by the arguments other than the data: the same
- * result at every call.
+ * float32 in an order that does not depend on what other work runs: the same
+ * result at every call with the same arguments and data.
  * ------------------------------------------------------------------------- */
 
 /*
@@ -733,8 +733,13 @@ int fp8bq_moe_combine_grad(const void* dout, int type, int64_t tokens, int64_t c
  * Product of a few rows with an MXFP4 weight, the rows kept as they are
  * (fp8bq_gemm_mxfp4 takes rows quantised to 4 bits):
  *   out[i][j] = sum_k x[i][k] * b_hat[j][k],
- * the weight's values exact, x exact in any of the three types, sums in float32,
- * rounded once to otype. For generated tokens: the weight's bytes are the cost.
+ * the weight's values exact (those of 2^128 and more, which scale bytes 253 and
+ * 254 can give, make the row's results not finite, zeros of x included), x exact in
+ * any of the three types (an fp32 x down to 2^-133, the smallest of BF16: bits
+ * below it are cut off), sums in float32, rounded once to otype. How the sums
+ * round depends on the sizes, and for fp16 rows also on whether fp16 holds the
+ * values of the neighbouring weight rows, those of tiles of zeros included.
+ * For generated tokens: the weight's bytes are the cost.
  * Any m is computed, in passes of 16 rows that read the weight again: of wide
  * weights the quantised product is faster from 17 rows on, where its accuracy
  * serves (32 rows of 18432 x 7168, us: 31.5, 21.7 with the rows' quantisation), of

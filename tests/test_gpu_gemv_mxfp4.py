@@ -216,3 +216,37 @@ def test_weights_past_4_gib():
     got = fb.grouped_gemv_mxfp4(off, x, w, ws)
     check_product(f64(got[1:, -64:]), f64(x)[1:], values, k, "bfloat16", "bfloat16")
     assert (got[0] == 0).all() and (got[1, :-64] == 0).all()
+
+
+def test_tiny_fp32_values_end_at_2_to_the_minus_133():
+    """Bits of an fp32 x below 2^-133, the smallest of bf16, are cut off; what is above them counts in full."""
+    import torch
+    k = 512
+    rng = np.random.default_rng(31)
+    x = np.ldexp(rng.uniform(1, 2, (16, k)) * rng.choice([-1, 1], (16, k)), rng.integers(-149, -100, (16, k))).astype(np.float32)
+    x[0, :6] = np.ldexp(np.float32([1, 1, 1.5, 1.9921875, -1, 1.0000001]), [-140, -133, -132, -127, -149, -126])
+    w, ws = mxfp4.quantise(np.eye(k) * 2.0 ** 100)
+    got = f64(fb.gemv_mxfp4(torch.from_numpy(x).cuda(), torch.from_numpy(w).cuda(), torch.from_numpy(ws).cuda()))
+    kept = np.trunc(np.ldexp(x.astype(np.float64), 133))
+    assert np.array_equal(got, np.ldexp(kept, -33)) and (got[0, :5] == np.ldexp([0, 1, 1.5, 1.984375, 0], [0, -33, -32, -27, 0])).all()
+
+
+@pytest.mark.parametrize("xtype", DTYPES)
+def test_codes_of_2_to_the_128_and_more_are_not_finite(xtype):
+    """The weight's values are exact below 2^128: scale bytes up to 252, and the smaller codes of 253 and 254."""
+    import torch
+    k, n = 256, 64
+    q = np.zeros((n, k // 2), np.uint8)
+    code = np.tile(np.arange(16, dtype=np.uint8), 4)
+    q[:, 0] = code                                                   # element 0; the others are zeros
+    byte = np.full((1, n, 8), 127, np.uint8)
+    byte[0, :, 0] = np.repeat([251, 252, 253, 254], 16)
+    vw = mxfp4.values(q, byte, k)[:, 0]
+    x = np.zeros((3, k))
+    x[:, 0] = [2.0 ** -10, -3.0 * 2.0 ** -10, 0.0]
+    got = f64(fb.gemv_mxfp4(torch.from_numpy(x).to(torch_dtype(xtype)).cuda(), torch.from_numpy(q).cuda(),
+                            torch.from_numpy(byte).cuda(), dtype=torch.float32))
+    big = np.abs(vw) >= 2.0 ** 128
+    assert big.sum() == 4 + 8 and not big[:32].any()
+    assert np.array_equal(got[:, ~big], np.outer(x[:, 0], vw[~big]))
+    assert not np.isfinite(got[:, big]).any()
