@@ -250,3 +250,38 @@ def test_codes_of_2_to_the_128_and_more_are_not_finite(xtype):
     assert big.sum() == 4 + 8 and not big[:32].any()
     assert np.array_equal(got[:, ~big], np.outer(x[:, 0], vw[~big]))
     assert not np.isfinite(got[:, big]).any()
+
+
+@pytest.mark.parametrize("xtype", DTYPES)
+def test_each_clamped_expert_has_its_rows(xtype):
+    """Offsets below zero and beyond the rows: one writer for every row, nothing behind them touched."""
+    import torch
+    w, ws, vw = experts(50, 4, 48, 600)
+    x = matrix(51, 30, 600, xtype)
+    buf = torch.full((36, 48), 7.0, dtype=x.dtype, device="cuda")
+    off = torch.tensor([-5, 4, 4, 13, 1 << 30], dtype=torch.int32, device="cuda")
+    got = f64(fb.grouped_gemv_mxfp4(off, x, w, ws, out=buf[2:32]))
+    for e, (lo, hi) in enumerate([(0, 4), (4, 4), (4, 13), (13, 30)]):
+        if lo < hi:
+            check_product(got[lo:hi], f64(x)[lo:hi], vw[e], 600, xtype, xtype)
+    assert (buf[:2] == 7).all() and (buf[32:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 300, 520), (12, 257, 1057), (20, 96, 64)])
+def test_gradient_through_the_column_form(m, n, k, dtype):
+    """dx of out = x w^T is the product of dout with the weight quantised along its columns."""
+    log(f"gemv gradient {m}x{n}x{k} {dtype}")
+    w = matrix(60, n, k, "float32", 0.05)
+    _, _, qt, st = fb.quant_mxfp4_1x32(w, rowwise=False, colwise=True)
+    values = mxfp4.values(qt.cpu().numpy(), st.cpu().numpy(), n)                # [k, n]
+    assert (np.abs(values - f64(w).T) <= np.kron(np.abs(np.pad(f64(w).T, ((0, 0), (0, -n % 32)))).reshape(k, -1, 32).max(2) / 4,
+                                                 np.ones((1, 32)))[:, :n]).all()
+    dout = matrix(61, m, n, dtype, 0.1)
+    check_product(f64(fb.gemv_mxfp4(dout, qt, st)), f64(dout), values, n, dtype, dtype)
+    if m > 1:
+        import torch
+        off = torch.tensor([0, 1, m], dtype=torch.int32, device="cuda")
+        got = f64(fb.grouped_gemv_mxfp4(off, dout, torch.stack((qt, qt.flip(0))), torch.stack((st, st.flip(1)))))
+        check_product(got[:1], f64(dout)[:1], values, n, dtype, dtype)
+        check_product(got[1:], f64(dout)[1:], values[::-1], n, dtype, dtype)

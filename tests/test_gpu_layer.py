@@ -254,3 +254,59 @@ def test_layer_without_rows(tokens, topk):
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
     out = torch.full((tokens, cols), 7.0, dtype=torch.bfloat16, device="cuda")
     assert torch.equal(fb.moe_combine(z, pos, out=out), torch.zeros_like(out))
+
+
+def test_training_step_within_its_roundings():
+    """The same chain, element by element: each step's roundings (those of its own test) carried through the steps behind it
+    to first order, 1% for the higher ones."""
+    import torch
+    tokens, cols, experts, topk = 60, 192, 5, 3
+    x, r, dout = (matrix(s, tokens, cols, "float32") for s in (211, 212, 213))
+    w = matrix(214, 1, cols, "float32", 0.2)[0].contiguous() + 1
+    idx, gate = router(215, tokens, experts, topk)
+    _, off, src, pos = fb.moe_plan(idx, experts, pad=32)
+    m = np.random.default_rng(216).normal(0, cols ** -0.5, (experts, cols, cols))
+    n_off, n_src, n_pos = (t.cpu().numpy() for t in (off, src, pos))
+    rows = len(n_src)
+
+    def experts_of(v, back=False, mat=m):
+        out = np.zeros_like(v)
+        for e in range(experts):
+            out[n_off[e]:n_off[e + 1]] = v[n_off[e]:n_off[e + 1]] @ (mat[e] if back else mat[e].T)
+        return out
+
+    def product(t, back=False):
+        return torch.from_numpy(experts_of(f64(t), back)).float().cuda()
+
+    _, _, y, h, rstd = fb.rmsnorm(x, w, residual=r, quant=False, norm=True)
+    z = product(fb.moe_dispatch(y, src, pos)[0])
+    out = fb.moe_combine(z, pos, gate, base=h)
+    dz, dgate = fb.moe_combine_grad(dout, z, pos, gate, src)
+    dz[off[-1]:] = 0                                                   # behind the last expert, not written
+    dy = fb.moe_combine(product(dz, True), pos)
+    dx, dw = fb.rmsnorm_grad(dy, h, w, rstd, dh=dout)
+
+    # the chain in float64, and beside every value what the fp32 one may be off by
+    RSTD = ROW / 2 + 4 * U
+    size = np.abs(m)
+    vw, vg, vd = f64(w), f64(gate), f64(dout)
+    wh, wr, wy = layer.rmsnorm(f64(x), f64(r), vw, 1e-6)
+    ey = (RSTD + 4 * U) * np.abs(wy)
+    to_rows = lambda v: layer.dispatch(v, n_pos, n_src, rows, 0.0)  # noqa: E731
+    wz = experts_of(to_rows(wy))
+    ez = experts_of(to_rows(ey), mat=size) + U * np.abs(wz)
+    wout, mag = layer.combine(wz, n_pos, vg, wh)
+    check("out", f64(out), wout, 1.01 * (layer.combine(ez, n_pos, vg, None)[0] + (topk + 1) * U * mag + 2 * U * np.abs(wh)))
+    wdz, wdg, mag = layer.combine_grad(vd, wz, n_pos, vg)
+    check("dgate", f64(dgate), wdg, 1.01 * (layer.combine_grad(np.abs(vd), ez, n_pos, vg)[1] + ROW * mag))
+    wrows = experts_of(wdz, True)
+    erows = experts_of(U * np.abs(wdz), True, size) + U * np.abs(wrows)
+    wdy, mag = layer.combine(wrows, n_pos, None, None)
+    edy = layer.combine(erows, n_pos, None, None)[0] + topk * U * mag
+    check("dy", f64(dy), wdy, 1.01 * edy)
+    wdx, wdw = layer.rmsnorm_grad(wdy, wh, vw, wr, vd)
+    hat, g, eg = np.abs(wh) * wr[:, None], np.abs(wdy * vw), edy * np.abs(vw)
+    whole = wr[:, None] * (g + hat * (g * hat).mean(1, keepdims=True))          # of dx's terms; each has rstd up to three times
+    edx = wr[:, None] * (eg + hat * (eg * hat).mean(1, keepdims=True)) + (3 * RSTD + 2 * U + ROW + 8 * U) * whole + 2 * U * np.abs(wdx)
+    check("dx", f64(dx), wdx, 1.01 * edx)
+    check("dw", f64(dw), wdw, 1.01 * ((edy * hat).sum(0) + (RSTD + U + (tokens + 600) * U) * np.abs(wdy * hat).sum(0)))
