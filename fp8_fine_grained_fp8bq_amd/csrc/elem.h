@@ -54,9 +54,12 @@ __device__ __forceinline__ V load_any(const void* p) {
   return v;
 }
 // Results that are written whole, as they go by: marked as not worth keeping in
-// the caches (rows of 8192 tokens dispatched to 64 experts: 115 -> 102 us, 4096 x
-// 7168 normalised: 49 -> 40). Loads so marked were slower by a fifth to a third wherever an
-// operand still was in a cache, and faster only far beyond their size.
+// the caches. Us without and with, called back to back: codes of 8192 tokens of 7168
+// columns dispatched to 64 experts 116 / 105; rows of 16384 x 7168 normalised, with
+// a residual and codes 193 / 189, the gradient 189 / 184; of 4096 x 7168 49 / 43 (53 /
+// 51 where no operand is in a cache), but with codes alone 36 / 38.6 (45 / 44). Loads
+// so marked were slower by a fifth to a third wherever an operand still was in a
+// cache, and faster only far beyond their size.
 template <class V>
 __device__ __forceinline__ void stream_store(void* p, const V& v) {
   if constexpr (sizeof(V) % 16 == 0) {

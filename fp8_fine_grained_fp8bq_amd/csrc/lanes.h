@@ -27,7 +27,7 @@ __device__ __forceinline__ float wave_reduce(float v, F&& f) {
 __device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, [](float a, float b) { return a + b; }); }
 __device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); }); }
 
-// The same over each aligned group of 16 lanes, and over LANES of them.
+// The same over each aligned group of 16 lanes.
 template <class F>
 __device__ __forceinline__ float row16_reduce(float v, F&& f) {
   v = f(v, dpp<0xB1>(v));

@@ -3,8 +3,8 @@
 // include/fp8bq.h. All of it is bound by memory, so each row is read and
 // written once: a wave takes a piece of a token's row and visits the token's
 // choices (`pos`) with it, instead of each dispatched row fetching its token.
-// 8192 tokens of 7168 columns, 8 of 64 experts each: codes out 102 us (5.6 TB/s),
-// 16-bit rows back 210, its gradient 412.
+// 8192 tokens of 7168 columns, 8 of 64 experts each, each operator called back to
+// back: codes out 105 us (5.2 TB/s), 16-bit rows back 218, its gradient 416.
 #include "../../include/fp8bq.h"
 #include "elem.h"
 #include "lanes.h"

@@ -342,8 +342,13 @@ void launch_dense(const GemvArgs& p, hipStream_t st) {
 // tiles, weights out of the caches: 16 rows of bf16, k = 4096, n = 8192 10.5 / 8.3 /
 // 9.6 / 11.9 / 12.3, n = 20480 20.5 / 17.7 / 16.1 / 19.7 / 13.6, n = 24576 24.3 /
 // 18.6 / 16.9 / 20.3 / 21.7; 4 rows of 18432 x 7168 18.8 / 18.5 / 17.6 / 21.6 / 15.7.
-// One and two rows differ by 3% where five tiles do best (15.8 / 15.6) and take
-// one. fp32 with more than 8 rows has registers for three.
+// From n = 12289 to 16384 it is four, 4% from five at most for bf16 (n = 13312 16.8 / 13.1 /
+// 15.8 / 12.5 / 12.9, k = 7168 24.9 / 18.9 / 22.1 / 17.7 / 18.1) and a tenth less for fp16
+// (25.7 / 20.1 / 24.2 / 18.8 / 20.9). One and two rows differ by 1% where five tiles do
+// best (15.8 / 15.6) and take one. fp32 with more than 8 rows has registers for three
+// (16 rows, k = 7168, one to three tiles: n = 2048 20.1 / 21.8 / 24.7, n = 7168 38 / 22 /
+// 25, n = 18432 91 / 61 / 48). Four tiles of bf16 for 16 rows and five of fp32 for 8
+// keep 16 bytes a lane in scratch memory.
 template <int T, int P>
 void launch_tiled(const GemvArgs& p, hipStream_t st) {
   constexpr int kMost = T == FP8BQ_FP32 && P == 8 ? 3 : 5;
@@ -374,7 +379,13 @@ void launch_grouped(const GemvArgs& p, hipStream_t st) {
 // waves) or x is fp32, for four where K gives each five chunks and there are
 // enough of them (32 tokens to 32 of 256 experts, 2048 x 7168: 54 us, 61 with two
 // waves; 16 rows to 16 experts at most 29, 23 with two tiles for two waves); and
-// two tiles for two waves (2048 x 3584: 27 us, 29 to 32 else).
+// two tiles for two waves (2048 x 3584: 27 us, 29 to 32 else). The bounds are coarse:
+// over 32 tokens to 32 of 256 experts, n from 1024 to 7168 and k from 2048 to 7168,
+// the rule's choice is the fastest of the four or within 9% of it (three tiles for
+// two waves already pay at 2560 to 3584 x 2048 or 3584, 29.0 for 31.5, and for four
+// at 4096 x 5120 or 7168, 66.7 for 71.5).
+// fp32, us, four waves / two: a token's 8 of 32 experts of 1024 x 2048 7.3 / 9.0, 2048 x
+// 2048 11.2 / 9.7, 2048 x 7168 21.8 / 20.8; 32 tokens to 32 of 256 89 / 73.
 template <int T>
 void launch_experts(const GemvArgs& p, hipStream_t st) {
   constexpr bool kFp32 = T == FP8BQ_FP32;

@@ -6,8 +6,10 @@
 // s = amax|y| / 448, q = E4M3(y / s). A row lives in the registers of its
 // lanes as fp32 from the load to the store, so the mean and the scales cost
 // no second read: 2 (4 with r) bytes read and 1 to 5 written per 16-bit element.
-// Bound by memory: 16384 x 7168 with codes and rows takes 184 us (5.8 TB/s),
-// 4096 x 7168 with codes 37.5, its gradient 49.6.
+// Bound by memory. Us, with a residual: 16384 x 7168 with codes and rows 184 to 189
+// (5.6 to 5.8 TB/s); 4096 x 7168 with codes 38.6 called back to back on the same
+// operands, which a cache then holds in part, 44 on others each time; its gradient,
+// dweight's sum included, 46.4 and 54.9.
 #include "../../include/fp8bq.h"
 #include "elem.h"
 #include "fp8_codec.h"
@@ -82,7 +84,8 @@ __device__ __forceinline__ void load_weights(const void* w, int wtype, const Col
 
 // A lane's elements of the row at p. Every lane loads, and what it has no column
 // for is set to zero after: loads under a lane's branch are waited for where the
-// branch ends, one after the other (4096 x 7168 back: 49.6 us, 70 to 84 then).
+// branch ends, one after the other (the gradient of 4096 x 7168, called back to
+// back: 70 to 84 us, 49.6 without the branches when they went).
 template <int T, int U>
 struct Row {
   Raw8<T> unit[kSome<U>];
@@ -338,8 +341,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* parts, in
 
 // How a row of `cols` columns is dealt: f(lanes, units, bound on the threads of
 // a workgroup, threads), the first three as constants. Up to 512 threads keep
-// 256 registers each, so that wide rows need no scratch memory up to 16384
-// columns.
+// 256 registers each, so that rows need no scratch memory up to 16384 columns
+// (24 bytes a lane for the fp32 gradient with dh above 8192). Up to 1024 threads
+// have 128, and wider rows keep 48 to 80 bytes there with a residual and 412 to
+// 544 in the gradient: us for bf16 with a residual and dh, 1792 rows of 16384
+// 46.3 and 55.2, 1778 of 16512 59.5 and 236, 896 of 32768 59.4 and 224.
 template <class F>
 void with_shape(int64_t cols, F&& f) {
   using std::integral_constant;
