@@ -372,3 +372,18 @@ def test_codes_bit_for_bit(cols, residual, dtype):
         assert z.dtype == np.float32 and want_s.dtype == np.float32
         assert np.array_equal(f32(s).T, want_s[:, :, 0])
         assert np.array_equal(q.cpu().numpy(), e4m3.encode(z.astype(np.float64)).reshape(rows, cols))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [5, 100, 333, 1057, 7168])
+def test_sum_over_x_itself(cols, dtype):
+    """h over x: what lanes without a column of their own load may be stored over by then."""
+    import torch
+    rows = 50
+    x, r, w = matrix(27, rows, cols, dtype), matrix(28, rows, cols, dtype), weight(18, cols, dtype)
+    want = fb.rmsnorm(x, w, 1e-6, residual=r, quant=False, norm=True)
+    h, y, rstd = x.clone(), torch.empty_like(want[2]), torch.empty(rows, device="cuda")
+    code = DTYPES.index(dtype)
+    fb.fp8bq_rmsnorm(h.data_ptr(), code, rows, cols, cols, r.data_ptr(), cols, w.data_ptr(), code, 1e-6, h.data_ptr(), cols,
+                     y.data_ptr(), cols, None, 0, None, 0, rstd.data_ptr(), 0, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(h, want[3]) and torch.equal(y, want[2]) and torch.equal(rstd, want[4])
