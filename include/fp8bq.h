@@ -648,7 +648,9 @@ int fp8bq_moe_balance_grad(const float* dloss, const void* logits, int ltype, in
  *           there or in that tile, and as 0 elsewhere (its rstd is 0).
  * rstd      NULL, or float [rows].
  * eps       finite, >= 0 (a row of zeros with eps = 0 is NaN). Sums of squares
- *           are float32: rows whose mean square passes 3e38 become 0.
+ *           are float32: rows whose mean square passes 3e38 become 0, and with
+ *           eps = 0 those below about 1e-19, whose squares are subnormal, lose
+ *           accuracy, down to an infinite rstd where the squares vanish.
  * flags     0 or FP8BQ_SCALE_POW2.
  * Errors: E_INVAL (null, sizes <= 0, ld too small, bad type, flags or eps, h
  *         without residual), E_SHAPE (cols % 128 with q, cols above 32768, too

@@ -387,3 +387,16 @@ def test_sum_over_x_itself(cols, dtype):
     fb.fp8bq_rmsnorm(h.data_ptr(), code, rows, cols, cols, r.data_ptr(), cols, w.data_ptr(), code, 1e-6, h.data_ptr(), cols,
                      y.data_ptr(), cols, None, 0, None, 0, rstd.data_ptr(), 0, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(h, want[3]) and torch.equal(y, want[2]) and torch.equal(rstd, want[4])
+
+
+def test_ends_of_the_sum_of_squares():
+    """Mean squares beyond float32 give zeros; squares that vanish an infinite rstd without eps, and nothing of note with it."""
+    import torch
+    x = torch.full((3, 256), 1e20, device="cuda")
+    x[1], x[2] = 1e-25, 1e-18
+    w = weight(19, 256, "float32")
+    q, s, y, _, rstd = fb.rmsnorm(x, w, 0.0, norm=True)
+    assert rstd[0] == 0 and (y[0] == 0).all() and (read_back(q, s)[0] == 0).all()
+    assert torch.isinf(rstd[1]) and torch.isinf(y[1]).all()
+    check("rstd", f64(rstd[2:]), np.array([1e18]), 1e18 * (RSTD + 256 * 2.0 ** -150 / 256e-36))
+    check_forward(x[1:], None, w, 1e-12, fb.rmsnorm(x[1:], w, 1e-12, norm=True), "float32")
